@@ -322,6 +322,139 @@ awq_status awq_quantize_pack_clipped(const void* W, int64_t N, int64_t K, const 
 awq_status awq_apply_inverse_scale(const void* A, int64_t rows, int64_t cols, const void* s,
                                    int32_t axis, void* out, uint32_t* flags, void* stream);
 
+/*
+ * ---------------------------------------------------------------- experts and adapters
+ * The linear with many packed weights (mixture of experts) or with a low-rank term per row
+ * (adapters). The rows of a batch are put in group order once; the linears read that order.
+ * Group ids, offsets and orders are device data that the host never sees: ids outside
+ * [0, groups) mean "no group", and offsets or orders with wrong contents give wrong results
+ * but no access outside the sizes passed. 1 <= groups <= AWQ_MAX_GROUPS everywhere.
+ */
+#define AWQ_MAX_GROUPS 512
+#define AWQ_MAX_TOP_K 64
+#define AWQ_MAX_LORA_RANK 256
+#define AWQ_LORA_SKINNY_MAX_M 64
+
+typedef enum awq_logits_type { AWQ_LOGITS_FP16 = 0, AWQ_LOGITS_FP32 = 1 } awq_logits_type;
+
+/*
+ * awq_group_rows -- the rows of a batch in group order (a stable counting sort).
+ *   ids      int32 [n]           group of each row (an adapter, an expert); outside
+ *                                [0, groups): none
+ *   offsets  int32 [groups + 1]  out: group e has positions [offsets[e], offsets[e + 1]);
+ *                                the rows without a group follow from offsets[groups] on
+ *   order    int32 [n]           out: the row at each position; within a group, and among
+ *                                the rows without one, rows keep their order
+ *   pos      int32 [n] or NULL   out: the position of each row (order's inverse)
+ *   workspace device scratch of awq_group_rows_workspace_size(n, groups) bytes, 16-byte
+ *            aligned (0 up to 8192 rows: may be NULL). 1 <= n < 2^30.
+ */
+size_t awq_group_rows_workspace_size(int64_t n, int32_t groups);
+awq_status awq_group_rows(const int32_t* ids, int64_t n, int32_t groups, int32_t* offsets,
+                          int32_t* order, int32_t* pos, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * awq_moe_route -- router of a mixture of experts: per token the top_k largest logits (ties
+ *   to the lowest expert), their softmax weights, and the T top_k (token, choice) pairs in
+ *   expert order (pair t top_k + j is choice j of token t; awq_group_rows on the ids).
+ *     renormalize = 1: w_j = exp(l_j - m) / sum over the chosen; 0: / sum over all experts
+ *   in fp32, m the token's largest logit. A logit of -inf is never chosen and weighs
+ *   nothing (a masked expert): a token with fewer than top_k others has id -1 and weight 0
+ *   in the rest of its choices, a padded token (all -inf) in all of them. NaN counts as
+ *   -inf and +inf as the largest finite value of the type; both raise NONFINITE_INPUT.
+ *   logits   fp16 or fp32 [T][ld] (type), experts in the first E columns; ld >= E, any
+ *            alignment of the type; T top_k < 2^30; 1 <= top_k <= min(E, AWQ_MAX_TOP_K)
+ *   weights  fp32 [T][top_k], ids int32 [T][top_k]: out, in falling order of the logits
+ *   offsets, order, pos (not NULL): as awq_group_rows, n = T top_k, groups = E
+ *   workspace device scratch of awq_moe_route_workspace_size(T, E) bytes, 16-byte aligned
+ *            (0 up to 64 tokens: may be NULL)
+ */
+size_t awq_moe_route_workspace_size(int64_t T, int32_t E);
+awq_status awq_moe_route(const void* logits, awq_logits_type type, int64_t T, int32_t E,
+                         int64_t ld, int32_t top_k, int32_t renormalize, float* weights,
+                         int32_t* ids, int32_t* offsets, int32_t* order, int32_t* pos,
+                         void* workspace, size_t workspace_bytes, uint32_t* flags, void* stream);
+
+/* Which kernel the grouped linear and the linear with adapters run. */
+typedef enum awq_grouped_kernel {
+  AWQ_GROUPED_AUTO = 0,   /* by rows per group (experts) or rows (adapters)              */
+  AWQ_GROUPED_SKINNY = 1, /* tiles of 32 rows, K split over the waves of a block
+                             (experts: n_rows <= 65536; adapters: M <= 64)              */
+  AWQ_GROUPED_GEMM64 = 2, /* MFMA GEMM on 64-row tiles                                   */
+  AWQ_GROUPED_GEMM = 3    /* MFMA GEMM on 256-row tiles (8-bit codes: 128)               */
+} awq_grouped_kernel;
+
+/*
+ * awq_linear_w4a16_grouped -- the packed linear of every group on its rows (the experts of
+ *   a mixture): Y[p] = x(p) deq(W_e)^T for offsets[e] <= p < offsets[e + 1].
+ *   X        fp16 [x_rows][K]; x(p) = X[p] if order is NULL (x_rows >= n_rows), else
+ *            X[order[p] / fan] (fan choices per token: fan x_rows >= n_rows)
+ *   offsets  int32 [groups + 1], order int32 [n_rows] or NULL: from awq_moe_route or
+ *            awq_group_rows; fan >= 1 (ignored without order)
+ *   qweight / scales / zeros: `groups` packed weights of [N][K], one after the other, each
+ *            as awq_quantize_pack writes it (packing the stacked [groups N][K] does)
+ *   Y        fp16 [n_rows][N] out, in group order; rows from offsets[groups] on are left
+ *            as they were
+ *   1 <= n_rows < 2^30; x_rows K < 2^35. Formats, flags and accuracy as awq_linear_w4a16.
+ *   _gated_silu: each weight is a gate|up pair (N even), Y fp16 [n_rows][N/2], as
+ *   awq_linear_w4a16_gated_silu.
+ */
+awq_status awq_linear_w4a16_grouped(const void* X, int64_t x_rows, const int32_t* offsets,
+                                    const int32_t* order, int64_t n_rows, int32_t fan,
+                                    int32_t groups, const uint32_t* qweight, const void* scales,
+                                    const uint8_t* zeros, int64_t N, int64_t K,
+                                    const awq_config* cfg, void* Y, uint32_t* flags,
+                                    awq_grouped_kernel kernel, void* stream);
+awq_status awq_linear_w4a16_grouped_gated_silu(const void* X, int64_t x_rows,
+                                               const int32_t* offsets, const int32_t* order,
+                                               int64_t n_rows, int32_t fan, int32_t groups,
+                                               const uint32_t* qweight, const void* scales,
+                                               const uint8_t* zeros, int64_t N, int64_t K,
+                                               const awq_config* cfg, void* Y, uint32_t* flags,
+                                               awq_grouped_kernel kernel, void* stream);
+
+/*
+ * awq_moe_combine -- expert outputs back to token order, weighted:
+ *     Y[t] = fp16(add[t] + sum_j weights[t][j] P[pos[t top_k + j]])
+ *   summed in fp32 in the order of j, rounded once. Pairs whose position is not below
+ *   offsets[groups] (no expert) add nothing; their rows of P are not read.
+ *   P fp16 [T top_k][N] (group order); weights fp32 [T][top_k], pos int32 [T top_k] and
+ *   offsets int32 [groups + 1] as awq_moe_route writes them; add fp16 [T][N] or NULL (a
+ *   shared expert, the residual); Y fp16 [T][N] out, may equal add.
+ *   1 <= T, 1 <= top_k <= AWQ_MAX_TOP_K, T top_k < 2^30, 1 <= N < 2^31, T N < 2^37.
+ */
+awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* pos,
+                           const int32_t* offsets, int32_t groups, int64_t T, int32_t top_k,
+                           int64_t N, const void* add, void* Y, void* stream);
+
+/*
+ * awq_linear_w4a16_lora -- the packed linear shared by all rows, plus each row's own
+ *   low-rank adapter (many requests in one batch):
+ *     Y[i] = X[i] deq(W)^T + lora_scale[a] (X[i] A_a^T) B_a^T,  a = ids[i]
+ *   rounded to fp16 once; rows with ids outside [0, adapters) take the linear alone.
+ *   X fp16 [M][K], packed weight and Y fp16 [M][N] as awq_linear_w4a16
+ *   A fp16 [adapters][rank][K], B fp16 [adapters][N][rank], lora_scale fp32 [adapters];
+ *   rank a multiple of 8 up to AWQ_MAX_LORA_RANK (smaller adapters padded with zero rows
+ *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; 1 <= M < 2^30, M K < 2^35
+ *   ids      int32 [M]
+ *   order    int32 [M] or NULL: a permutation of the rows that brings those of one adapter
+ *            together (awq_group_rows); it changes the speed of large mixed batches only
+ *   workspace device scratch of awq_linear_w4a16_lora_workspace_size(M, rank) bytes,
+ *            16-byte aligned (X A^T in fp32)
+ *   flags    NONFINITE_INPUT: an Inf or NaN in X, the group scales, A or B
+ *   X A^T is accumulated and kept in fp32; for the second product its rows are split into
+ *   fp16 hi + lo after scaling by a power of two (22 significant bits).
+ */
+size_t awq_linear_w4a16_lora_workspace_size(int64_t M, int32_t rank);
+awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweight,
+                                 const void* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                                 const awq_config* cfg, const void* A, const void* B,
+                                 const float* lora_scale, int32_t adapters, int32_t rank,
+                                 const int32_t* ids, const int32_t* order, void* Y,
+                                 void* workspace, size_t workspace_bytes, uint32_t* flags,
+                                 awq_grouped_kernel kernel, void* stream);
+
 /* Largest M served by a GEMV-class kernel under AWQ_LINEAR_AUTO with 4-bit codes (64, or
  * the value of the AWQ_GEMV_MAX_M environment variable clamped to 0..64, read at library
  * load). */

@@ -8,3 +8,7 @@ from .awq import (  # noqa: F401
     candidate_scales, clip_search, gemv_max_m, linear_w4a16, linear_w4a16_gated_silu, quantize_pack,
     search_scales,
 )
+from .grouped import (  # noqa: F401
+    LoraAdapters, PackedExperts, Routing, RowGroups, group_rows, linear_w4a16_grouped,
+    linear_w4a16_grouped_gated_silu, linear_w4a16_lora, moe_combine, moe_route, quantize_pack_experts,
+)

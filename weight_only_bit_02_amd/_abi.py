@@ -31,6 +31,7 @@ class AwqConfig(C.Structure):
 
 P = C.c_void_p
 I64 = C.c_int64
+I32 = C.c_int32
 CFG = C.POINTER(AwqConfig)
 
 # name -> (restype, argtypes); every name here is exported by the library
@@ -51,6 +52,19 @@ SIGNATURES = {
     "awq_linear_w4a16_gated_silu": (C.c_int, [P, I64, P, P, P, I64, I64, CFG, P, P, P]),
     "awq_linear_w4a16_gated_silu_ex": (C.c_int, [P, I64, P, P, P, I64, I64, CFG, P, P, C.c_int, P]),
     "awq_apply_inverse_scale": (C.c_int, [P, I64, I64, P, C.c_int32, P, P, P]),
+    # experts and adapters
+    "awq_group_rows_workspace_size": (C.c_size_t, [I64, I32]),
+    "awq_group_rows": (C.c_int, [P, I64, I32, P, P, P, P, C.c_size_t, P]),
+    "awq_moe_route_workspace_size": (C.c_size_t, [I64, I32]),
+    "awq_moe_route": (C.c_int, [P, C.c_int, I64, I32, I64, I32, I32, P, P, P, P, P, P, C.c_size_t, P, P]),
+    "awq_linear_w4a16_grouped": (C.c_int, [P, I64, P, P, I64, I32, I32, P, P, P, I64, I64, CFG, P, P,
+                                           C.c_int, P]),
+    "awq_linear_w4a16_grouped_gated_silu": (C.c_int, [P, I64, P, P, I64, I32, I32, P, P, P, I64, I64, CFG,
+                                                      P, P, C.c_int, P]),
+    "awq_moe_combine": (C.c_int, [P, P, P, P, I32, I64, I32, I64, P, P, P]),
+    "awq_linear_w4a16_lora_workspace_size": (C.c_size_t, [I64, I32]),
+    "awq_linear_w4a16_lora": (C.c_int, [P, I64, P, P, P, I64, I64, CFG, P, P, P, I32, I32, P, P, P, P,
+                                        C.c_size_t, P, C.c_int, P]),
     "awq_gemv_max_m": (C.c_int32, []),
     # calibration probes (include/awq_peaks.h)
     "awq_peak_read_stream": (C.c_int, [P, C.c_size_t, P, C.c_int32, P]),

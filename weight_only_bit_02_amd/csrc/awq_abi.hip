@@ -84,6 +84,21 @@ ClipLayout clip_layout(int64_t T, int64_t N, int64_t K, int n_shrink, int group)
   return L;
 }
 
+// Limits of the expert and adapter calls.
+constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and rows are kept in 32 bits
+constexpr int64_t kMaxElements = (int64_t)1 << 35;  // of X: 16-byte units are kept in 32 bits
+constexpr int64_t kSkinnyMaxRows = 65536;           // its grid: one row of blocks per row tile
+
+bool good_groups(int32_t g) { return g >= 1 && g <= AWQ_MAX_GROUPS; }
+bool good_rank(int32_t r) { return r >= 8 && r <= AWQ_MAX_LORA_RANK && r % 8 == 0; }
+bool good_workspace(const void* p, size_t have, size_t need) {
+  return need == 0 || (p && have >= need && aligned16(p));
+}
+// Every tiling's block count stays in 31 bits (the narrowest: 64 rows x 128 outputs).
+bool grouped_grid_ok(int64_t n, int64_t N, int64_t groups) {
+  return (n / 64 + groups + 1) < ((int64_t)1 << 30) / (N / 128 + 1);
+}
+
 // Largest M that AWQ_LINEAR_AUTO serves with a GEMV-class kernel (above it, the MFMA
 // GEMM); AWQ_GEMV_MAX_M overrides it (0 .. 64) to measure the crossover.
 int gemv_max_m_from_env() {
@@ -430,6 +445,206 @@ awq_status awq_apply_inverse_scale(const void* A, int64_t rows, int64_t cols, co
     return AWQ_ERR_MISALIGNED;
   return hip_status(awq::launch_inverse_scale((const uint16_t*)A, rows, cols, (const uint16_t*)s,
                                               axis, (uint16_t*)out, flags, (hipStream_t)stream));
+}
+
+size_t awq_group_rows_workspace_size(int64_t n, int32_t groups) {
+  if (n < 1 || n >= kMaxRows || !good_groups(groups)) return 0;
+  return align256(awq::group_rows_workspace(n, groups));
+}
+
+awq_status awq_group_rows(const int32_t* ids, int64_t n, int32_t groups, int32_t* offsets,
+                          int32_t* order, int32_t* pos, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  if (!ids || !offsets || !order) return AWQ_ERR_NULL_POINTER;
+  if (n < 1 || n >= kMaxRows || !good_groups(groups)) return AWQ_ERR_BAD_SHAPE;
+  if (!good_workspace(workspace, workspace_bytes, awq_group_rows_workspace_size(n, groups)))
+    return AWQ_ERR_WORKSPACE;
+  if (!aligned16(ids) || !aligned16(offsets) || !aligned16(order) || (pos && !aligned16(pos)))
+    return AWQ_ERR_MISALIGNED;
+  return hip_status(awq::launch_group_rows(ids, n, groups, offsets, order, pos, (int*)workspace,
+                                           (hipStream_t)stream));
+}
+
+size_t awq_moe_route_workspace_size(int64_t T, int32_t E) {
+  if (T < 1 || T >= kMaxRows || !good_groups(E)) return 0;
+  return align256(awq::moe_route_workspace(T, E));
+}
+
+awq_status awq_moe_route(const void* logits, awq_logits_type type, int64_t T, int32_t E,
+                         int64_t ld, int32_t top_k, int32_t renormalize, float* weights,
+                         int32_t* ids, int32_t* offsets, int32_t* order, int32_t* pos,
+                         void* workspace, size_t workspace_bytes, uint32_t* flags, void* stream) {
+  int tv = 0;  // any integer may arrive: read it as one
+  static_assert(sizeof(type) == sizeof(tv), "awq_logits_type is an int-sized enum");
+  memcpy(&tv, &type, sizeof tv);
+  if (!logits || !weights || !ids || !offsets || !order || !pos) return AWQ_ERR_NULL_POINTER;
+  if ((tv != AWQ_LOGITS_FP16 && tv != AWQ_LOGITS_FP32) || (renormalize != 0 && renormalize != 1))
+    return AWQ_ERR_UNSUPPORTED;
+  if (T < 1 || !good_groups(E) || ld < E || ld >= kMaxDim || top_k < 1 || top_k > E ||
+      top_k > AWQ_MAX_TOP_K || T >= kMaxRows / top_k)
+    return AWQ_ERR_BAD_SHAPE;
+  if (!good_workspace(workspace, workspace_bytes, awq_moe_route_workspace_size(T, E)))
+    return AWQ_ERR_WORKSPACE;
+  if (((uintptr_t)logits & (tv == AWQ_LOGITS_FP16 ? 1u : 3u)) != 0 || !aligned16(weights) ||
+      !aligned16(ids) || !aligned16(offsets) || !aligned16(order) || !aligned16(pos) ||
+      (flags && !aligned4(flags)))
+    return AWQ_ERR_MISALIGNED;
+  return hip_status(awq::launch_moe_route(logits, tv == AWQ_LOGITS_FP16, ld, T, E, top_k,
+                                          renormalize != 0, weights, ids, offsets, order, pos,
+                                          (int*)workspace, flags, (hipStream_t)stream));
+}
+
+static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* offsets,
+                                 const int32_t* order, int64_t n_rows, int32_t fan, int32_t groups,
+                                 const uint32_t* qweight, const void* scales, const uint8_t* zeros,
+                                 int64_t N, int64_t K, const awq_config* cfg, void* Y, uint32_t* flags,
+                                 awq_grouped_kernel kernel_arg, bool gated, void* stream) {
+  int kv = 0;
+  static_assert(sizeof(kernel_arg) == sizeof(kv), "awq_grouped_kernel is an int-sized enum");
+  memcpy(&kv, &kernel_arg, sizeof kv);
+  const awq_config c = resolve(cfg);
+  if (!X || !offsets || !qweight || !scales || !zeros || !Y) return AWQ_ERR_NULL_POINTER;
+  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM) return AWQ_ERR_UNSUPPORTED;
+  if (n_rows < 1 || n_rows >= kMaxRows || x_rows < 1 || x_rows >= kMaxRows || !good_nk(N, K) ||
+      !good_groups(groups) || (gated && N % 2 != 0))
+    return AWQ_ERR_BAD_SHAPE;
+  if (order ? fan < 1 || x_rows < (n_rows + fan - 1) / fan : x_rows < n_rows) return AWQ_ERR_BAD_SHAPE;
+  if (x_rows > kMaxElements / K || !grouped_grid_ok(n_rows, N, groups)) return AWQ_ERR_BAD_SHAPE;
+  if (kv == AWQ_GROUPED_SKINNY && n_rows > kSkinnyMaxRows) return AWQ_ERR_BAD_SHAPE;
+  if (!aligned16(X) || !aligned16(offsets) || (order && !aligned16(order)) || !aligned16(qweight) ||
+      !aligned16(scales) || !aligned16(zeros) || !aligned16(Y) || (flags && !aligned4(flags)))
+    return AWQ_ERR_MISALIGNED;
+  hipStream_t st = (hipStream_t)stream;
+  if (flags) {
+    const hipError_t e = awq::launch_nonfinite_scan((const uint16_t*)X, x_rows * K,
+                                                    (const uint16_t*)scales,
+                                                    groups * N * (K / c.group_size), flags, st);
+    if (e != hipSuccess) return AWQ_ERR_HIP;
+  }
+  awq::GroupedArgs g{};
+  g.X = (const uint16_t*)X;
+  g.offsets = offsets;
+  g.order = order;
+  g.qweight = qweight;
+  g.scales = (const uint16_t*)scales;
+  g.zeros = zeros;
+  g.Y = (uint16_t*)Y;
+  g.N = N;
+  g.K = K;
+  g.n = (int)n_rows;
+  g.fan = fan;
+  g.groups = groups;
+  g.group = c.group_size;
+  const int mode = gated ? awq::kGated : awq::kPlain;
+  if (kv == AWQ_GROUPED_AUTO) {
+    const int64_t mean = n_rows / groups;
+    kv = mean < awq::kSkinnyMeanRows && n_rows <= kSkinnyMaxRows ? AWQ_GROUPED_SKINNY
+         : mean < awq::kGemm64MeanRows                           ? AWQ_GROUPED_GEMM64
+                                                                 : AWQ_GROUPED_GEMM;
+  }
+  if (kv == AWQ_GROUPED_SKINNY) return hip_status(awq::launch_grouped_skinny(g, mode, c.w_bit, st));
+  return hip_status(awq::launch_grouped_gemm(g, mode, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
+}
+
+awq_status awq_linear_w4a16_grouped(const void* X, int64_t x_rows, const int32_t* offsets,
+                                    const int32_t* order, int64_t n_rows, int32_t fan,
+                                    int32_t groups, const uint32_t* qweight, const void* scales,
+                                    const uint8_t* zeros, int64_t N, int64_t K,
+                                    const awq_config* cfg, void* Y, uint32_t* flags,
+                                    awq_grouped_kernel kernel, void* stream) {
+  return grouped_common(X, x_rows, offsets, order, n_rows, fan, groups, qweight, scales, zeros, N, K,
+                        cfg, Y, flags, kernel, false, stream);
+}
+
+awq_status awq_linear_w4a16_grouped_gated_silu(const void* X, int64_t x_rows,
+                                               const int32_t* offsets, const int32_t* order,
+                                               int64_t n_rows, int32_t fan, int32_t groups,
+                                               const uint32_t* qweight, const void* scales,
+                                               const uint8_t* zeros, int64_t N, int64_t K,
+                                               const awq_config* cfg, void* Y, uint32_t* flags,
+                                               awq_grouped_kernel kernel, void* stream) {
+  return grouped_common(X, x_rows, offsets, order, n_rows, fan, groups, qweight, scales, zeros, N, K,
+                        cfg, Y, flags, kernel, true, stream);
+}
+
+awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* pos,
+                           const int32_t* offsets, int32_t groups, int64_t T, int32_t top_k,
+                           int64_t N, const void* add, void* Y, void* stream) {
+  if (!P || !weights || !pos || !offsets || !Y) return AWQ_ERR_NULL_POINTER;
+  if (!good_groups(groups) || T < 1 || top_k < 1 || top_k > AWQ_MAX_TOP_K || T >= kMaxRows / top_k ||
+      N < 1 || N >= kMaxDim || T > kMaxElements * 4 / N)
+    return AWQ_ERR_BAD_SHAPE;
+  if (!aligned16(P) || !aligned16(weights) || !aligned16(pos) || !aligned16(offsets) ||
+      (add && !aligned16(add)) || !aligned16(Y))
+    return AWQ_ERR_MISALIGNED;
+  return hip_status(awq::launch_combine((const uint16_t*)P, weights, pos, offsets + groups, T, top_k, N,
+                                        (const uint16_t*)add, (uint16_t*)Y, (hipStream_t)stream));
+}
+
+size_t awq_linear_w4a16_lora_workspace_size(int64_t M, int32_t rank) {
+  if (M < 1 || M >= kMaxRows || !good_rank(rank)) return 0;
+  return align256((size_t)M * rank * 4);
+}
+
+awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweight,
+                                 const void* scales, const uint8_t* zeros, int64_t N, int64_t K,
+                                 const awq_config* cfg, const void* A, const void* B,
+                                 const float* lora_scale, int32_t adapters, int32_t rank,
+                                 const int32_t* ids, const int32_t* order, void* Y,
+                                 void* workspace, size_t workspace_bytes, uint32_t* flags,
+                                 awq_grouped_kernel kernel_arg, void* stream) {
+  int kv = 0;
+  memcpy(&kv, &kernel_arg, sizeof kv);
+  const awq_config c = resolve(cfg);
+  if (!X || !qweight || !scales || !zeros || !A || !B || !lora_scale || !ids || !Y)
+    return AWQ_ERR_NULL_POINTER;
+  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM) return AWQ_ERR_UNSUPPORTED;
+  if (M < 1 || M >= kMaxRows || !good_nk(N, K) || !good_groups(adapters) || !good_rank(rank) ||
+      M > kMaxElements / K || !grouped_grid_ok(M, N, 1))
+    return AWQ_ERR_BAD_SHAPE;
+  if (kv == AWQ_GROUPED_SKINNY && M > AWQ_LORA_SKINNY_MAX_M) return AWQ_ERR_BAD_SHAPE;
+  if (!good_workspace(workspace, workspace_bytes, awq_linear_w4a16_lora_workspace_size(M, rank)))
+    return AWQ_ERR_WORKSPACE;
+  if (!aligned16(X) || !aligned16(qweight) || !aligned16(scales) || !aligned16(zeros) ||
+      !aligned16(A) || !aligned16(B) || !aligned16(lora_scale) || !aligned16(ids) ||
+      (order && !aligned16(order)) || !aligned16(Y) || (flags && !aligned4(flags)))
+    return AWQ_ERR_MISALIGNED;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (flags) {
+    e = awq::launch_nonfinite_scan((const uint16_t*)X, M * K, (const uint16_t*)scales,
+                                   N * (K / c.group_size), flags, st);
+    if (e == hipSuccess)
+      e = awq::launch_nonfinite_scan((const uint16_t*)A, (int64_t)adapters * rank * K, (const uint16_t*)B,
+                                     (int64_t)adapters * rank * N, flags, st);
+    if (e != hipSuccess) return AWQ_ERR_HIP;
+  }
+  e = awq::launch_lora_shrink((const uint16_t*)X, (int)M, K, (const uint16_t*)A, lora_scale, adapters,
+                              rank, ids, order, (float*)workspace, st);
+  if (e != hipSuccess) return AWQ_ERR_HIP;
+  awq::GroupedArgs g{};
+  g.X = (const uint16_t*)X;
+  g.order = order;
+  g.qweight = qweight;
+  g.scales = (const uint16_t*)scales;
+  g.zeros = zeros;
+  g.Y = (uint16_t*)Y;
+  g.ids = ids;
+  g.H = (const float*)workspace;
+  g.B = (const uint16_t*)B;
+  g.N = N;
+  g.K = K;
+  g.n = (int)M;
+  g.fan = 1;
+  g.groups = adapters;
+  g.group = c.group_size;
+  g.rank = rank;
+  if (kv == AWQ_GROUPED_AUTO)
+    kv = M <= AWQ_LORA_SKINNY_MAX_M          ? AWQ_GROUPED_SKINNY
+         : M < awq::kLoraGemmMinM            ? AWQ_GROUPED_GEMM64
+                                             : AWQ_GROUPED_GEMM;
+  if (kv == AWQ_GROUPED_SKINNY) return hip_status(awq::launch_grouped_skinny(g, awq::kLora, c.w_bit, st));
+  return hip_status(awq::launch_grouped_gemm(g, awq::kLora, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
 }
 
 }  // extern "C"

@@ -1,0 +1,14 @@
+// 4-bit instantiations of the ragged-row GEMM (kLora), in a file of their own so that the
+// build compiles the variants in parallel.
+#include "grouped_gemm.hpp"
+
+namespace awq {
+
+void launch_grouped4_lora(const GroupedArgs& g, bool big, dim3 grid, hipStream_t stream) {
+  if (big)
+    hipLaunchKernelGGL((k_grouped<kLora, 8, 4>), grid, dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL((k_grouped<kLora, 2, 4>), grid, dim3(256), 0, stream, g);
+}
+
+}  // namespace awq

@@ -129,4 +129,53 @@ hipError_t launch_gemv_mfma(const uint16_t* X, int64_t M, const uint32_t* qweigh
 constexpr int kGemvMaxM = 8;       // the vector-ALU GEMV serves M <= 8 when asked for
 constexpr int kVgemvAutoMaxM = 3;  // and is the automatic choice up to M = 3
 
+// ---------------------------------------------------------------- experts and adapters
+// Router and grouping (route.hip). counts: workspace of the size the query returns (0: the
+// call runs in one block and needs none).
+size_t group_rows_workspace(int64_t n, int groups);
+hipError_t launch_group_rows(const int32_t* ids, int64_t n, int groups, int32_t* offsets,
+                             int32_t* order, int32_t* pos, int* counts, hipStream_t stream);
+size_t moe_route_workspace(int64_t T, int E);
+hipError_t launch_moe_route(const void* logits, bool half, int64_t ld, int64_t T, int E, int top_k,
+                            bool renorm, float* weights, int32_t* ids, int32_t* offsets, int32_t* order,
+                            int32_t* pos, int* counts, uint32_t* flags, hipStream_t stream);
+
+// Y[t] = fp16(add[t] + sum_j w[t][j] P[pos[t][j]]), pairs with pos >= *valid left out.
+hipError_t launch_combine(const uint16_t* P, const float* weights, const int32_t* pos,
+                          const int32_t* valid, int64_t T, int top_k, int64_t N, const uint16_t* add,
+                          uint16_t* Y, hipStream_t stream);
+
+// Operands of the ragged-row linears. Experts: rows [offsets[e], offsets[e + 1]) take weight
+// e (weights stacked; `groups` of them), from X row p or order[p] / fan. Adapters: all n rows
+// (through order, if any) take the one weight, and row i adds H[i] B[ids[i]]^T.
+struct GroupedArgs {
+  const uint16_t* X;
+  const int32_t *offsets, *order;
+  const uint32_t* qweight;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  uint16_t* Y;
+  const int32_t* ids;   // adapters: per row, outside [0, groups) none
+  const float* H;       // adapters: [n][rank], scale X A^T
+  const uint16_t* B;    // adapters: [groups][N][rank]
+  int64_t N, K;
+  int n, fan, groups, group, nt, rank;
+};
+enum GroupedMode { kPlain = 0, kGated = 1, kLora = 2 };
+
+// The GEMM tiles (big: 256 rows, 128 with 8-bit codes; else 64) and the kernel that splits
+// K over the waves of a block, for few rows per group (grouped_skinny.hip).
+hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, bool big, hipStream_t stream);
+hipError_t launch_grouped_skinny(GroupedArgs g, int mode, int w_bit, hipStream_t stream);
+
+// AWQ_GROUPED_AUTO: by the mean rows per group (experts) or the rows (adapters).
+constexpr int64_t kSkinnyMeanRows = 16;
+constexpr int64_t kGemm64MeanRows = 96;
+constexpr int64_t kLoraGemmMinM = 512;
+
+// Adapters: H[i] = scale[a] X[i] A_a^T (fp32), a = ids[i]; rows without an adapter are left.
+hipError_t launch_lora_shrink(const uint16_t* X, int n, int64_t K, const uint16_t* A, const float* scale,
+                              int adapters, int rank, const int32_t* ids, const int32_t* order, float* H,
+                              hipStream_t stream);
+
 }  // namespace awq
