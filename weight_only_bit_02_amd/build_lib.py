@@ -21,12 +21,15 @@ LIB = os.path.join(LIB_DIR, "libawq_mi355x.so")
 SOURCES = [  # the slowest units (GEMM instantiations, the searches) first: they bound the build
     "grouped_i3_plain.hip", "grouped_i3_gated.hip", "grouped_i3_lora.hip", "grouped_i4_plain.hip",
     "grouped_i4_gated.hip", "grouped_i4_lora.hip", "grouped_i8_plain.hip", "grouped_i8_gated.hip",
-    "grouped_i8_lora.hip", "grouped_skinny.hip",
+    "grouped_i8_lora.hip",
+    "stream_i3_plain.hip", "stream_i3_gated.hip", "stream_i3_lora.hip", "stream_i4_plain.hip",
+    "stream_i4_gated.hip", "stream_i4_lora.hip", "stream_i8_plain.hip", "stream_i8_gated.hip",
+    "stream_i8_lora.hip",
     "gemm_i3_plain.hip", "gemm_i3_gated.hip", "gemm_i3_plain_g32.hip", "gemm_i3_gated_g32.hip",
     "gemm_i8_plain.hip", "gemm_i8_gated.hip", "gemm_i4_plain.hip", "gemm_i4_gated.hip",
     "gemm_i4_plain_g32.hip", "gemm_i4_gated_g32.hip", "search.hip", "gemm_wide.hip", "gemv.hip", "gemv_mfma.hip",
-    "gemv8.hip", "gemv3.hip", "quant_pack.hip", "stats.hip", "fold.hip", "check.hip", "peaks.hip", "gemm.hip", "grouped_gemm.hip",
-    "lora.hip", "route.hip", "combine.hip", "awq_abi.hip"]
+    "gemv8.hip", "gemv3.hip", "quant_pack.hip", "stats.hip", "fold.hip", "check.hip", "peaks.hip", "gemm.hip",
+    "grouped_gemm.hip", "grouped_stream.hip", "lora.hip", "route.hip", "combine.hip", "awq_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -542,7 +542,12 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
          : mean < awq::kGemm64MeanRows                           ? AWQ_GROUPED_GEMM64
                                                                  : AWQ_GROUPED_GEMM;
   }
-  if (kv == AWQ_GROUPED_SKINNY) return hip_status(awq::launch_grouped_skinny(g, mode, c.w_bit, st));
+  if (kv == AWQ_GROUPED_SKINNY && !awq::grouped_stream_supported(groups, N, K, c.group_size, c.w_bit))
+    kv = AWQ_GROUPED_GEMM64;
+  if (kv == AWQ_GROUPED_SKINNY) {
+    const int64_t mean = n_rows / groups;
+    return hip_status(awq::launch_grouped_stream(g, mode, c.w_bit, mean <= 6 ? 1 : 2, st));
+  }
   return hip_status(awq::launch_grouped_gemm(g, mode, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
 }
 
@@ -583,7 +588,7 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
 
 size_t awq_linear_w4a16_lora_workspace_size(int64_t M, int32_t rank) {
   if (M < 1 || M >= kMaxRows || !good_rank(rank)) return 0;
-  return align256((size_t)M * rank * 4);
+  return align256((size_t)M * ((rank + awq::kLoraBlock - 1) / awq::kLoraBlock) * sizeof(awq::LoraRow));
 }
 
 awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweight,
@@ -620,7 +625,7 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
     if (e != hipSuccess) return AWQ_ERR_HIP;
   }
   e = awq::launch_lora_shrink((const uint16_t*)X, (int)M, K, (const uint16_t*)A, lora_scale, adapters,
-                              rank, ids, order, (float*)workspace, st);
+                              rank, ids, order, (awq::LoraRow*)workspace, st);
   if (e != hipSuccess) return AWQ_ERR_HIP;
   awq::GroupedArgs g{};
   g.X = (const uint16_t*)X;
@@ -630,7 +635,7 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
   g.zeros = zeros;
   g.Y = (uint16_t*)Y;
   g.ids = ids;
-  g.H = (const float*)workspace;
+  g.H = (const awq::LoraRow*)workspace;
   g.B = (const uint16_t*)B;
   g.N = N;
   g.K = K;
@@ -643,7 +648,10 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
     kv = M <= AWQ_LORA_SKINNY_MAX_M          ? AWQ_GROUPED_SKINNY
          : M < awq::kLoraGemmMinM            ? AWQ_GROUPED_GEMM64
                                              : AWQ_GROUPED_GEMM;
-  if (kv == AWQ_GROUPED_SKINNY) return hip_status(awq::launch_grouped_skinny(g, awq::kLora, c.w_bit, st));
+  if (kv == AWQ_GROUPED_SKINNY && !awq::grouped_stream_supported(1, N, K, c.group_size, c.w_bit))
+    kv = AWQ_GROUPED_GEMM64;
+  if (kv == AWQ_GROUPED_SKINNY)
+    return hip_status(awq::launch_grouped_stream(g, awq::kLora, c.w_bit, M <= 16 ? 1 : 2, st));
   return hip_status(awq::launch_grouped_gemm(g, awq::kLora, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
 }
 

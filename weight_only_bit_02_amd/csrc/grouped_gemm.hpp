@@ -23,9 +23,8 @@
 //
 // Adapters (MODE kLora): the rows of one batch, optionally through `order` (then Y is
 // scattered back through it). Before the K loop each 32-row tile starts, for every adapter
-// among its rows, from H B_a^T (H = scale X A_a^T, fp32, from the shrink kernel), rows of other
-// adapters masked. H enters the matrix cores as fp16 hi + lo after scaling each row by a
-// power of two, so 22 bits of it count.
+// among its rows, from H B_a^T (H = scale X A_a^T from the first product's kernel, as fp16 hi
+// + lo under a power of two), rows of other adapters masked.
 #pragma once
 
 #include <type_traits>
@@ -145,17 +144,8 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
     const int r = r0 + m32;
     const int src = source(row0 + (r < rows ? r : rows - 1));
     const int id = r < rows ? g.ids[src] : -1;
-    const float* const h = g.H + (int64_t)src * g.rank;
-    // the row's power of two: its largest |h| goes to [1, 2)
-    float mx = 0.0f;
-    for (int k = kh * 8; k < g.rank; k += 16)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, __builtin_fabsf(h[k + j]));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const uint32_t ex = __builtin_bit_cast(uint32_t, mx) >> 23;
-    const bool fit = ex >= 1 && ex < 253;  // zero, tiny or not finite: as it is
-    const float up = fit ? __builtin_bit_cast(float, (254u - ex) << 23) : 1.0f;
-    const float down = fit ? __builtin_bit_cast(float, ex << 23) : 1.0f;
+    const int blocks = (g.rank + kLoraBlock - 1) / kLoraBlock;
+    const LoraRow* const h = g.H + (int64_t)src * blocks;
     uint64_t rest = __ballot((unsigned)id < (unsigned)g.groups);
     while (rest) {  // one adapter after the other, by its first row
       const int ad = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)rest) - 1);
@@ -163,36 +153,32 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
       const uint64_t rows_of = __ballot(mine);
       rest &= ~rows_of;
       const uint16_t* const B = g.B + (int64_t)ad * N * g.rank;
-      f32x16w d[2] = {f32x16w{}, f32x16w{}};
-      for (int k = 0; k < g.rank; k += 16) {
-        half8w hi{}, lo{}, bw[2] = {half8w{}, half8w{}};
-        if (k + kh * 8 < g.rank) {
+      for (int k = 0; k < blocks; ++k) {
+        f32x16w d[2] = {f32x16w{}, f32x16w{}};
+        const float f = h[k].f;
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            bw[b] = *reinterpret_cast<const half8w*>(B + bcol[b] * g.rank + k + kh * 8);
-          if (mine) {
+        for (int s = 0; s < 2; ++s) {
+          const int at = s * 16 + kh * 8;
+          const half8w hi = mine ? *reinterpret_cast<const half8w*>(h[k].hi + at) : half8w{};
+          const half8w lo = mine ? *reinterpret_cast<const half8w*>(h[k].lo + at) : half8w{};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float v = h[k + kh * 8 + j] * up;
-              hi[j] = (_Float16)v;
-              lo[j] = (_Float16)(v - (float)hi[j]);
-            }
+          for (int b = 0; b < 2; ++b) {
+            const half8w bw = k * kLoraBlock + at < g.rank
+                                  ? *reinterpret_cast<const half8w*>(B + bcol[b] * g.rank + k * kLoraBlock + at)
+                                  : half8w{};
+            d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, bw, d[b], 0, 0, 0);
+            d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, bw, d[b], 0, 0, 0);
           }
         }
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, bw[b], d[b], 0, 0, 0);
-          d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, bw[b], d[b], 0, 0, 0);
+        for (int i = 0; i < 16; ++i) {
+          // only the adapter's own rows: an Inf or NaN of its B stays out of the others
+          const int ri = 8 * (i >> 2) + 4 * kh + (i & 3);
+          const float fr = __shfl(f, ri);
+          const bool on = (rows_of >> ri) & 1;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) acc[b][i] = on ? __builtin_fmaf(fr, d[b][i], acc[b][i]) : acc[b][i];
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        // only the adapter's own rows: an Inf or NaN of its B stays out of the others
-        const int ri = 8 * (i >> 2) + 4 * kh + (i & 3);
-        const float f = __shfl(down, ri);
-        const bool on = (rows_of >> ri) & 1;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) acc[b][i] = on ? f * d[b][i] : acc[b][i];
       }
     }
   };

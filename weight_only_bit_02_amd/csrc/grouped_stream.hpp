@@ -1,0 +1,655 @@
+// Ragged-row linear for few rows per group (decoding): the products of grouped_gemm.hpp on
+// tiles of 16 MT rows. Decoding streams every active weight once and multiplies it with a
+// handful of rows, so the design is about bytes in flight, cache-line requests per byte and
+// instructions per byte.
+//
+//   - A work item is one row tile x 16 R weight rows over all of K, split over the S waves of a
+//     block, which meet in LDS in a fixed order. Blocks are persistent: the launch fills the
+//     chip once, each block takes a contiguous run of the items there are (counted on the
+//     device from the offsets).
+//   - A wave owns L K steps (128 channels each) of every item, so its part of X stays in
+//     registers for as long as the tile does: nothing but codes, scales and zeros is loaded per
+//     item. (K beyond S L steps is walked in parts, which reload X.)
+//   - Codes go global -> LDS by 16-byte DMA, eight neighbouring lanes on 128 contiguous bytes of
+//     a weight row, a whole cache line per request: the matrix cores want neighbouring lanes on
+//     neighbouring rows, and loading in that order straight into registers costs an L1 access
+//     per lane (12.1 M instead of 4.3 M for 64 experts x 4096 x 1024 on 384 rows), loading 64
+//     bytes per row twice the requests in flight for the same bytes. The buffers belong to one
+//     wave, so there is no barrier: a buffer is refilled as soon as its codes are in registers,
+//     and a wave keeps 16 KB in flight. Pieces are stored so that the reads have no bank
+//     conflicts. The waits are written out (take_codes, meet): left to itself the compiler
+//     drains every load in flight before each read, barrier and loop end.
+//   - v_mfma_f32_16x16x32_f16: lane l works on weight row l % 16 and on the 32 channels
+//     [32 kg, 32 kg + 32), kg = l / 16, of a step: 16 bytes of 4-bit codes per weight row,
+//     widened 8 channels at a time to exact q - z.
+//   - Scales and zeros of the L steps are loaded one weight row per lane, all steps at once
+//     (2 bytes per group would ask for a cache line each), and handed to the lanes that need
+//     them by ds_bpermute. Their addresses have the alignment of their type only.
+//   - 128-channel groups: the codes enter the matrix cores as they are widened, with the bias of
+//     their exponent (bias_of), the partial tile of a step starts from -sum(bias x) - z sum(x)
+//     (both from products with constants when X is loaded), and the scale multiplies it in fp32.
+//     The fp32 partial sums are then up to 1024 |sum(x)| instead of |sum((q - z) x)|: an error
+//     of 2^-24 1024 |sum(x)| per step, some 1e-5 of the step's sum |x (q - z)| at most.
+//     Smaller groups: a lane's channels lie in one group but the lanes of a slice do not, so
+//     the operand carries the scale ((q - z) sc, rounded to fp16 once).
+//   - A chunk that would pass the last weight row starts earlier instead and computes some
+//     columns twice, to the same values.
+//
+// Gated: tiles 0 .. R / 2 - 1 are gate rows, the rest their up rows, so a lane's sums hold
+// both and the epilogue needs no exchange. Adapters: as in grouped_gemm.hpp; the waves share
+// the adapters among a tile's rows.
+#pragma once
+
+#include "common.hpp"
+#include "groups.hpp"
+#include "launch.hpp"
+#include "widen.hpp"
+
+namespace awq {
+
+typedef float f32x4w __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+#define AWQ_INLINE __attribute__((always_inline))
+
+constexpr int kStreamWaves = 8;     // S at most
+constexpr int kStreamSlots = 2048;  // resident waves: two per SIMD
+
+// Columns of an item: 8-bit codes take twice the LDS, two row tiles twice the registers.
+constexpr int stream_cols(int w_bit, int row_tiles) { return w_bit == 8 || row_tiles > 1 ? 32 : 64; }
+constexpr int stream_steps(int row_tiles) { return row_tiles == 1 ? 4 : 2; }
+
+// Descriptor of the memory from p on (uniform): raw, offsets up to 2^32.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+}
+
+// 16 bytes per lane from offset `lane_at` + `at` of b to consecutive slots from lds on. (The
+// global_load_lds form counts as a flat access, after which the compiler waits for everything.)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t b, uint4* lds, uint32_t lane_at, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the 16-byte form
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, lane_at, at, 0, 0);
+#endif
+}
+
+// Eight bytes at byte `at` of [p, p + bytes), bytes >= 8, at any alignment; those past the end
+// are not read: the load moves back, and the value is shifted when it is used (shifting it here
+// would wait for the load).
+struct Eight {
+  uint64_t v;
+  uint32_t shift;
+  __device__ __forceinline__ uint64_t value() const { return v >> (shift & 63); }
+};
+__device__ __forceinline__ Eight load8(const void* p, int64_t at, int64_t bytes) {
+  const int64_t from = at < bytes - 8 ? at : bytes - 8;
+  Eight e;
+  __builtin_memcpy(&e.v, (const char*)p + from, 8);
+  e.shift = (uint32_t)(8 * (at - from));
+  return e;
+}
+
+// A zero point as the subtrahends of widened codes: -(1024 + z) twice, and -(64 + z) twice.
+struct ZeroPair {
+  half2w z1024, z64;
+};
+__device__ __forceinline__ ZeroPair zero_pair(uint32_t z) {
+  const uint32_t a = 0xE400u + z, b = 0xD400u + (z << 4);  // negative fp16
+  return ZeroPair{__builtin_bit_cast(half2w, a | (a << 16)), __builtin_bit_cast(half2w, b | (b << 16))};
+}
+
+// Codes of 8 channels (slice s of a lane's 32) as exact q - z.
+template <int BITS>
+__device__ __forceinline__ half8w centered(const uint32_t (&w)[BITS], int s, const ZeroPair& z,
+                                           uint32_t magic) {
+  half2w d[4];
+  if constexpr (BITS == 4) {
+    const uint32_t w0 = w[s], w8 = w[s] >> 8;
+    d[0] = __builtin_bit_cast(half2w, (w0 & 0x000F000Fu) | magic) + z.z1024;
+    d[1] = __builtin_bit_cast(half2w, (w0 & 0x00F000F0u) | 0x54005400u) + z.z64;
+    d[2] = __builtin_bit_cast(half2w, (w8 & 0x000F000Fu) | magic) + z.z1024;
+    d[3] = __builtin_bit_cast(half2w, (w8 & 0x00F000F0u) | 0x54005400u) + z.z64;
+  } else if constexpr (BITS == 8) {
+    const uint32_t m8 = 0x64646464u;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      d[p] = __builtin_bit_cast(half2w, __builtin_amdgcn_perm(m8, w[2 * s + (p >> 1)], p & 1 ? 0x04030402u : 0x04010400u)) + z.z1024;
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      d[p] = __builtin_bit_cast(half2w, widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic)) + z.z1024;
+  }
+  return half8w{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
+}
+
+// The same as bias + q, bias_of<BITS>() by pair: one shift per word of 4-bit codes and one
+// v_and_or_b32 (v_perm_b32) per pair of channels.
+template <int BITS>
+__device__ __forceinline__ half8w biased(const uint32_t (&w)[BITS], int s, uint32_t magic) {
+  uint32_t d[4];
+  if constexpr (BITS == 4) {
+    const uint32_t w0 = w[s], w8 = w[s] >> 8;
+    d[0] = (w0 & 0x000F000Fu) | magic;
+    d[1] = (w0 & 0x00F000F0u) | 0x54005400u;
+    d[2] = (w8 & 0x000F000Fu) | magic;
+    d[3] = (w8 & 0x00F000F0u) | 0x54005400u;
+  } else if constexpr (BITS == 8) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      d[p] = __builtin_amdgcn_perm(0x64646464u, w[2 * s + (p >> 1)], p & 1 ? 0x04030402u : 0x04010400u);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) d[p] = widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic);
+  }
+  return __builtin_bit_cast(half8w, uint4{d[0], d[1], d[2], d[3]});
+}
+template <int BITS>
+__device__ __forceinline__ half8w bias_of() {
+  const _Float16 a = 1024, b = BITS == 4 ? 64 : 1024;
+  return half8w{a, a, b, b, a, a, b, b};
+}
+
+// A position of the walk: an item (row tile x column chunk) and a part of K. Uniform.
+struct StreamItem {
+  int tile, chunk, part, row0, rows;
+};
+
+// G128: 128-channel groups (else 64 or 32).
+template <int MODE, int BITS, bool G128, int MT, int R, int L, int S>
+__global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2)))
+    k_stream(GroupedArgs g) {
+  constexpr int BM = 16 * MT, kCols = MODE == kGated ? 8 * R : 16 * R;
+  constexpr int H = BITS == 8 ? 1 : 2;        // steps of a buffer: 128 bytes of a row (3-bit: 96)
+  constexpr int NB = 4 / H, PU = 4 / L;       // buffers; positions that they hold together
+  constexpr int P = BITS * H;                 // 16-byte pieces of a row in a buffer
+  constexpr int kBuf = R * 2 * 64;            // slots of a wave's buffer: two DMA instructions a tile
+  __shared__ __attribute__((aligned(16))) uint4 st0[S][kBuf];
+  __shared__ __attribute__((aligned(16))) uint4 st1[S][kBuf];
+  __shared__ __attribute__((aligned(16))) uint4 st2[NB > 2 ? S : 1][NB > 2 ? kBuf : 1];
+  __shared__ __attribute__((aligned(16))) uint4 st3[NB > 2 ? S : 1][NB > 2 ? kBuf : 1];
+  __shared__ __attribute__((aligned(16))) f32x4w red[S * R * 64];
+  static_assert(L == 2 || L == 4, "steps of a wave");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, kg = lane >> 4;
+  const int64_t N = g.N, K = g.K, nh = N / 2;
+  const int outs = (int)(MODE == kGated ? nh : N);
+  const int nsteps = (int)(K / kGroup), nt = g.nt, parts = (nsteps + S * L - 1) / (S * L);
+  const int gsh = G128 ? 2 : g.group == 64 ? 1 : 0, per = 4 >> gsh;  // groups of a step: 1, 2, 4
+  const int64_t Gs = K / g.group, zbw = BITS == 8 ? Gs : (Gs + 1) / 2, words = K * BITS / 32;
+  const int64_t sbytes = (MODE == kLora ? 1 : g.groups) * N * Gs * 2;
+  const int64_t zbytes = (MODE == kLora ? 1 : g.groups) * N * zbw;
+  const uint32_t magic = wide_magic();
+
+  // ---- this block's run of items (item = tile * nt + column chunk)
+  const int mt = MODE == kLora ? (g.n + BM - 1) / BM
+                               : __builtin_amdgcn_readfirstlane(count_tiles<BM>(g.offsets, g.groups, g.n, lane));
+  const int64_t items = (int64_t)mt * nt;
+  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  if (i0 >= i1) return;  // uniform over the block
+  int left = (int)(i1 - i0) * parts;  // positions still to be loaded
+
+  // ---- addresses: a lane's offsets in the weight rows, and the rest uniform
+  const uint32_t rowq = (uint32_t)(words * 4);
+  auto weight_row = [&](int c) AWQ_INLINE -> uint32_t {  // of column c of a chunk, less the first's
+    int o = MODE == kGated ? c % (8 * R) : c;
+    o = o < outs ? o : outs - 1;
+    return (uint32_t)o + (MODE == kGated && c >= 8 * R ? (uint32_t)nh : 0u);
+  };
+  // DMA slot of a weight tile's buffer: piece (slot % P) ^ swizzle of row slot / P (3-bit: not
+  // swizzled; slots past the last row repeat it)
+  uint32_t vq[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int slot = d * 64 + lane, row = slot / P < 16 ? slot / P : 15;
+      const int piece = BITS == 3 ? slot % P : (slot & 7) ^ (row >> 1);
+      vq[r][d] = weight_row(r * 16 + row) * rowq + piece * 16;
+    }
+  const uint32_t my_row = weight_row(lane % (16 * R));  // scales and zeros: one weight row per lane
+  __amdgpu_buffer_rsrc_t codes;
+  int64_t expert_row = 0;  // first weight row of the loads' expert
+  auto first = [&](int chunk) AWQ_INLINE -> int {  // first output column of a chunk
+    const int c = chunk * kCols, last = outs > kCols ? outs - kCols : 0;
+    return c < last ? c : last;
+  };
+  auto source = [&](int p) AWQ_INLINE -> int {  // the row that order names (out of range: row 0)
+    if (!g.order) return p;
+    const int o = g.order[p];
+    return (unsigned)o < (unsigned)g.n ? o : 0;
+  };
+  auto step_of = [&](int part, int j) AWQ_INLINE -> int { return (part * S + wave) * L + j; };
+
+  StreamItem ld{(int)(i0 / nt), (int)(i0 % nt), 0, 0, 0};  // the position being loaded
+  auto open_tile = [&]() AWQ_INLINE {
+    const RowTile rt = MODE == kLora ? RowTile{0, ld.tile * BM, g.n - ld.tile * BM < BM ? g.n - ld.tile * BM : BM}
+                                     : find_tile<BM>(g.offsets, g.groups, g.n, ld.tile, lane);
+    ld.row0 = __builtin_amdgcn_readfirstlane(rt.row0);
+    ld.rows = __builtin_amdgcn_readfirstlane(rt.rows);
+    const int64_t e = MODE == kLora ? 0 : __builtin_amdgcn_readfirstlane(rt.e);
+    expert_row = e * N;
+    codes = buffer_at(g.qweight + e * N * words);
+  };
+  auto next = [&]() AWQ_INLINE {
+    if (--left <= 0) return;  // the last position's loads are repeated
+    if (++ld.part < parts) return;
+    ld.part = 0;
+    if (++ld.chunk < nt) return;
+    ld.chunk = 0;
+    ++ld.tile;
+    open_tile();
+  };
+
+  auto buffer = [&](int b) AWQ_INLINE -> uint4* {
+    return b == 0 ? st0[wave] : b == 1 ? st1[wave] : b == 2 ? st2[NB > 2 ? wave : 0] : st3[NB > 2 ? wave : 0];
+  };
+  // steps H i .. of the position being loaded into buffer b (those past the last step: the last
+  // ones, not multiplied)
+  auto load_codes = [&](int b, int i) AWQ_INLINE {
+    int s = step_of(ld.part, H * i);
+    s = s + H <= nsteps ? s : nsteps - H;
+    const uint32_t at = (uint32_t)first(ld.chunk) * rowq + (s < 0 ? 0 : s) * (16 * BITS);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        dma16(codes, buffer(b) + (r * 2 + d) * 64, vq[r][d], at);
+  };
+  // Buffer b's codes into registers: this lane's 32 channels of weight row c16 of every tile and
+  // step (3-bit: two low-plane words and one of the high plane). The DMAs sent after buffer b's
+  // are those of the other buffers, so vmcnt(their number) covers buffer b whatever else was
+  // sent in between; the LDS reads end before the block does.
+  constexpr int kLater = (NB - 1) * R * 2;
+  auto take_codes = [&](int b, uint32_t (&w)[H][R][BITS]) AWQ_INLINE {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)(buffer(b) + r * 128);
+        if constexpr (BITS == 3) {
+          const uint32_t at = base + (c16 * 24 + h * 12) * 4;
+          uint2 lo;
+          asm volatile("ds_read_b64 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                       : "=&v"(lo), "=&v"(w[h][r][2])
+                       : "v"(at + kg * 8), "v"(at + 32 + kg * 4)
+                       : "memory");
+          w[h][r][0] = lo.x;
+          w[h][r][1] = lo.y;
+        } else if constexpr (BITS == 8) {
+          const uint32_t row = base + c16 * 128;
+          u32x4 v0, v1;
+          asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                       : "=&v"(v0), "=&v"(v1)
+                       : "v"(row + ((2 * kg) ^ (c16 >> 1)) * 16), "v"(row + ((2 * kg + 1) ^ (c16 >> 1)) * 16)
+                       : "memory");
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[h][r][i] = v0[i];
+            w[h][r][4 + i] = v1[i];
+          }
+        }
+      }
+    if constexpr (BITS == 4) {
+      // both steps of two tiles per block: four reads in flight
+#pragma unroll
+      for (int r = 0; r < R; r += 2) {
+        const uint32_t row = (uint32_t)(uintptr_t)(lds_void*)(buffer(b) + r * 128) + c16 * 128;
+        u32x4 v[4];
+        asm volatile(
+            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:2048\n\t"
+            "ds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+            : "v"(row + (kg ^ (c16 >> 1)) * 16), "v"(row + ((4 + kg) ^ (c16 >> 1)) * 16)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[i & 1][r + (i >> 1)][k] = v[i][k];
+      }
+    }
+  };
+  struct ScaleZero {
+    Eight sc[G128 ? 1 : L], z[!G128 && BITS == 8 ? 2 : 1];  // as many as the group size asks for
+  };
+  auto load_scales = [&](ScaleZero& q) AWQ_INLINE {
+    int s = step_of(ld.part, 0);
+    s = s < nsteps ? s : 0;
+    const int64_t n = expert_row + first(ld.chunk) + my_row;
+    const int64_t as = (n * Gs + s * per) * 2, az = n * zbw + (BITS == 8 ? s * per : s * per / 2);
+    q.sc[0] = load8(g.scales, as, sbytes);
+    q.z[0] = load8(g.zeros, az, zbytes);
+    if constexpr (!G128) {  // the most that 32-channel groups need
+#pragma unroll
+      for (int i = 1; i < L; ++i) q.sc[i] = load8(g.scales, as + 8 * i, sbytes);
+      if constexpr (BITS == 8) q.z[1] = load8(g.zeros, az + 8, zbytes);
+    }
+  };
+
+  half8w a[MT][L][4];  // this wave's part of the tile's rows of X
+  f32x4w xs[MT][L], xb[MT][L];  // 128-channel groups: per step, -sum(x) and -sum(bias x)
+  auto load_x = [&](const StreamItem& it) AWQ_INLINE {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int r = t * 16 + c16;  // rows past the last read the last one, never stored
+      int xr = it.rows > 0 ? source(it.row0 + (r < it.rows ? r : it.rows - 1)) : 0;
+      if (MODE != kLora && g.order) xr = (int)((unsigned)xr / (unsigned)g.fan);
+      const uint16_t* const x = g.X + (int64_t)xr * K + kg * 32;
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const int s = step_of(it.part, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[t][j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * 8);
+          if (s >= nsteps) a[t][j][i] = half8w{};  // steps past the last add nothing
+        }
+      }
+    }
+    if constexpr (G128) {
+      const _Float16 o = -1;
+      const half8w ones{o, o, o, o, o, o, o, o}, bias = -bias_of<BITS>();
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+          xs[t][j] = xb[t][j] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            xs[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][i], ones, xs[t][j], 0, 0, 0);
+            xb[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][i], bias, xb[t][j], 0, 0, 0);
+          }
+        }
+    }
+  };
+
+  f32x4w acc[MT][R];
+  auto clear = [&]() AWQ_INLINE {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[t][r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  // A slice's scales and zeros of this lane's weight row of tile r, fetched from the lane that
+  // loaded them.
+  struct Fetched {
+    uint32_t sc[R][G128 ? L / 2 : 2 * L], z[R][G128 ? 1 : BITS == 8 ? L : 2];
+  };
+  auto fetch_all = [&](Fetched& f, const ScaleZero& q) AWQ_INLINE {
+    auto get = [&](const Eight* e, int at, int r) AWQ_INLINE -> uint32_t {
+      const uint32_t v = (uint32_t)(e[at / 2].value() >> (32 * (at & 1)));
+      return (uint32_t)__builtin_amdgcn_ds_bpermute((r * 16 + c16) * 4, (int)v);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < (G128 ? L / 2 : 2 * L); ++i) f.sc[r][i] = get(q.sc, i, r);
+#pragma unroll
+      for (int i = 0; i < (G128 ? 1 : BITS == 8 ? L : 2); ++i) f.z[r][i] = get(q.z, i, r);
+    }
+  };
+  // Step j of the wave's slice, codes w; on: the step exists. The R weight tiles are independent
+  // chains, walked side by side.
+  auto multiply_128 = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
+    f32x4w d[R][MT];
+    float f[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t sc = q.sc[r][j / 2] >> (16 * (j & 1));
+      f[r] = on ? h2f((uint16_t)sc) : 0.0f;
+      const float z = (float)(BITS == 8 ? (q.z[r][0] >> (8 * j)) & 0xFF : (q.z[r][0] >> (4 * j)) & 0xF);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[r][t][i] = __builtin_fmaf(z, xs[t][j][i], xb[t][j][i]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const half8w v = biased<BITS>(w[r], s, magic);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          d[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][s], v, d[r][t], 0, 0, 0);
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][r][i] = __builtin_fmaf(f[r], d[r][t][i], acc[t][r][i]);
+  };
+  auto multiply_small = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
+    // this lane's group of the step: per j + (kg >> gsh) within the slice
+    half2w c[R];
+    ZeroPair zp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // (both forms' words first: choosing between their places would put the array in memory)
+      const uint32_t a1 = q.sc[r][j], a2 = q.sc[r][2 * j], a3 = q.sc[r][2 * j + 1];
+      const uint32_t z1 = q.z[r][BITS == 8 ? j / 2 : 0], z2 = q.z[r][BITS == 8 ? j : j / 2];
+      uint32_t sc = gsh == 1 ? a1 : kg & 2 ? a3 : a2;
+      sc >>= 16 * (gsh == 1 ? kg >> 1 : kg & 1);
+      const uint32_t z = BITS == 8 ? (gsh == 1 ? z1 >> (16 * (j & 1) + 8 * (kg >> 1)) : z2 >> (8 * kg))
+                                   : (gsh == 1 ? z1 >> (8 * j + 4 * (kg >> 1)) : z2 >> (16 * (j & 1) + 4 * kg));
+      sc = on ? sc & 0xFFFF : 0;
+      c[r] = __builtin_bit_cast(half2w, sc | (sc << 16));
+      zp[r] = zero_pair(z & (BITS == 8 ? 0xFF : 0xF));
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const half8w v = centered<BITS>(w[r], s, zp[r], magic) *
+                         half8w{c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1]};
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][s], v, acc[t][r], 0, 0, 0);
+      }
+  };
+  // Adapters among the tile's rows in order of their first row, shared by the waves: their
+  // terms start the accumulators, while the item's codes are on their way.
+  auto adapters = [&](const StreamItem& it) AWQ_INLINE {
+    int src[MT], id[MT];
+    bool todo[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int r = t * 16 + c16;
+      src[t] = source(it.row0 + (r < it.rows ? r : it.rows - 1));
+      id[t] = r < it.rows ? g.ids[src[t]] : -1;
+      todo[t] = (unsigned)id[t] < (unsigned)g.groups;
+    }
+    const int blocks = (g.rank + kLoraBlock - 1) / kLoraBlock;
+    // the next adapter whose turn is this wave's, -1 after the last
+    int turn = 0;
+    auto pick = [&]() AWQ_INLINE -> int {
+      while (true) {
+        int ad = -1;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const uint64_t m = __ballot(todo[t]);
+          if (ad < 0 && m) ad = __builtin_amdgcn_readlane(id[t], __ffsll((unsigned long long)m) - 1);
+        }
+        if (ad < 0) return -1;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) todo[t] = todo[t] && id[t] != ad;
+        const bool hit = turn == wave;
+        turn = turn + 1 < S ? turn + 1 : 0;
+        if (hit) return ad;
+      }
+    };
+    struct Term {
+      half8w b[R], hi[MT], lo[MT];
+      float f[MT];
+    };
+    auto load_term = [&](Term& u, int ad, int k) AWQ_INLINE {
+      const uint16_t* const B = g.B + ((int64_t)ad * N + first(it.chunk)) * g.rank;
+      const int at = k * kLoraBlock + kg * 8;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        u.b[r] = at < g.rank ? *reinterpret_cast<const half8w*>(B + (int64_t)weight_row(r * 16 + c16) * g.rank + at)
+                             : half8w{};
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const LoraRow* const h = g.H + (int64_t)src[t] * blocks + k;
+        const bool mine = id[t] == ad;
+        u.hi[t] = mine ? *reinterpret_cast<const half8w*>(h->hi + kg * 8) : half8w{};
+        u.lo[t] = mine ? *reinterpret_cast<const half8w*>(h->lo + kg * 8) : half8w{};
+        u.f[t] = mine ? h->f : 0.0f;
+      }
+    };
+    int ad = pick(), k = 0;
+    if (ad < 0) return;
+    Term u;
+    load_term(u, ad, k);
+    while (ad >= 0) {
+      int ad2 = ad, k2 = k + 1;
+      if (k2 == blocks) {
+        k2 = 0;
+        ad2 = pick();
+      }
+      Term v;
+      if (ad2 >= 0) load_term(v, ad2, k2);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint64_t rows_of = __ballot(id[t] == ad);
+        if (!rows_of) continue;
+        float fr[4];
+        bool on[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fr[i] = __shfl(u.f[t], 4 * kg + i);
+          on[i] = (rows_of >> (4 * kg + i)) & 1;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          f32x4w d{0.0f, 0.0f, 0.0f, 0.0f};
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.hi[t], u.b[r], d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.lo[t], u.b[r], d, 0, 0, 0);
+          // only the adapter's own rows: an Inf or NaN of its B stays out of the others
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[t][r][i] = on[i] ? __builtin_fmaf(fr[i], d[i], acc[t][r][i]) : acc[t][r][i];
+        }
+      }
+      u = v;
+      ad = ad2;
+      k = k2;
+    }
+  };
+  // A barrier for LDS data alone: the DMAs in flight stay in flight.
+  auto meet = [&]() AWQ_INLINE { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  // The waves' partial tiles summed in a fixed order and stored. Accumulator layout: element i
+  // of lane l is (row 4 (l / 16) + i, column l % 16).
+  auto finish = [&](const StreamItem& it) AWQ_INLINE {
+    constexpr int RO = MODE == kGated ? R / 2 : R;  // output tiles
+    const int col0 = first(it.chunk) + c16;
+    auto sum = [&](int tile) AWQ_INLINE {
+      f32x4w v = red[tile * 64 + lane];
+#pragma unroll
+      for (int i = 1; i < S; ++i) v += red[(i * R + tile) * 64 + lane];
+      return v;
+    };
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) red[(wave * R + r) * 64 + lane] = acc[t][r];
+      meet();
+      for (int r = wave; r < RO; r += S) {
+        f32x4w v = sum(r);
+        if constexpr (MODE == kGated) {
+          const f32x4w up = sum(r + RO);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]) * up[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = t * 16 + 4 * kg + i;
+          if (row < it.rows && r * 16 + c16 < outs) {
+            const int64_t yr = MODE == kLora ? source(it.row0 + row) : it.row0 + row;
+            g.Y[yr * outs + col0 + r * 16] = f2h_bits(v[i]);
+          }
+        }
+      }
+      meet();  // before the next partial tiles
+    }
+    clear();
+  };
+
+  clear();
+  int todo = left;
+  open_tile();
+  StreamItem it[PU];
+  ScaleZero q[PU];
+#pragma unroll
+  for (int u = 0; u < PU; ++u) {
+    if (u) next();
+    it[u] = ld;
+    load_scales(q[u]);
+#pragma unroll
+    for (int i = 0; i < L / H; ++i) load_codes(u * (L / H) + i, i);
+  }
+  load_x(it[0]);
+  while (true) {
+#pragma unroll
+    for (int u = 0; u < PU; ++u) {
+      next();  // ld is PU positions ahead of it[u]
+      Fetched f;
+      fetch_all(f, q[u]);
+      load_scales(q[u]);
+      if (MODE == kLora && it[u].part == 0) adapters(it[u]);
+#pragma unroll
+      for (int i = 0; i < L / H; ++i) {
+        uint32_t w[H][R][BITS];
+        take_codes(u * (L / H) + i, w);
+        load_codes(u * (L / H) + i, i);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int s = step_of(it[u].part, H * i + h);
+          if constexpr (H > 1) {
+            // an odd last step lies in the second half of its buffer, loaded from one step earlier
+            if (h == 0 && s + 1 == nsteps && nsteps > 1) {
+              asm volatile("");  // a branch: not a select per word on every step
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int k = 0; k < BITS; ++k) w[0][r][k] = w[H - 1][r][k];
+            }
+          }
+          if constexpr (G128)
+            multiply_128(w[h], H * i + h, s < nsteps, f);
+          else
+            multiply_small(w[h], H * i + h, s < nsteps, f);
+        }
+      }
+      if (it[u].part == parts - 1) finish(it[u]);
+      if (--todo == 0) return;
+      const int tile = it[u].tile;
+      it[u] = ld;
+      const StreamItem& then = it[(u + 1) % PU];  // the position multiplied next
+      if (parts > 1 || then.tile != tile) load_x(then);
+    }
+  }
+}
+
+// The variants that the launcher picks from: row tiles mt, waves s.
+template <int MODE, int BITS, bool G128>
+void launch_stream_g(const GroupedArgs& g, int mt, int s, dim3 grid, hipStream_t stream) {
+  constexpr int R = stream_cols(BITS, 1) / 16;
+#define AWQ_CASE(MT, R, L, S) \
+  if (mt == MT && s == S)      \
+    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, MT, R, L, S>), grid, dim3(S * 64), 0, stream, g);
+  AWQ_CASE(1, R, 4, 2)
+  AWQ_CASE(1, R, 4, 4)
+  AWQ_CASE(1, R, 4, 8)
+  AWQ_CASE(2, 2, 2, 2)
+  AWQ_CASE(2, 2, 2, 4)
+  AWQ_CASE(2, 2, 2, 8)
+#undef AWQ_CASE
+}
+
+template <int MODE, int BITS>
+void launch_stream_t(const GroupedArgs& g, int mt, int s, dim3 grid, hipStream_t stream) {
+  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, mt, s, grid, stream);
+  else launch_stream_g<MODE, BITS, false>(g, mt, s, grid, stream);
+}
+
+}  // namespace awq

@@ -10,13 +10,16 @@ namespace awq {
 
 constexpr int kMaxGroups = 512;
 
-// Inclusive sum over the wave.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    v += lane >= d ? o : 0;
-  }
+// Inclusive sum over the wave: DPP row shifts, then the row broadcasts.
+__device__ __forceinline__ int wave_scan(int v) {
+#define AWQ_STEP(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false)
+  AWQ_STEP(0x111, 0xF);  // row_shr:1
+  AWQ_STEP(0x112, 0xF);
+  AWQ_STEP(0x114, 0xF);
+  AWQ_STEP(0x118, 0xF);
+  AWQ_STEP(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  AWQ_STEP(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef AWQ_STEP
   return v;
 }
 
@@ -45,7 +48,7 @@ __device__ __forceinline__ int count_tiles(const int32_t* offsets, int groups, i
       group_range(offsets, c + lane, n, lo, hi);
       t = (hi - lo + BM - 1) / BM;
     }
-    sum += __shfl(wave_scan(t, lane), kWave - 1);
+    sum += __builtin_amdgcn_readlane(wave_scan(t), kWave - 1);
   }
   return sum;
 }
@@ -59,18 +62,19 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int groups,
     int lo = 0, hi = 0;
     if (c + lane < groups) group_range(offsets, c + lane, n, lo, hi);
     const int t = (hi - lo + BM - 1) / BM;
-    const int incl = before + wave_scan(t, lane);
+    const int incl = before + wave_scan(t);
     const uint64_t m = __ballot(incl > at);
     if (m) {
       const int src = __ffsll((unsigned long long)m) - 1;
-      const int k = at - (__shfl(incl, src) - __shfl(t, src));  // tile k of that group
-      lo = __shfl(lo, src);
-      hi = __shfl(hi, src);
+      // tile k of that group
+      const int k = at - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(t, src));
+      lo = __builtin_amdgcn_readlane(lo, src);
+      hi = __builtin_amdgcn_readlane(hi, src);
       if ((unsigned)k >= (unsigned)((hi - lo + BM - 1) / BM)) break;  // sums that wrapped (wrong offsets)
       const int row0 = lo + k * BM;
       return RowTile{c + src, row0, hi - row0 < BM ? hi - row0 : BM};
     }
-    before = __shfl(incl, kWave - 1);
+    before = __builtin_amdgcn_readlane(incl, kWave - 1);
   }
   return RowTile{0, 0, 0};
 }

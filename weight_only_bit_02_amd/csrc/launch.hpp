@@ -145,6 +145,14 @@ hipError_t launch_combine(const uint16_t* P, const float* weights, const int32_t
                           const int32_t* valid, int64_t T, int top_k, int64_t N, const uint16_t* add,
                           uint16_t* Y, hipStream_t stream);
 
+// 32 values of scale X A^T for one row, as the second product's matrix cores take them:
+// v = f (hi + lo) with f a power of two and the largest |hi| in [1, 2), zeros past the rank.
+constexpr int kLoraBlock = 32;
+struct LoraRow {
+  uint16_t hi[kLoraBlock], lo[kLoraBlock];
+  float f, pad[3];
+};
+
 // Operands of the ragged-row linears. Experts: rows [offsets[e], offsets[e + 1]) take weight
 // e (weights stacked; `groups` of them), from X row p or order[p] / fan. Adapters: all n rows
 // (through order, if any) take the one weight, and row i adds H[i] B[ids[i]]^T.
@@ -156,26 +164,28 @@ struct GroupedArgs {
   const uint8_t* zeros;
   uint16_t* Y;
   const int32_t* ids;   // adapters: per row, outside [0, groups) none
-  const float* H;       // adapters: [n][rank], scale X A^T
+  const LoraRow* H;     // adapters: [n][ceil(rank / 32)], scale X A^T
   const uint16_t* B;    // adapters: [groups][N][rank]
   int64_t N, K;
   int n, fan, groups, group, nt, rank;
 };
 enum GroupedMode { kPlain = 0, kGated = 1, kLora = 2 };
 
-// The GEMM tiles (big: 256 rows, 128 with 8-bit codes; else 64) and the kernel that splits
-// K over the waves of a block, for few rows per group (grouped_skinny.hip).
+// The GEMM tiles (big: 256 rows, 128 with 8-bit codes; else 64) and the streaming kernel for
+// few rows per group (grouped_stream.hpp), on tiles of 16 row_tiles (1 or 2) rows, for the
+// sizes that it takes.
+bool grouped_stream_supported(int64_t weights, int64_t N, int64_t K, int group, int w_bit);
 hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, bool big, hipStream_t stream);
-hipError_t launch_grouped_skinny(GroupedArgs g, int mode, int w_bit, hipStream_t stream);
+hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, int row_tiles, hipStream_t stream);
 
 // AWQ_GROUPED_AUTO: by the mean rows per group (experts) or the rows (adapters).
 constexpr int64_t kSkinnyMeanRows = 16;
 constexpr int64_t kGemm64MeanRows = 96;
 constexpr int64_t kLoraGemmMinM = 512;
 
-// Adapters: H[i] = scale[a] X[i] A_a^T (fp32), a = ids[i]; rows without an adapter are left.
+// Adapters: H[i] = scale[a] X[i] A_a^T, a = ids[i]; rows without an adapter are left.
 hipError_t launch_lora_shrink(const uint16_t* X, int n, int64_t K, const uint16_t* A, const float* scale,
-                              int adapters, int rank, const int32_t* ids, const int32_t* order, float* H,
-                              hipStream_t stream);
+                              int adapters, int rank, const int32_t* ids, const int32_t* order,
+                              LoraRow* H, hipStream_t stream);
 
 }  // namespace awq

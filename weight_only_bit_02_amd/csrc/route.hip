@@ -140,7 +140,7 @@ __device__ __forceinline__ void block_exclusive(int* count, int n, int* part, in
   int base = 0;
   for (int c = 0; c < n; c += kThreads) {
     const int v = c + tid < n ? count[c + tid] : 0;
-    const int incl = wave_scan(v, lane);
+    const int incl = wave_scan(v);
     __syncthreads();  // part[] of the pass before has been read
     if (lane == 63) part[wave] = incl;
     __syncthreads();

@@ -1,0 +1,11 @@
+// 3-bit instantiations of the ragged-row streaming linear (kPlain), in a file of their own so
+// that the build compiles the variants in parallel.
+#include "grouped_stream.hpp"
+
+namespace awq {
+
+void launch_stream3_plain(const GroupedArgs& g, int mt, int s, dim3 grid, hipStream_t stream) {
+  launch_stream_t<kPlain, 3>(g, mt, s, grid, stream);
+}
+
+}  // namespace awq

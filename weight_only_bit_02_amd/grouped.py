@@ -30,17 +30,22 @@ _GROUPED_KERNELS = {"auto": 0, "skinny": 1, "gemm64": 2, "gemm": 3}
 
 
 def _check(t, dtype, shape, name, device):
+    """The address of a tensor that is what the call needs; these run on every call of a
+    decoding step, so what is right takes one pass and only a wrong tensor is looked at again."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, dtypes, dims, name):
@@ -86,6 +91,11 @@ def _launch(name, device, *args):
         _abi.check(name, status)
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(name, *sizes):
+    return getattr(_abi.load(), name)(*sizes)
+
+
 @functools.lru_cache(maxsize=None)
 def _config(group: int, w_bit: int):
     return C.pointer(_abi.config(group_size=group, w_bit=w_bit))
@@ -126,7 +136,7 @@ def group_rows(ids: torch.Tensor, n_groups: int, out: RowGroups | None = None,
     op = _check(out.offsets, torch.int32, (n_groups + 1,), "out.offsets", dev)
     rp = _check(out.order, torch.int32, (n,), "out.order", dev)
     pp = _check(out.pos, torch.int32, (n,), "out.pos", dev)
-    wp, wn, _keep = _workspace(workspace, _abi.load().awq_group_rows_workspace_size(n, n_groups), dev)
+    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_group_rows_workspace_size", n, n_groups), dev)
     _launch("awq_group_rows", dev, ip, n, n_groups, op, rp, pp, wp, wn)
     return out
 
@@ -150,7 +160,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: R
     op = _check(out.groups.offsets, torch.int32, (E + 1,), "out.groups.offsets", dev)
     rp = _check(out.groups.order, torch.int32, (n,), "out.groups.order", dev)
     pp = _check(out.groups.pos, torch.int32, (n,), "out.groups.pos", dev)
-    wp, wn, _keep = _workspace(workspace, _abi.load().awq_moe_route_workspace_size(T, E), dev)
+    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_moe_route_workspace_size", T, E), dev)
     _launch("awq_moe_route", dev, logits.data_ptr(), 0 if logits.dtype == torch.float16 else 1, T, E, ld,
             top_k, int(bool(renormalize)), wtp, ip, op, rp, pp, wp, wn, _flags(flags, dev))
     return out
@@ -309,7 +319,7 @@ def linear_w4a16_lora(X: torch.Tensor, w: PackedLinear, lora: LoraAdapters, ids:
     if out is None:
         out = torch.empty((M, w.N), dtype=torch.float16, device=dev)
     yp = _check(out, torch.float16, (M, w.N), "out", dev)
-    wp, wn, _keep = _workspace(workspace, _abi.load().awq_linear_w4a16_lora_workspace_size(M, rank), dev)
+    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_linear_w4a16_lora_workspace_size", M, rank), dev)
     _launch("awq_linear_w4a16_lora", dev, xp, M, qp, sp, zp, w.N, K, _config(w.group, w.w_bit), ap, bp, cp, L,
             rank, ip, rp, yp, wp, wn, _flags(flags, dev), _GROUPED_KERNELS[kernel])
     return out
