@@ -379,10 +379,14 @@ awq_status awq_moe_route(const void* logits, awq_logits_type type, int64_t T, in
 /* Which kernel the grouped linear and the linear with adapters run. */
 typedef enum awq_grouped_kernel {
   AWQ_GROUPED_AUTO = 0,   /* by rows per group (experts) or rows (adapters)              */
-  AWQ_GROUPED_SKINNY = 1, /* tiles of 32 rows, K split over the waves of a block
-                             (experts: n_rows <= 65536; adapters: M <= 64)              */
+  AWQ_GROUPED_SKINNY = 1, /* streaming kernel for few rows, tiles of 16 (experts:
+                             n_rows <= 65536; adapters: M <= 64; weights of less than
+                             eight bytes of zeros in all run GEMM64)                     */
   AWQ_GROUPED_GEMM64 = 2, /* MFMA GEMM on 64-row tiles                                   */
-  AWQ_GROUPED_GEMM = 3    /* MFMA GEMM on 256-row tiles (8-bit codes: 128)               */
+  AWQ_GROUPED_GEMM128 = 3,
+  AWQ_GROUPED_GEMM256 = 4,/* with 8-bit codes 128-row tiles                              */
+  AWQ_GROUPED_GEMM64K = 5 /* 64 x 64 tiles (32 x 64 with 8-bit codes), K split over a
+                             block's waves: several times the blocks                     */
 } awq_grouped_kernel;
 
 /*
@@ -396,7 +400,7 @@ typedef enum awq_grouped_kernel {
  *            as awq_quantize_pack writes it (packing the stacked [groups N][K] does)
  *   Y        fp16 [n_rows][N] out, in group order; rows from offsets[groups] on are left
  *            as they were
- *   1 <= n_rows < 2^30; x_rows K < 2^35. Formats, flags and accuracy as awq_linear_w4a16.
+ *   1 <= n_rows < 2^30; x_rows K <= 2^31, one weight's codes below 4 GiB. Formats, flags and accuracy as awq_linear_w4a16.
  *   _gated_silu: each weight is a gate|up pair (N even), Y fp16 [n_rows][N/2], as
  *   awq_linear_w4a16_gated_silu.
  */
@@ -436,7 +440,8 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
  *   X fp16 [M][K], packed weight and Y fp16 [M][N] as awq_linear_w4a16
  *   A fp16 [adapters][rank][K], B fp16 [adapters][N][rank], lora_scale fp32 [adapters];
  *   rank a multiple of 8 up to AWQ_MAX_LORA_RANK (smaller adapters padded with zero rows
- *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; 1 <= M < 2^30, M K < 2^35
+ *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; M >= 1, M K <= 2^31, codes below
+ *   4 GiB
  *   ids      int32 [M]
  *   order    int32 [M] or NULL: a permutation of the rows that brings those of one adapter
  *            together (awq_group_rows); it changes the speed of large mixed batches only

@@ -12,7 +12,7 @@ from tests.grouped_ref import (U, TINY, gated_reference, group_reference, linear
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["skinny", "gemm64", "gemm", "auto"]
+KERNELS = ["skinny", "gemm64", "gemm128", "gemm256", "gemm64k", "auto"]
 FORMATS = [(4, 128), (4, 64), (4, 32), (8, 128), (8, 64), (8, 32), (3, 128), (3, 64), (3, 32)]
 
 
@@ -133,12 +133,12 @@ def test_one_group_equals_the_plain_linear(w_bit, group, gated):
     f, h = ((awq.linear_w4a16_gated_silu, awq.linear_w4a16_grouped_gated_silu) if gated
             else (awq.linear_w4a16, awq.linear_w4a16_grouped))
     ref = f(X, p, kernel="gemm")
-    for kernel in ("gemm", "gemm64"):
+    for kernel in ("gemm64", "gemm128", "gemm256"):
         assert torch.equal(h(X, w, ids, kernel=kernel), ref)
         assert torch.equal(h(X, w, ids, fan=1, kernel=kernel), ref)
 
 
-@pytest.mark.parametrize("kernel", ["skinny", "gemm64", "gemm"])
+@pytest.mark.parametrize("kernel", ["skinny", "gemm64", "gemm128", "gemm256", "gemm64k"])
 def test_wrong_device_contents_stay_in_bounds(kernel):
     """Offsets and orders that say anything: no write outside the output, no fault."""
     E, N, K, n = 4, 40, 256, 50

@@ -55,7 +55,7 @@ def test_few_rows(M, kind):
     _check(case, si.activations(M, 384, offset=M), _ids(kind, M, 5, M), "auto")
 
 
-@pytest.mark.parametrize("kernel", ["gemm64", "gemm"])
+@pytest.mark.parametrize("kernel", ["gemm64", "gemm128", "gemm256", "gemm64k"])
 @pytest.mark.parametrize("grouped", [False, True])
 @pytest.mark.parametrize("M,kind", [(1, "same"), (65, "mixed"), (33, "none"), (300, "mixed"), (300, "runs"), (257, "same")])
 def test_many_rows(M, kind, grouped, kernel):
@@ -64,21 +64,21 @@ def test_many_rows(M, kind, grouped, kernel):
 
 
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 128, 256])
-@pytest.mark.parametrize("M,kernel", [(20, "skinny"), (70, "gemm64"), (140, "gemm")])
+@pytest.mark.parametrize("M,kernel", [(20, "skinny"), (70, "gemm64"), (130, "gemm128"), (140, "gemm256"), (90, "gemm64k")])
 def test_ranks(r, M, kernel):
     case = _case(40, 256, 3, r, seed=r)
     _check(case, si.activations(M, 256, offset=r), _ids("mixed", M, 3, r), kernel)
 
 
 @pytest.mark.parametrize("w_bit,group", [(4, 64), (4, 32), (8, 128), (8, 64), (8, 32), (3, 128), (3, 64), (3, 32)])
-@pytest.mark.parametrize("M,kernel", [(40, "skinny"), (70, "gemm64"), (140, "gemm")])
+@pytest.mark.parametrize("M,kernel", [(40, "skinny"), (70, "gemm64"), (130, "gemm128"), (140, "gemm256"), (90, "gemm64k")])
 def test_formats(w_bit, group, M, kernel):
     case = _case(90, 384, 4, 16, group, w_bit, seed=w_bit * group)
     _check(case, si.activations(M, 384, offset=M), _ids("mixed", M, 4, M), kernel)
 
 
 @pytest.mark.parametrize("N,K", [(1, 128), (2, 1152), (513, 128)])
-@pytest.mark.parametrize("M,kernel", [(1, "skinny"), (50, "skinny"), (66, "gemm64"), (258, "gemm")])
+@pytest.mark.parametrize("M,kernel", [(1, "skinny"), (50, "skinny"), (66, "gemm64"), (130, "gemm128"), (258, "gemm256"), (97, "gemm64k")])
 def test_odd_shapes(N, K, M, kernel):
     case = _case(N, K, 2, 8, seed=N)
     _check(case, si.activations(M, K, offset=K), _ids("mixed", M, 2, M), kernel)
@@ -86,7 +86,7 @@ def test_odd_shapes(N, K, M, kernel):
 
 def test_more_adapters_than_rows_of_a_tile():
     case = _case(64, 256, 100, 8, seed=5)
-    for M, kernel in ((64, "skinny"), (130, "gemm64"), (130, "gemm")):
+    for M, kernel in ((64, "skinny"), (130, "gemm64"), (130, "gemm128"), (130, "gemm256"), (130, "gemm64k")):
         ids = np.random.default_rng(M).permutation(100)[np.arange(M) % 100].astype(np.int32)
         _check(case, si.activations(M, 256, offset=M), ids, kernel)
         _check(case, si.activations(M, 256, offset=M), ids, kernel, grouped=True)
@@ -102,7 +102,7 @@ def test_magnitudes(size, M, kernel):
     _check((w, Wd, A, B, scale * np.float32(8)), X, _ids("mixed", M, 2, 8), kernel)
 
 
-@pytest.mark.parametrize("M,kernel", [(12, "skinny"), (100, "gemm64"), (200, "gemm")])
+@pytest.mark.parametrize("M,kernel", [(12, "skinny"), (100, "gemm64"), (150, "gemm128"), (200, "gemm256"), (90, "gemm64k")])
 def test_nonfinite_adapter_reaches_its_own_rows_only(M, kernel):
     w, Wd, A, B, scale = _case(64, 256, 4, 16, seed=9)
     X = si.activations(M, 256, offset=9)
@@ -126,7 +126,7 @@ def test_without_adapters_equals_the_plain_linear():
     lora = awq.LoraAdapters(to_dev(A), to_dev(B), to_dev(scale))
     none = torch.full((300,), -1, dtype=torch.int32, device=DEV)
     ref = awq.linear_w4a16(X, w, kernel="gemm")
-    for kernel in ("gemm64", "gemm"):
+    for kernel in ("gemm64", "gemm128", "gemm256"):
         assert torch.equal(awq.linear_w4a16_lora(X, w, lora, none, kernel=kernel), ref)
 
 
@@ -138,7 +138,7 @@ def test_wrong_orders_stay_in_bounds():
     g = awq.group_rows(ids, 2)
     for v in (-1, 100, 2 ** 31 - 1):
         g.order.fill_(v)
-        for kernel in ("gemm64", "gemm"):
+        for kernel in ("gemm64", "gemm128", "gemm256", "gemm64k"):
             out, check = guarded((100, 64), torch.float16)
             awq.linear_w4a16_lora(X, w, lora, ids, groups=g, out=out, kernel=kernel)
             check()

@@ -72,7 +72,7 @@ def test_grouped_linear(lib, gated):
     assert call(N=0) == SHAPE and call(K=100) == SHAPE and call(K=0) == SHAPE
     assert call(x_rows=1 << 28, K=256) == SHAPE                  # X of 2^36 values
     assert call(N=(1 << 31) - 2, n=1 << 20, x_rows=1 << 20) == SHAPE  # more tiles than a grid holds
-    assert call(kernel=4) == UNSUPPORTED and call(kernel=-1) == UNSUPPORTED
+    assert call(kernel=6) == UNSUPPORTED and call(kernel=-1) == UNSUPPORTED
     assert call(kernel=1, n=65537, x_rows=65537) == SHAPE
     if gated:
         assert call(N=63) == SHAPE
@@ -109,7 +109,7 @@ def test_lora(lib):
     need = lib.awq_linear_w4a16_lora_workspace_size(4, 16)
     assert need >= 4 * 16 * 4 and lib.awq_linear_w4a16_lora_workspace_size(0, 16) == 0
     assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE and call(ws=FAKE_ODD) == WORKSPACE
-    assert call(kernel=4) == UNSUPPORTED and call(M=65, kernel=1) == SHAPE
+    assert call(kernel=6) == UNSUPPORTED and call(M=65, kernel=1) == SHAPE
     assert call(cfg=C.byref(_abi.config(w_bit=2))) == UNSUPPORTED
 
 

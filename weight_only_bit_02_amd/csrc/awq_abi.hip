@@ -86,14 +86,18 @@ ClipLayout clip_layout(int64_t T, int64_t N, int64_t K, int n_shrink, int group)
 
 // Limits of the expert and adapter calls.
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and rows are kept in 32 bits
-constexpr int64_t kMaxElements = (int64_t)1 << 35;  // of X: 16-byte units are kept in 32 bits
+constexpr int64_t kMaxElements = (int64_t)1 << 31;  // of X: offsets in it are kept in 32 bits
 constexpr int64_t kSkinnyMaxRows = 65536;           // its grid: one row of blocks per row tile
+
+// One weight's codes are addressed with 32-bit offsets too.
+bool good_weight(int64_t N, int64_t K, int w_bit) { return N < ((int64_t)1 << 32) / (K * w_bit / 8); }
 
 bool good_groups(int32_t g) { return g >= 1 && g <= AWQ_MAX_GROUPS; }
 bool good_rank(int32_t r) { return r >= 8 && r <= AWQ_MAX_LORA_RANK && r % 8 == 0; }
 bool good_workspace(const void* p, size_t have, size_t need) {
   return need == 0 || (p && have >= need && aligned16(p));
 }
+// Row tiles of 32 rows of the GEMM choices.
 // Every tiling's block count stays in 31 bits (the narrowest: 64 rows x 128 outputs).
 bool grouped_grid_ok(int64_t n, int64_t N, int64_t groups) {
   return (n / 64 + groups + 1) < ((int64_t)1 << 30) / (N / 128 + 1);
@@ -504,12 +508,12 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
   memcpy(&kv, &kernel_arg, sizeof kv);
   const awq_config c = resolve(cfg);
   if (!X || !offsets || !qweight || !scales || !zeros || !Y) return AWQ_ERR_NULL_POINTER;
-  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM) return AWQ_ERR_UNSUPPORTED;
+  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM64K) return AWQ_ERR_UNSUPPORTED;
   if (n_rows < 1 || n_rows >= kMaxRows || x_rows < 1 || x_rows >= kMaxRows || !good_nk(N, K) ||
       !good_groups(groups) || (gated && N % 2 != 0))
     return AWQ_ERR_BAD_SHAPE;
   if (order ? fan < 1 || x_rows < (n_rows + fan - 1) / fan : x_rows < n_rows) return AWQ_ERR_BAD_SHAPE;
-  if (x_rows > kMaxElements / K || !grouped_grid_ok(n_rows, N, groups)) return AWQ_ERR_BAD_SHAPE;
+  if (x_rows > kMaxElements / K || !good_weight(N, K, c.w_bit) || !grouped_grid_ok(n_rows, N, groups)) return AWQ_ERR_BAD_SHAPE;
   if (kv == AWQ_GROUPED_SKINNY && n_rows > kSkinnyMaxRows) return AWQ_ERR_BAD_SHAPE;
   if (!aligned16(X) || !aligned16(offsets) || (order && !aligned16(order)) || !aligned16(qweight) ||
       !aligned16(scales) || !aligned16(zeros) || !aligned16(Y) || (flags && !aligned4(flags)))
@@ -536,19 +540,14 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
   g.groups = groups;
   g.group = c.group_size;
   const int mode = gated ? awq::kGated : awq::kPlain;
-  if (kv == AWQ_GROUPED_AUTO) {
-    const int64_t mean = n_rows / groups;
-    kv = mean < awq::kSkinnyMeanRows && n_rows <= kSkinnyMaxRows ? AWQ_GROUPED_SKINNY
-         : mean < awq::kGemm64MeanRows                           ? AWQ_GROUPED_GEMM64
-                                                                 : AWQ_GROUPED_GEMM;
-  }
-  if (kv == AWQ_GROUPED_SKINNY && !awq::grouped_stream_supported(groups, N, K, c.group_size, c.w_bit))
-    kv = AWQ_GROUPED_GEMM64;
-  if (kv == AWQ_GROUPED_SKINNY) {
-    const int64_t mean = n_rows / groups;
-    return hip_status(awq::launch_grouped_stream(g, mode, c.w_bit, mean <= 6 ? 1 : 2, st));
-  }
-  return hip_status(awq::launch_grouped_gemm(g, mode, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
+  const bool streams = awq::grouped_stream_supported(groups, N, K, c.group_size, c.w_bit);
+  if (kv == AWQ_GROUPED_AUTO)
+    kv = streams && n_rows <= kSkinnyMaxRows && n_rows <= (int64_t)awq::kSkinnyMeanRows * groups
+             ? AWQ_GROUPED_SKINNY
+             : awq::choose_grouped_gemm(g, mode, c.w_bit);
+  if (kv == AWQ_GROUPED_SKINNY && streams) return hip_status(awq::launch_grouped_stream(g, mode, c.w_bit, st));
+  if (kv == AWQ_GROUPED_SKINNY) kv = AWQ_GROUPED_GEMM64;
+  return hip_status(awq::launch_grouped_gemm(g, mode, c.w_bit, kv, st));
 }
 
 awq_status awq_linear_w4a16_grouped(const void* X, int64_t x_rows, const int32_t* offsets,
@@ -577,7 +576,7 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
                            int64_t N, const void* add, void* Y, void* stream) {
   if (!P || !weights || !pos || !offsets || !Y) return AWQ_ERR_NULL_POINTER;
   if (!good_groups(groups) || T < 1 || top_k < 1 || top_k > AWQ_MAX_TOP_K || T >= kMaxRows / top_k ||
-      N < 1 || N >= kMaxDim || T > kMaxElements * 4 / N)
+      N < 1 || N >= kMaxDim || T > ((int64_t)1 << 37) / N)
     return AWQ_ERR_BAD_SHAPE;
   if (!aligned16(P) || !aligned16(weights) || !aligned16(pos) || !aligned16(offsets) ||
       (add && !aligned16(add)) || !aligned16(Y))
@@ -603,9 +602,9 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
   const awq_config c = resolve(cfg);
   if (!X || !qweight || !scales || !zeros || !A || !B || !lora_scale || !ids || !Y)
     return AWQ_ERR_NULL_POINTER;
-  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM) return AWQ_ERR_UNSUPPORTED;
+  if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM64K) return AWQ_ERR_UNSUPPORTED;
   if (M < 1 || M >= kMaxRows || !good_nk(N, K) || !good_groups(adapters) || !good_rank(rank) ||
-      M > kMaxElements / K || !grouped_grid_ok(M, N, 1))
+      M > kMaxElements / K || !good_weight(N, K, c.w_bit) || !grouped_grid_ok(M, N, 1))
     return AWQ_ERR_BAD_SHAPE;
   if (kv == AWQ_GROUPED_SKINNY && M > AWQ_LORA_SKINNY_MAX_M) return AWQ_ERR_BAD_SHAPE;
   if (!good_workspace(workspace, workspace_bytes, awq_linear_w4a16_lora_workspace_size(M, rank)))
@@ -644,15 +643,12 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
   g.groups = adapters;
   g.group = c.group_size;
   g.rank = rank;
+  const bool streams = awq::grouped_stream_supported(1, N, K, c.group_size, c.w_bit);
   if (kv == AWQ_GROUPED_AUTO)
-    kv = M <= AWQ_LORA_SKINNY_MAX_M          ? AWQ_GROUPED_SKINNY
-         : M < awq::kLoraGemmMinM            ? AWQ_GROUPED_GEMM64
-                                             : AWQ_GROUPED_GEMM;
-  if (kv == AWQ_GROUPED_SKINNY && !awq::grouped_stream_supported(1, N, K, c.group_size, c.w_bit))
-    kv = AWQ_GROUPED_GEMM64;
-  if (kv == AWQ_GROUPED_SKINNY)
-    return hip_status(awq::launch_grouped_stream(g, awq::kLora, c.w_bit, M <= 16 ? 1 : 2, st));
-  return hip_status(awq::launch_grouped_gemm(g, awq::kLora, c.w_bit, kv == AWQ_GROUPED_GEMM, st));
+    kv = streams && M <= awq::kLoraSkinnyRows ? AWQ_GROUPED_SKINNY : awq::choose_grouped_gemm(g, awq::kLora, c.w_bit);
+  if (kv == AWQ_GROUPED_SKINNY && streams) return hip_status(awq::launch_grouped_stream(g, awq::kLora, c.w_bit, st));
+  if (kv == AWQ_GROUPED_SKINNY) kv = AWQ_GROUPED_GEMM64;
+  return hip_status(awq::launch_grouped_gemm(g, awq::kLora, c.w_bit, kv, st));
 }
 
 }  // extern "C"

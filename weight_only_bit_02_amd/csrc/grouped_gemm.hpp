@@ -9,21 +9,27 @@
 //
 // Tile RTM x 32 rows x 256 columns, K step 128, four waves side by side along the columns,
 // each owning all rows x 64 columns (v_mfma_f32_32x32x16_f16), so a column is widened once
-// per tile. Both operands go global -> LDS by 16-byte DMA into the other of two buffers
-// while a step is multiplied; A's DMA takes a row address per lane, so gathering costs
-// nothing. A row's 16 chunks are stored in slots c ^ (row % 16) and codes quarter-major:
-// both are read without bank conflicts. A tile with fewer rows runs a body with fewer row
-// tiles (a power of two), so a group's last tile costs the matrix work of the rows it has.
+// per tile. Both operands go global -> LDS by 16-byte DMA, up to NS - 1 steps ahead in a ring
+// of NS buffers that fills LDS (a step of a 64-row tile is multiplied in a quarter of the time
+// that its operands take to arrive: with two buffers 256 x 4096 x 4096 took 64 us, a step each
+// memory latency). A's DMA takes a row address per lane, so gathering costs nothing. A row's
+// 16 chunks are stored in slots c ^ (row % 16) and codes quarter-major: both are read without
+// bank conflicts. A tile with fewer rows runs a body with fewer row tiles (a power of two), so
+// a group's last tile costs the matrix work of the rows it has.
 //
-// RTM = 8 (8-bit codes: 4, LDS holds no more) serves large groups, one wave per SIMD;
-// RTM = 2 small ones, two blocks per CU.
+// One barrier per step, with a wait of its own for the DMAs of the step that begins
+// (__syncthreads would wait for those of all steps). The DMAs are written as instructions: of
+// the builtin's the compiler waits for every one in flight before each read of LDS.
+//
+// RTM = 8 (not with 8-bit codes: LDS holds no more) serves large groups, 4 middling ones or
+// grids that would leave CUs idle, 2 small ones.
 //
 // Operand values and their order along K are those of the 256-row GEMM, so an expert's rows
 // equal the plain linear's bit for bit where that runs its GEMM.
 //
 // Adapters (MODE kLora): the rows of one batch, optionally through `order` (then Y is
-// scattered back through it). Before the K loop each 32-row tile starts, for every adapter
-// among its rows, from H B_a^T (H = scale X A_a^T from the first product's kernel, as fp16 hi
+// scattered back through it). After the K loop each 32-row tile adds, for every adapter
+// among its rows, H B_a^T (H = scale X A_a^T from the first product's kernel, as fp16 hi
 // + lo under a power of two), rows of other adapters masked.
 #pragma once
 
@@ -40,28 +46,32 @@ namespace awq {
 constexpr int kGN = 256, kGK = 128;   // columns of a tile, channels of a K step
 constexpr int kGroupedTiles = 4;      // row tiles that share a column panel in the tile order
 
-template <int MODE, int RTM, int BITS>
-__global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(GroupedArgs g) {
-  constexpr int BM = RTM * 32;
-  constexpr int kQ = BITS;             // 16-byte quarters of a column's codes per step
-  constexpr int kBT = kGN * kQ / 256;  // B transfers per wave and step
-  __shared__ __attribute__((aligned(16))) uint4 a0s[BM * 16];
-  __shared__ __attribute__((aligned(16))) uint4 a1s[BM * 16];
-  __shared__ __attribute__((aligned(16))) uint4 b0s[kGN * kQ];
-  __shared__ __attribute__((aligned(16))) uint4 b1s[kGN * kQ];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// G32: 32-channel groups (else 128 or 64). KW: waves along K (1: four along the columns; 4).
+template <int MODE, int RTM, int BITS, bool G32, int KW>
+__global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
+  constexpr int BM = RTM * 32, BN = kGN / KW;
+  constexpr int kQ = BITS;   // 16-byte quarters of a column's codes per step
+  constexpr int kBT = kQ;    // B transfers per wave and step
+  constexpr int kBuf = BM * 16 + BN * kQ;  // 16-byte slots of a buffer: A, then codes
+  constexpr int kFit = 160 * 1024 / 16 / KW / kBuf, NS = kFit < 5 ? kFit : 5;
+  static_assert(NS >= 2, "two buffers fit LDS");
+  __shared__ __attribute__((aligned(16))) uint4 lds[KW * NS * kBuf];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m32 = lane & 31, kh = lane >> 5;
   const int64_t N = g.N, K = g.K, nh = N / 2;
+  // this wave among those that share its ring, among those along the columns and along K
+  const int part = KW == 1 ? wave : 0, kw = KW == 1 ? 0 : wave;
+  uint4* const ring = lds + kw * (NS * kBuf);
 
   // ---- this block's tile: XCD blockIdx % 8 takes a contiguous run of the tiles there are
-  const int mt = MODE == kLora ? (g.n + BM - 1) / BM : count_tiles<BM>(g.offsets, g.groups, g.n, lane);
+  const int mt = MODE == kLora ? (g.n + BM - 1) / BM : __builtin_amdgcn_readfirstlane(count_tiles<BM>(g.offsets, g.groups, g.n, lane));
   const int64_t tiles = (int64_t)mt * g.nt, per_xcd = (tiles + 7) / 8;
   const int64_t slot = blockIdx.x / 8, t = (int64_t)(blockIdx.x % 8) * per_xcd + slot;
   if (slot >= per_xcd || t >= tiles) return;
   const int first_m = (int)(t / ((int64_t)kGroupedTiles * g.nt)) * kGroupedTiles;
   const int gsz = mt - first_m < kGroupedTiles ? mt - first_m : kGroupedTiles;
   const int within = (int)(t - (int64_t)first_m * g.nt);
-  const int64_t n0 = (int64_t)(within / gsz) * (MODE == kGated ? kGN / 2 : kGN);
+  const int64_t n0 = (int64_t)(within / gsz) * (MODE == kGated ? BN / 2 : BN);
   const int at = first_m + within % gsz;
   const RowTile rt = MODE == kLora ? RowTile{0, at * BM, g.n - at * BM < BM ? g.n - at * BM : BM}
                                    : find_tile<BM>(g.offsets, g.groups, g.n, at, lane);
@@ -69,9 +79,9 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
   const int64_t e = MODE == kLora ? 0 : __builtin_amdgcn_readfirstlane(rt.e);
   if (rows <= 0) return;
 
-  const int g64 = g.group == 64, g32 = g.group == 32;
+  const int g64 = g.group == 64;
   const int64_t Gs = K / g.group, zbw = BITS == 8 ? Gs : (Gs + 1) / 2, words = K * BITS / 32;
-  const int64_t nsteps = K / kGK;
+  const int ksteps = (int)(K / kGK), nsteps = (ksteps - kw + KW - 1) / KW;  // all, this wave's
   const uint32_t* const qweight = g.qweight + e * N * words;
   const uint16_t* const scales = g.scales + e * N * Gs;
   const uint8_t* const zeros = g.zeros + e * N * zbw;
@@ -86,15 +96,16 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
     return (unsigned)o < (unsigned)g.n ? o : 0;
   };
 
-  // B DMA map, quarter-major: slot (wave * kBT + i) * 64 + lane = 16-byte quarter slot / 256
-  // of tile column slot % 256. Gated: tile columns [64 w, 64 w + 32) hold the gate rows and
+  // B DMA map, quarter-major: slot (part * kBT + i) * 64 + lane = 16-byte quarter slot / BN
+  // of tile column slot % BN. Gated: tile columns [64 w, 64 w + 32) hold the gate rows and
   // [64 w + 32, 64 w + 64) the up rows of outputs n0 + 32 w ... Columns past the end read the
   // last one (never stored).
-  const uint32_t* bptr[kBT];
+  uint32_t boff[kBT];
+  const u32x4 W = buffer_words(qweight);
 #pragma unroll
   for (int i = 0; i < kBT; ++i) {
-    const int s = (wave * kBT + i) * 64 + lane;
-    const int c = s % kGN, q = s / kGN;
+    const int s = (part * kBT + i) * 64 + lane;
+    const int c = s % BN, q = s / BN;
     int64_t n;
     if constexpr (MODE == kGated) {
       int64_t o = n0 + (c >> 6) * 32 + (c & 31);
@@ -103,82 +114,137 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
     } else {
       n = n0 + c < N ? n0 + c : N - 1;
     }
-    bptr[i] = qweight + n * words + q * 4;
+    boff[i] = (uint32_t)(n * words + q * 4) * 4;
   }
   // this lane's weight rows (gated: gate row and up row): scales and zeros
   int64_t bcol[2];
   if constexpr (MODE == kGated) {
-    const int64_t o = n0 + wave * 32 + m32;
+    const int64_t o = n0 + part * 32 + m32;
     bcol[0] = o < nh ? o : nh - 1;
     bcol[1] = bcol[0] + nh;
   } else {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int64_t n = n0 + wave * 64 + b * 32 + m32;
+      const int64_t n = n0 + part * 64 + b * 32 + m32;
       bcol[b] = n < N ? n : N - 1;
     }
   }
   // per column, the zero(s) and scale(s) of the lane half's 64 channels of a step: one group
   // of 128 (step) or 64 (2 step + kh), or two of 32 (4 step + 2 kh and the next)
+  constexpr int kZ = G32 ? 2 : 1;
   struct ScaleZero {
-    uint32_t zb[2], sc[2][2];
+    uint32_t zb[2][BITS == 8 ? kZ : 1], sc[2][kZ];
   };
-  auto load_sz = [&](ScaleZero& st, int64_t step) {
-    const int64_t g0 = g32 ? 4 * step + 2 * kh : g64 ? 2 * step + kh : step;
+  auto load_sz = [&](ScaleZero& st, int own) {
+    const int64_t step = own * KW + kw < ksteps ? own * KW + kw : ksteps - 1;
+    const int64_t g0 = G32 ? 4 * step + 2 * kh : g64 ? 2 * step + kh : step;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      st.zb[b] = zeros[bcol[b] * zbw + (BITS == 8 ? g0 : g0 >> 1)];
-      st.sc[b][0] = scales[bcol[b] * Gs + g0];
-      if (g32) {
-        if constexpr (BITS == 8) st.zb[b] |= (uint32_t)zeros[bcol[b] * zbw + g0 + 1] << 8;
-        st.sc[b][1] = scales[bcol[b] * Gs + g0 + 1];
-      } else {
-        st.sc[b][1] = st.sc[b][0];
-      }
+#pragma unroll
+      for (int i = 0; i < (BITS == 8 ? kZ : 1); ++i)
+        st.zb[b][i] = zeros[bcol[b] * zbw + (BITS == 8 ? g0 + i : g0 >> 1)];
+#pragma unroll
+      for (int i = 0; i < kZ; ++i) st.sc[b][i] = scales[bcol[b] * Gs + g0 + i];
     }
   };
 
-  // Adapters: the 32 rows from r0 on, times the adapters' B, into acc (zero at the start): the
-  // accumulators begin with the low-rank term, and the K loop adds the linear to it.
-  auto lora_tile = [&](int r0, f32x16w (&acc)[2]) {
-    const int r = r0 + m32;
-    const int src = source(row0 + (r < rows ? r : rows - 1));
-    const int id = r < rows ? g.ids[src] : -1;
+  // Adapters: adds the adapters' terms of T tiles of 32 rows from r0 on to their accumulators,
+  // one adapter after the other by first row (waves along K share them), the next one's B on its
+  // way meanwhile.
+  auto add_adapters = [&](int r0, auto tc, auto acc_of) __attribute__((always_inline)) {
+    constexpr int T = decltype(tc)::value;
+    int src[T], id[T];
+#pragma unroll
+    for (int a = 0; a < T; ++a) {
+      const int r = r0 + a * 32 + m32;
+      src[a] = source(row0 + (r < rows ? r : rows - 1));
+    }
+#pragma unroll
+    for (int a = 0; a < T; ++a) id[a] = g.ids[src[a]];
     const int blocks = (g.rank + kLoraBlock - 1) / kLoraBlock;
-    const LoraRow* const h = g.H + (int64_t)src * blocks;
-    uint64_t rest = __ballot((unsigned)id < (unsigned)g.groups);
-    while (rest) {  // one adapter after the other, by its first row
-      const int ad = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)rest) - 1);
-      const bool mine = id == ad;
-      const uint64_t rows_of = __ballot(mine);
-      rest &= ~rows_of;
-      const uint16_t* const B = g.B + (int64_t)ad * N * g.rank;
-      for (int k = 0; k < blocks; ++k) {
-        f32x16w d[2] = {f32x16w{}, f32x16w{}};
-        const float f = h[k].f;
+    for (int k = 0; k < blocks; ++k) {
+      half8w hi[T][2], lo[T][2];
+      float f[T];
+      bool todo[T];
+#pragma unroll
+      for (int a = 0; a < T; ++a) {
+        const LoraRow* const h = g.H + (int64_t)src[a] * blocks + k;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int at = s * 16 + kh * 8;
-          const half8w hi = mine ? *reinterpret_cast<const half8w*>(h[k].hi + at) : half8w{};
-          const half8w lo = mine ? *reinterpret_cast<const half8w*>(h[k].lo + at) : half8w{};
+          hi[a][s] = *reinterpret_cast<const half8w*>(h->hi + s * 16 + kh * 8);
+          lo[a][s] = *reinterpret_cast<const half8w*>(h->lo + s * 16 + kh * 8);
+        }
+        f[a] = h->f;
+        if (k == 0 && r0 + a * 32 + m32 >= rows) id[a] = -1;
+        todo[a] = (unsigned)id[a] < (unsigned)g.groups;
+      }
+      int turn = 0;
+      auto pick = [&]() __attribute__((always_inline)) -> int {  // the next adapter, -1 after the last
+        while (true) {
+          int ad = -1;
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const half8w bw = k * kLoraBlock + at < g.rank
-                                  ? *reinterpret_cast<const half8w*>(B + bcol[b] * g.rank + k * kLoraBlock + at)
-                                  : half8w{};
-            d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, bw, d[b], 0, 0, 0);
-            d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, bw, d[b], 0, 0, 0);
+          for (int a = 0; a < T; ++a) {
+            const uint64_t m = __ballot(todo[a]);
+            if (ad < 0 && m) ad = __builtin_amdgcn_readlane(id[a], __ffsll((unsigned long long)m) - 1);
+          }
+          if (ad < 0) return -1;
+#pragma unroll
+          for (int a = 0; a < T; ++a) todo[a] = todo[a] && id[a] != ad;
+          const bool hit = turn == kw;
+          turn = turn + 1 < KW ? turn + 1 : 0;
+          if (hit) return ad;
+        }
+      };
+      struct Weights {
+        half8w w[2][2];
+      };
+      auto load_b = [&](Weights& v, int ad) __attribute__((always_inline)) {
+        const uint16_t* const B = g.B + (int64_t)ad * N * g.rank + k * kLoraBlock + kh * 8;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            v.w[s][b] = k * kLoraBlock + s * 16 + kh * 8 < g.rank
+                            ? *reinterpret_cast<const half8w*>(B + bcol[b] * g.rank + s * 16)
+                            : half8w{};
+      };
+      int ad = pick();
+      if (ad < 0) return;
+      Weights now;
+      load_b(now, ad);
+      while (ad >= 0) {
+        const int ad2 = pick();
+        Weights then;
+        if (ad2 >= 0) load_b(then, ad2);
+#pragma unroll
+        for (int a = 0; a < T; ++a) {
+          const bool mine = id[a] == ad;
+          const uint32_t rows_of = (uint32_t)__ballot(mine);
+          if (!rows_of) continue;
+          f32x16w d[2] = {f32x16w{}, f32x16w{}};
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const half8w h = mine ? hi[a][s] : half8w{}, l = mine ? lo[a][s] : half8w{};
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(h, now.w[s][b], d[b], 0, 0, 0);
+              d[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(l, now.w[s][b], d[b], 0, 0, 0);
+            }
+          }
+          f32x16w* const acc = acc_of(a);
+          const uint32_t rows_kh = rows_of >> (4 * kh);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            // only the adapter's own rows: an Inf or NaN of its B stays out of the others
+            const int ri = 8 * (i >> 2) + (i & 3);
+            const float fr = __shfl(f[a], ri + 4 * kh);
+            const bool on = (rows_kh >> ri) & 1;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) acc[b][i] = on ? __builtin_fmaf(fr, d[b][i], acc[b][i]) : acc[b][i];
           }
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          // only the adapter's own rows: an Inf or NaN of its B stays out of the others
-          const int ri = 8 * (i >> 2) + 4 * kh + (i & 3);
-          const float fr = __shfl(f, ri);
-          const bool on = (rows_of >> ri) & 1;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) acc[b][i] = on ? __builtin_fmaf(fr, d[b][i], acc[b][i]) : acc[b][i];
-        }
+        now = then;
+        ad = ad2;
       }
     }
   };
@@ -186,19 +252,19 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
   // RT row tiles of 32 rows cover this tile's rows.
   auto run = [&](auto rtc) {
     constexpr int RT = decltype(rtc)::value;
-    constexpr int kAT = 2 * RT;  // A transfers per wave and step
-    // A DMA map: wave transfer i fills slots (wave * kAT + i) * 64 + lane: row r = (wave * kAT
-    // + i) * 4 + lane / 16, slot lane % 16 <- chunk (lane % 16) ^ (r % 16), as 16-byte units of
-    // X (the host admits X up to 2^32 of them). Rows past the last read the last one.
+    constexpr int kAT = 2 * RT * KW;  // A transfers per wave and step
+    // A DMA map: wave transfer i fills slots (part * kAT + i) * 64 + lane: row r = (part * kAT
+    // + i) * 4 + lane / 16, slot lane % 16 <- chunk (lane % 16) ^ (r % 16), as offsets in X (the
+    // host admits X up to 2^32 bytes). Rows past the last read the last one.
     uint32_t aoff[kAT];
 #pragma unroll
     for (int i = 0; i < kAT; ++i) {
-      const int r = (wave * kAT + i) * 4 + (lane >> 4);
+      const int r = (part * kAT + i) * 4 + (lane >> 4);
       int x = source(row0 + (r < rows ? r : rows - 1));
       if (MODE != kLora && g.order) x = (int)((unsigned)x / (unsigned)g.fan);
-      aoff[i] = (uint32_t)x * (uint32_t)(K / 8) + ((lane & 15) ^ (r & 15));
+      aoff[i] = (uint32_t)x * (uint32_t)(K * 2) + ((lane & 15) ^ (r & 15)) * 16;
     }
-    const uint4* const X = reinterpret_cast<const uint4*>(g.X);
+    const u32x4 X = buffer_words(g.X);
 
     f32x16w acc[RT][2];
 #pragma unroll
@@ -206,52 +272,60 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
 #pragma unroll
       for (int b = 0; b < 2; ++b) acc[a][b] = f32x16w{};
 
-    ScaleZero s0, s1;
+    // Share i of 4 of this wave's step `step` into buffer c, if there is such a step.
+    constexpr int kA4 = (kAT + 3) / 4, kB4 = (kBT + 3) / 4;
+    auto send = [&](auto c, int step, int i) __attribute__((always_inline)) {
+      if (step >= nsteps) return;
+      const uint32_t at = (uint32_t)(step * KW + kw);
+      uint4* const dst = ring + decltype(c)::value * kBuf;
 #pragma unroll
-    for (int i = 0; i < kAT; ++i)
-      __builtin_amdgcn_global_load_lds((const void*)(X + aoff[i]), (lds_void*)&a0s[(wave * kAT + i) * 64],
-                                       16, 0, 0);
+      for (int k = i * kA4; k < (i + 1) * kA4 && k < kAT; ++k)
+        dma16_own(X, &dst[(part * kAT + k) * 64], aoff[k], at * 256);
 #pragma unroll
-    for (int i = 0; i < kBT; ++i)
-      __builtin_amdgcn_global_load_lds((const void*)(bptr[i]), (lds_void*)&b0s[(wave * kBT + i) * 64],
-                                       16, 0, 0);
-    load_sz(s0, 0);
-    if constexpr (MODE == kLora) {
+      for (int k = i * kB4; k < (i + 1) * kB4 && k < kBT; ++k)
+        dma16_own(W, &dst[BM * 16 + (part * kBT + k) * 64], boff[k], at * (kQ * 16));
+    };
+    ScaleZero sz[NS];
+    auto prologue = [&](auto c) __attribute__((always_inline)) {
+      constexpr int b = decltype(c)::value;
+      if constexpr (b < NS - 1) {
+        load_sz(sz[b], b);
 #pragma unroll
-      for (int a = 0; a < RT; ++a) lora_tile(a * 32, acc[a]);
-    }
-    __syncthreads();
+        for (int i = 0; i < 4; ++i) send(c, b, i);
+      }
+    };
+    prologue(std::integral_constant<int, 0>{});
+    prologue(std::integral_constant<int, 1>{});
+    prologue(std::integral_constant<int, 2>{});
+    prologue(std::integral_constant<int, 3>{});
 
-    // One K step on buffer BUF (a compile-time constant, so each LDS access names one object).
-    auto body = [&](auto bufc, ScaleZero& cur, ScaleZero& nxt, int64_t step) {
-      constexpr int BUF = decltype(bufc)::value;
-      const uint4* ab = BUF ? a1s : a0s;
-      const uint4* bb = BUF ? b1s : b0s;
-      // the next step's operands (clamped: the last step reloads itself into the idle buffer)
-      const int64_t sn = step + 1 < nsteps ? step + 1 : nsteps - 1;
-      load_sz(nxt, sn);
+    // One K step from buffer C; the step NS - 1 ahead goes into the buffer of the step before.
+    auto body = [&](auto bufc, int step) __attribute__((always_inline)) {
+      constexpr int C = decltype(bufc)::value, F = (C + NS - 1) % NS;
+      using Free = std::integral_constant<int, F>;
+      // all but the DMAs of the NS - 2 steps after this one have landed (other loads in between
+      // only make the wait longer) and the last step's reads are done, in every wave of the ring
+      if (step + NS - 2 < nsteps)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * (kAT + kBT)) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      if constexpr (KW == 1) asm volatile("s_barrier" ::: "memory");
+      const uint4* ab = ring + C * kBuf;
+      const uint4* bb = ab + BM * 16;
+      const ScaleZero& cur = sz[C];
+      load_sz(sz[F], step + NS - 1);
       __builtin_amdgcn_sched_barrier(0);  // keep the scale loads at the top of the step
-      uint4* const adn = BUF ? a0s : a1s;
-      uint4* const bdn = BUF ? b0s : b1s;
-      auto dma_a = [&](int i) {
-        __builtin_amdgcn_global_load_lds((const void*)(X + (uint64_t)aoff[i] + sn * 16),
-                                         (lds_void*)&adn[(wave * kAT + i) * 64], 16, 0, 0);
-      };
-      auto dma_b = [&](int i) {
-        __builtin_amdgcn_global_load_lds((const void*)(bptr[i] + sn * (kQ * 4)),
-                                         (lds_void*)&bdn[(wave * kBT + i) * 64], 16, 0, 0);
-      };
-      half2w zz[2][2], zz64[2][2], s2[2][2];
-      const int hi = g64 ? kh : (int)(step & 1);  // zero nibble: group of 128 (step) or 64 (2 step + kh)
+      half2w zz[2][kZ], zz64[2][kZ], s2[2][kZ];
+      const int hi = g64 ? kh : (step * KW + kw) & 1;  // zero nibble: group of 128 (step) or 64 (2 step + kh)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kZ; ++i) {
           uint32_t z;
           if constexpr (BITS == 8)
-            z = g32 ? (cur.zb[b] >> (8 * i)) & 0xFF : cur.zb[b];
+            z = cur.zb[b][i];
           else
-            z = (cur.zb[b] >> (4 * (g32 ? i : hi))) & 0xF;
+            z = (cur.zb[b][0] >> (4 * (G32 ? i : hi))) & 0xF;
           const uint32_t z1024 = 0x6400u + z, z64 = 0x5400u + (z << 4);
           zz[b][i] = -__builtin_bit_cast(half2w, z1024 | (z1024 << 16));
           zz64[b][i] = -__builtin_bit_cast(half2w, z64 | (z64 << 16));
@@ -264,19 +338,19 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
       uint2 bh[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int col = wave * 64 + b * 32 + m32;
+        const int col = part * 64 + b * 32 + m32;
         if constexpr (BITS == 3) {
-          bq[b][0] = bb[kh * kGN + col];
-          const uint4 h4 = bb[2 * kGN + col];
+          bq[b][0] = bb[kh * BN + col];
+          const uint4 h4 = bb[2 * BN + col];
           bh[b] = kh ? make_uint2(h4.z, h4.w) : make_uint2(h4.x, h4.y);
         } else {
 #pragma unroll
-          for (int h = 0; h < kQL; ++h) bq[b][h] = bb[(kQL * kh + h) * kGN + col];
+          for (int h = 0; h < kQL; ++h) bq[b][h] = bb[(kQL * kh + h) * BN + col];
         }
       }
-      auto frags = [&](int s, half8w (&A)[RT], half8w (&B)[2]) {
+      auto frags = [&](int s, half8w (&A)[RT], half8w (&B)[2]) __attribute__((always_inline)) {
         const int c = kh * 8 + s;
-        const int zi = s >> 2;  // slices 0-3 lie in the half's first 32 channels
+        const int zi = G32 ? s >> 2 : 0;  // slices 0-3 lie in the half's first 32 channels
 #pragma unroll
         for (int a = 0; a < RT; ++a) {
           const int r = a * 32 + m32;
@@ -306,17 +380,9 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
       frags(0, A0, B0);
 #pragma unroll
       for (int s = 0; s < kGK / 16; s += 2) {
-        {  // a quarter of the next step's transfers
-          __builtin_amdgcn_sched_barrier(0);
-          constexpr int kA4 = (kAT + 3) / 4, kB4 = (kBT + 3) / 4;
-#pragma unroll
-          for (int i = 0; i < kA4; ++i)
-            if ((s >> 1) * kA4 + i < kAT) dma_a((s >> 1) * kA4 + i);
-#pragma unroll
-          for (int i = 0; i < kB4; ++i)
-            if ((s >> 1) * kB4 + i < kBT) dma_b((s >> 1) * kB4 + i);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        send(Free{}, step + NS - 1, s >> 1);  // a quarter of the transfers
+        __builtin_amdgcn_sched_barrier(0);
         frags(s + 1, A1, B1);
 #pragma unroll
         for (int a = 0; a < RT; ++a)
@@ -330,36 +396,76 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
           for (int b = 0; b < 2; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A1[a], B1[b], acc[a][b], 0, 0, 0);
       }
-      __syncthreads();  // the next step's DMA has landed; this step's buffer is free
     };
-    int64_t step = 0;
-    for (; step + 2 <= nsteps; step += 2) {
-      body(std::integral_constant<int, 0>{}, s0, s1, step);
-      body(std::integral_constant<int, 1>{}, s1, s0, step + 1);
+    int step = 0;
+    auto at = [&](auto c) __attribute__((always_inline)) {
+      if constexpr (decltype(c)::value < NS) body(c, step + decltype(c)::value);
+    };
+    for (; step + NS <= nsteps; step += NS) {
+      at(std::integral_constant<int, 0>{});
+      at(std::integral_constant<int, 1>{});
+      at(std::integral_constant<int, 2>{});
+      at(std::integral_constant<int, 3>{});
+      at(std::integral_constant<int, 4>{});
     }
-    if (step < nsteps) body(std::integral_constant<int, 0>{}, s0, s1, step);
+    if (step < nsteps) at(std::integral_constant<int, 0>{});
+    if (step + 1 < nsteps) at(std::integral_constant<int, 1>{});
+    if (step + 2 < nsteps) at(std::integral_constant<int, 2>{});
+    if (step + 3 < nsteps) at(std::integral_constant<int, 3>{});
 
+    if constexpr (MODE == kLora) {
+      constexpr int T = RT == 8 ? 2 : RT;  // (the sums of 256 rows leave registers for two)
+#pragma unroll
+      for (int a0 = 0; a0 < RT; a0 += T)
+        add_adapters(a0 * 32, std::integral_constant<int, T>{},
+                     [&](int a) __attribute__((always_inline)) { return acc[a0 + a]; });
+    }
     // 32x32 accumulator layout: element e of lane l is (row 8(e/4) + 4(l/32) + e%4, col l%32).
     const int64_t ldy = MODE == kGated ? nh : N;
-#pragma unroll
-    for (int a = 0; a < RT; ++a)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = a * 32 + 8 * (i >> 2) + 4 * kh + (i & 3);
-        if (r < rows) {
-          const int64_t yr = MODE == kLora ? source(row0 + r) : row0 + r;
-          if constexpr (MODE == kGated) {
-            const int64_t col = n0 + wave * 32 + m32;
-            if (col < nh) g.Y[yr * ldy + col] = f2h_bits(silu_f32(acc[a][0][i]) * acc[a][1][i]);
-          } else {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int64_t col = n0 + wave * 64 + b * 32 + m32;
-              if (col < N) g.Y[yr * ldy + col] = f2h_bits(acc[a][b][i]);
-            }
-          }
-        }
+    auto store = [&](int r, float v0, float v1) {
+      if (r >= rows) return;
+      const int64_t yr = MODE == kLora ? source(row0 + r) : row0 + r;
+      if constexpr (MODE == kGated) {
+        const int64_t col = n0 + part * 32 + m32;
+        if (col < nh) g.Y[yr * ldy + col] = f2h_bits(silu_f32(v0) * v1);
+      } else {
+        const int64_t col = n0 + part * 64 + m32;
+        if (col < N) g.Y[yr * ldy + col] = f2h_bits(v0);
+        if (col + 32 < N) g.Y[yr * ldy + col + 32] = f2h_bits(v1);
       }
+    };
+    if constexpr (KW == 1) {
+#pragma unroll
+      for (int a = 0; a < RT; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) store(a * 32 + 8 * (i >> 2) + 4 * kh + (i & 3), acc[a][0][i], acc[a][1][i]);
+    } else {
+      // the waves' sums meet in LDS, in the waves' order; wave w stores rows 8 w .. of every tile
+      static_assert(KW * RT * 8 * 64 <= KW * NS * kBuf, "the sums fit LDS");
+      f32x4w* const sums = reinterpret_cast<f32x4w*>(lds);
+      __syncthreads();  // no ring is read or filled any more
+#pragma unroll
+      for (int a = 0; a < RT; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sums[(wave * RT * 8 + (a * 2 + b) * 4 + q) * 64 + lane] =
+                f32x4w{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+      __syncthreads();
+#pragma unroll
+      for (int a = 0; a < RT; ++a) {
+        f32x4w v[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          v[b] = sums[((a * 2 + b) * 4 + wave) * 64 + lane];
+#pragma unroll
+          for (int w = 1; w < KW; ++w) v[b] += sums[(w * RT * 8 + (a * 2 + b) * 4 + wave) * 64 + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store(a * 32 + 8 * wave + 4 * kh + i, v[0][i], v[1][i]);
+      }
+    }
   };
   if constexpr (RTM == 8) {
     if (rows > 128) return run(std::integral_constant<int, 8>{});
@@ -367,8 +473,32 @@ __global__ void __launch_bounds__(256, RTM == 2 && BITS != 8 ? 2 : 1) k_grouped(
   if constexpr (RTM >= 4) {
     if (rows > 64) return run(std::integral_constant<int, 4>{});
   }
-  if (rows > 32) return run(std::integral_constant<int, 2>{});
+  if constexpr (RTM >= 2) {
+    if (rows > 32) return run(std::integral_constant<int, 2>{});
+  }
   run(std::integral_constant<int, 1>{});
+}
+
+// The variants that the launcher picks from (row tiles of 32, waves along K).
+template <int MODE, int BITS, bool G32>
+void launch_grouped_g(const GroupedArgs& g, int row_tiles, int k_waves, dim3 grid, hipStream_t stream) {
+  constexpr int kSplit = BITS == 8 ? 1 : 2;  // 8-bit: two 64-row steps of four waves would not fit LDS
+  if (k_waves > 1)
+    hipLaunchKernelGGL((k_grouped<MODE, kSplit, BITS, G32, 4>), grid, dim3(256), 0, stream, g);
+  else if (row_tiles == 2)
+    hipLaunchKernelGGL((k_grouped<MODE, 2, BITS, G32, 1>), grid, dim3(256), 0, stream, g);
+  else if (row_tiles == 4 || BITS == 8)
+    hipLaunchKernelGGL((k_grouped<MODE, 4, BITS, G32, 1>), grid, dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL((k_grouped<MODE, BITS == 8 ? 4 : 8, BITS, G32, 1>), grid, dim3(256), 0, stream, g);
+}
+
+template <int MODE, int BITS>
+void launch_grouped_t(const GroupedArgs& g, int row_tiles, int k_waves, dim3 grid, hipStream_t stream) {
+  if (g.group == 32)
+    launch_grouped_g<MODE, BITS, true>(g, row_tiles, k_waves, grid, stream);
+  else
+    launch_grouped_g<MODE, BITS, false>(g, row_tiles, k_waves, grid, stream);
 }
 
 }  // namespace awq

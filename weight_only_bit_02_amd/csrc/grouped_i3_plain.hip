@@ -4,11 +4,8 @@
 
 namespace awq {
 
-void launch_grouped3_plain(const GroupedArgs& g, bool big, dim3 grid, hipStream_t stream) {
-  if (big)
-    hipLaunchKernelGGL((k_grouped<kPlain, 8, 3>), grid, dim3(256), 0, stream, g);
-  else
-    hipLaunchKernelGGL((k_grouped<kPlain, 2, 3>), grid, dim3(256), 0, stream, g);
+void launch_grouped3_plain(const GroupedArgs& g, int row_tiles, int k_waves, dim3 grid, hipStream_t stream) {
+  launch_grouped_t<kPlain, 3>(g, row_tiles, k_waves, grid, stream);
 }
 
 }  // namespace awq

@@ -4,11 +4,8 @@
 
 namespace awq {
 
-void launch_grouped4_gated(const GroupedArgs& g, bool big, dim3 grid, hipStream_t stream) {
-  if (big)
-    hipLaunchKernelGGL((k_grouped<kGated, 8, 4>), grid, dim3(256), 0, stream, g);
-  else
-    hipLaunchKernelGGL((k_grouped<kGated, 2, 4>), grid, dim3(256), 0, stream, g);
+void launch_grouped4_gated(const GroupedArgs& g, int row_tiles, int k_waves, dim3 grid, hipStream_t stream) {
+  launch_grouped_t<kGated, 4>(g, row_tiles, k_waves, grid, stream);
 }
 
 }  // namespace awq

@@ -4,11 +4,8 @@
 
 namespace awq {
 
-void launch_grouped8_lora(const GroupedArgs& g, bool big, dim3 grid, hipStream_t stream) {
-  if (big)
-    hipLaunchKernelGGL((k_grouped<kLora, 4, 8>), grid, dim3(256), 0, stream, g);
-  else
-    hipLaunchKernelGGL((k_grouped<kLora, 2, 8>), grid, dim3(256), 0, stream, g);
+void launch_grouped8_lora(const GroupedArgs& g, int row_tiles, int k_waves, dim3 grid, hipStream_t stream) {
+  launch_grouped_t<kLora, 8>(g, row_tiles, k_waves, grid, stream);
 }
 
 }  // namespace awq

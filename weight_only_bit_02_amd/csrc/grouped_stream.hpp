@@ -1,5 +1,5 @@
 // Ragged-row linear for few rows per group (decoding): the products of grouped_gemm.hpp on
-// tiles of 16 MT rows. Decoding streams every active weight once and multiplies it with a
+// tiles of 16 rows. Decoding streams every active weight once and multiplies it with a
 // handful of rows, so the design is about bytes in flight, cache-line requests per byte and
 // instructions per byte.
 //
@@ -47,7 +47,6 @@
 
 namespace awq {
 
-typedef float f32x4w __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define AWQ_INLINE __attribute__((always_inline))
@@ -55,22 +54,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kStreamWaves = 8;     // S at most
 constexpr int kStreamSlots = 2048;  // resident waves: two per SIMD
 
-// Columns of an item: 8-bit codes take twice the LDS, two row tiles twice the registers.
-constexpr int stream_cols(int w_bit, int row_tiles) { return w_bit == 8 || row_tiles > 1 ? 32 : 64; }
-constexpr int stream_steps(int row_tiles) { return row_tiles == 1 ? 4 : 2; }
+constexpr int kStreamSteps = 4;     // L
 
-// Descriptor of the memory from p on (uniform): raw, offsets up to 2^32.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
-}
-
-// 16 bytes per lane from offset `lane_at` + `at` of b to consecutive slots from lds on. (The
-// global_load_lds form counts as a flat access, after which the compiler waits for everything.)
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t b, uint4* lds, uint32_t lane_at, uint32_t at) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the 16-byte form
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, lane_at, at, 0, 0);
-#endif
-}
+// Columns of an item: 8-bit codes take twice the LDS.
+constexpr int stream_cols(int w_bit) { return w_bit == 8 ? 32 : 64; }
 
 // Eight bytes at byte `at` of [p, p + bytes), bytes >= 8, at any alignment; those past the end
 // are not read: the load moves back, and the value is shifted when it is used (shifting it here
@@ -154,12 +141,12 @@ struct StreamItem {
 };
 
 // G128: 128-channel groups (else 64 or 32).
-template <int MODE, int BITS, bool G128, int MT, int R, int L, int S>
+template <int MODE, int BITS, bool G128, int R, int L, int S>
 __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2)))
     k_stream(GroupedArgs g) {
-  constexpr int BM = 16 * MT, kCols = MODE == kGated ? 8 * R : 16 * R;
+  constexpr int BM = 16, kCols = MODE == kGated ? 8 * R : 16 * R;
   constexpr int H = BITS == 8 ? 1 : 2;        // steps of a buffer: 128 bytes of a row (3-bit: 96)
-  constexpr int NB = 4 / H, PU = 4 / L;       // buffers; positions that they hold together
+  constexpr int NB = L / H;                   // buffers, one position's codes
   constexpr int P = BITS * H;                 // 16-byte pieces of a row in a buffer
   constexpr int kBuf = R * 2 * 64;            // slots of a wave's buffer: two DMA instructions a tile
   __shared__ __attribute__((aligned(16))) uint4 st0[S][kBuf];
@@ -194,6 +181,8 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     o = o < outs ? o : outs - 1;
     return (uint32_t)o + (MODE == kGated && c >= 8 * R ? (uint32_t)nh : 0u);
   };
+  // (K of a single step: a row's bytes end inside the buffer; the rest repeats its first piece)
+  const int pieces = BITS * (nsteps < H ? nsteps : H);
   // DMA slot of a weight tile's buffer: piece (slot % P) ^ swizzle of row slot / P (3-bit: not
   // swizzled; slots past the last row repeat it)
   uint32_t vq[R][2];
@@ -203,7 +192,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     for (int d = 0; d < 2; ++d) {
       const int slot = d * 64 + lane, row = slot / P < 16 ? slot / P : 15;
       const int piece = BITS == 3 ? slot % P : (slot & 7) ^ (row >> 1);
-      vq[r][d] = weight_row(r * 16 + row) * rowq + piece * 16;
+      vq[r][d] = weight_row(r * 16 + row) * rowq + (piece < pieces ? piece * 16 : 0);
     }
   const uint32_t my_row = weight_row(lane % (16 * R));  // scales and zeros: one weight row per lane
   __amdgpu_buffer_rsrc_t codes;
@@ -325,48 +314,41 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     }
   };
 
-  half8w a[MT][L][4];  // this wave's part of the tile's rows of X
-  f32x4w xs[MT][L], xb[MT][L];  // 128-channel groups: per step, -sum(x) and -sum(bias x)
+  half8w a[L][4];  // this wave's part of the tile's rows of X
+  f32x4w xs[L], xb[L];  // 128-channel groups: per step, -sum(x) and -sum(bias x)
   auto load_x = [&](const StreamItem& it) AWQ_INLINE {
+    const int r = c16;  // rows past the last read the last one, never stored
+    int xr = it.rows > 0 ? source(it.row0 + (r < it.rows ? r : it.rows - 1)) : 0;
+    if (MODE != kLora && g.order) xr = (int)((unsigned)xr / (unsigned)g.fan);
+    const uint16_t* const x = g.X + (int64_t)xr * K + kg * 32;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int r = t * 16 + c16;  // rows past the last read the last one, never stored
-      int xr = it.rows > 0 ? source(it.row0 + (r < it.rows ? r : it.rows - 1)) : 0;
-      if (MODE != kLora && g.order) xr = (int)((unsigned)xr / (unsigned)g.fan);
-      const uint16_t* const x = g.X + (int64_t)xr * K + kg * 32;
+    for (int j = 0; j < L; ++j) {
+      const int s = step_of(it.part, j);
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const int s = step_of(it.part, j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[t][j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * 8);
-          if (s >= nsteps) a[t][j][i] = half8w{};  // steps past the last add nothing
-        }
+      for (int i = 0; i < 4; ++i) {
+        a[j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * 8);
+        if (s >= nsteps) a[j][i] = half8w{};  // steps past the last add nothing
       }
     }
     if constexpr (G128) {
       const _Float16 o = -1;
       const half8w ones{o, o, o, o, o, o, o, o}, bias = -bias_of<BITS>();
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int j = 0; j < L; ++j) {
+        xs[j] = xb[j] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-          xs[t][j] = xb[t][j] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xs[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][i], ones, xs[t][j], 0, 0, 0);
-            xb[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][i], bias, xb[t][j], 0, 0, 0);
-          }
+        for (int i = 0; i < 4; ++i) {
+          xs[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][i], ones, xs[j], 0, 0, 0);
+          xb[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][i], bias, xb[j], 0, 0, 0);
         }
+      }
     }
   };
 
-  f32x4w acc[MT][R];
+  f32x4w acc[R];
   auto clear = [&]() AWQ_INLINE {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[t][r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int r = 0; r < R; ++r) acc[r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
   };
   // A slice's scales and zeros of this lane's weight row of tile r, fetched from the lane that
   // loaded them.
@@ -389,7 +371,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   // Step j of the wave's slice, codes w; on: the step exists. The R weight tiles are independent
   // chains, walked side by side.
   auto multiply_128 = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
-    f32x4w d[R][MT];
+    f32x4w d[R];
     float f[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -397,25 +379,19 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       f[r] = on ? h2f((uint16_t)sc) : 0.0f;
       const float z = (float)(BITS == 8 ? (q.z[r][0] >> (8 * j)) & 0xFF : (q.z[r][0] >> (4 * j)) & 0xF);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[r][t][i] = __builtin_fmaf(z, xs[t][j][i], xb[t][j][i]);
+      for (int i = 0; i < 4; ++i) d[r][i] = __builtin_fmaf(z, xs[j][i], xb[j][i]);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const half8w v = biased<BITS>(w[r], s, magic);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          d[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][s], v, d[r][t], 0, 0, 0);
+        d[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], v, d[r], 0, 0, 0);
       }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][r][i] = __builtin_fmaf(f[r], d[r][t][i], acc[t][r][i]);
+      for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(f[r], d[r][i], acc[r][i]);
   };
   auto multiply_small = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
     // this lane's group of the step: per j + (kg >> gsh) within the slice
@@ -440,45 +416,35 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       for (int r = 0; r < R; ++r) {
         const half8w v = centered<BITS>(w[r], s, zp[r], magic) *
                          half8w{c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1]};
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          acc[t][r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t][j][s], v, acc[t][r], 0, 0, 0);
+        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], v, acc[r], 0, 0, 0);
       }
   };
   // Adapters among the tile's rows in order of their first row, shared by the waves: their
   // terms start the accumulators, while the item's codes are on their way.
   auto adapters = [&](const StreamItem& it) AWQ_INLINE {
-    int src[MT], id[MT];
-    bool todo[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int r = t * 16 + c16;
-      src[t] = source(it.row0 + (r < it.rows ? r : it.rows - 1));
-      id[t] = r < it.rows ? g.ids[src[t]] : -1;
-      todo[t] = (unsigned)id[t] < (unsigned)g.groups;
-    }
+    int src, id;
+    bool todo;
+    const int r = c16;
+    src = source(it.row0 + (r < it.rows ? r : it.rows - 1));
+    id = r < it.rows ? g.ids[src] : -1;
+    todo = (unsigned)id < (unsigned)g.groups;
     const int blocks = (g.rank + kLoraBlock - 1) / kLoraBlock;
     // the next adapter whose turn is this wave's, -1 after the last
     int turn = 0;
     auto pick = [&]() AWQ_INLINE -> int {
       while (true) {
-        int ad = -1;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const uint64_t m = __ballot(todo[t]);
-          if (ad < 0 && m) ad = __builtin_amdgcn_readlane(id[t], __ffsll((unsigned long long)m) - 1);
-        }
-        if (ad < 0) return -1;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) todo[t] = todo[t] && id[t] != ad;
+        const uint64_t m = __ballot(todo);
+        if (!m) return -1;
+        const int ad = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)m) - 1);
+        todo = todo && id != ad;
         const bool hit = turn == wave;
         turn = turn + 1 < S ? turn + 1 : 0;
         if (hit) return ad;
       }
     };
     struct Term {
-      half8w b[R], hi[MT], lo[MT];
-      float f[MT];
+      half8w b[R], hi, lo;
+      float f;
     };
     auto load_term = [&](Term& u, int ad, int k) AWQ_INLINE {
       const uint16_t* const B = g.B + ((int64_t)ad * N + first(it.chunk)) * g.rank;
@@ -487,14 +453,11 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       for (int r = 0; r < R; ++r)
         u.b[r] = at < g.rank ? *reinterpret_cast<const half8w*>(B + (int64_t)weight_row(r * 16 + c16) * g.rank + at)
                              : half8w{};
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const LoraRow* const h = g.H + (int64_t)src[t] * blocks + k;
-        const bool mine = id[t] == ad;
-        u.hi[t] = mine ? *reinterpret_cast<const half8w*>(h->hi + kg * 8) : half8w{};
-        u.lo[t] = mine ? *reinterpret_cast<const half8w*>(h->lo + kg * 8) : half8w{};
-        u.f[t] = mine ? h->f : 0.0f;
-      }
+      const LoraRow* const h = g.H + (int64_t)src * blocks + k;
+      const bool mine = id == ad;
+      u.hi = mine ? *reinterpret_cast<const half8w*>(h->hi + kg * 8) : half8w{};
+      u.lo = mine ? *reinterpret_cast<const half8w*>(h->lo + kg * 8) : half8w{};
+      u.f = mine ? h->f : 0.0f;
     };
     int ad = pick(), k = 0;
     if (ad < 0) return;
@@ -508,27 +471,23 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       }
       Term v;
       if (ad2 >= 0) load_term(v, ad2, k2);
+      const uint64_t rows_of = __ballot(id == ad);
+      float fr[4];
+      bool on[4];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const uint64_t rows_of = __ballot(id[t] == ad);
-        if (!rows_of) continue;
-        float fr[4];
-        bool on[4];
+      for (int i = 0; i < 4; ++i) {
+        fr[i] = __shfl(u.f, 4 * kg + i);
+        on[i] = (rows_of >> (4 * kg + i)) & 1;
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fr[i] = __shfl(u.f[t], 4 * kg + i);
-          on[i] = (rows_of >> (4 * kg + i)) & 1;
-        }
+      for (int r = 0; r < R; ++r) {
+        f32x4w d{0.0f, 0.0f, 0.0f, 0.0f};
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.hi, u.b[r], d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.lo, u.b[r], d, 0, 0, 0);
+        // only the adapter's own rows: an Inf or NaN of its B stays out of the others
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          f32x4w d{0.0f, 0.0f, 0.0f, 0.0f};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.hi[t], u.b[r], d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(u.lo[t], u.b[r], d, 0, 0, 0);
-          // only the adapter's own rows: an Inf or NaN of its B stays out of the others
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[t][r][i] = on[i] ? __builtin_fmaf(fr[i], d[i], acc[t][r][i]) : acc[t][r][i];
-        }
+        for (int i = 0; i < 4; ++i)
+          acc[r][i] = on[i] ? __builtin_fmaf(fr[i], d[i], acc[r][i]) : acc[r][i];
       }
       u = v;
       ad = ad2;
@@ -549,107 +508,92 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       return v;
     };
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    for (int r = 0; r < R; ++r) red[(wave * R + r) * 64 + lane] = acc[r];
+    meet();
+    for (int r = wave; r < RO; r += S) {
+      f32x4w v = sum(r);
+      if constexpr (MODE == kGated) {
+        const f32x4w up = sum(r + RO);
 #pragma unroll
-      for (int r = 0; r < R; ++r) red[(wave * R + r) * 64 + lane] = acc[t][r];
-      meet();
-      for (int r = wave; r < RO; r += S) {
-        f32x4w v = sum(r);
-        if constexpr (MODE == kGated) {
-          const f32x4w up = sum(r + RO);
+        for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]) * up[i];
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = silu_f32(v[i]) * up[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = t * 16 + 4 * kg + i;
-          if (row < it.rows && r * 16 + c16 < outs) {
-            const int64_t yr = MODE == kLora ? source(it.row0 + row) : it.row0 + row;
-            g.Y[yr * outs + col0 + r * 16] = f2h_bits(v[i]);
-          }
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * kg + i;
+        if (row < it.rows && r * 16 + c16 < outs) {
+          const int64_t yr = MODE == kLora ? source(it.row0 + row) : it.row0 + row;
+          g.Y[yr * outs + col0 + r * 16] = f2h_bits(v[i]);
         }
       }
-      meet();  // before the next partial tiles
     }
+    meet();  // before the next partial tiles
     clear();
   };
 
   clear();
   int todo = left;
   open_tile();
-  StreamItem it[PU];
-  ScaleZero q[PU];
+  StreamItem it = ld;
+  ScaleZero q;
+  load_scales(q);
 #pragma unroll
-  for (int u = 0; u < PU; ++u) {
-    if (u) next();
-    it[u] = ld;
-    load_scales(q[u]);
-#pragma unroll
-    for (int i = 0; i < L / H; ++i) load_codes(u * (L / H) + i, i);
-  }
-  load_x(it[0]);
+  for (int i = 0; i < L / H; ++i) load_codes(i, i);
+  load_x(it);
   while (true) {
+    next();  // ld is a position ahead of it
+    Fetched f;
+    fetch_all(f, q);
+    load_scales(q);
+    if (MODE == kLora && it.part == 0) adapters(it);
 #pragma unroll
-    for (int u = 0; u < PU; ++u) {
-      next();  // ld is PU positions ahead of it[u]
-      Fetched f;
-      fetch_all(f, q[u]);
-      load_scales(q[u]);
-      if (MODE == kLora && it[u].part == 0) adapters(it[u]);
+    for (int i = 0; i < L / H; ++i) {
+      uint32_t w[H][R][BITS];
+      take_codes(i, w);
+      load_codes(i, i);
 #pragma unroll
-      for (int i = 0; i < L / H; ++i) {
-        uint32_t w[H][R][BITS];
-        take_codes(u * (L / H) + i, w);
-        load_codes(u * (L / H) + i, i);
+      for (int h = 0; h < H; ++h) {
+        const int s = step_of(it.part, H * i + h);
+        if constexpr (H > 1) {
+          // an odd last step lies in the second half of its buffer, loaded from one step earlier
+          if (h == 0 && s + 1 == nsteps && nsteps > 1) {
+            asm volatile("");  // a branch: not a select per word on every step
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const int s = step_of(it[u].part, H * i + h);
-          if constexpr (H > 1) {
-            // an odd last step lies in the second half of its buffer, loaded from one step earlier
-            if (h == 0 && s + 1 == nsteps && nsteps > 1) {
-              asm volatile("");  // a branch: not a select per word on every step
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < BITS; ++k) w[0][r][k] = w[H - 1][r][k];
-            }
+              for (int k = 0; k < BITS; ++k) w[0][r][k] = w[H - 1][r][k];
           }
-          if constexpr (G128)
-            multiply_128(w[h], H * i + h, s < nsteps, f);
-          else
-            multiply_small(w[h], H * i + h, s < nsteps, f);
         }
+        if constexpr (G128)
+          multiply_128(w[h], H * i + h, s < nsteps, f);
+        else
+          multiply_small(w[h], H * i + h, s < nsteps, f);
       }
-      if (it[u].part == parts - 1) finish(it[u]);
-      if (--todo == 0) return;
-      const int tile = it[u].tile;
-      it[u] = ld;
-      const StreamItem& then = it[(u + 1) % PU];  // the position multiplied next
-      if (parts > 1 || then.tile != tile) load_x(then);
     }
+    if (it.part == parts - 1) finish(it);
+    if (--todo == 0) break;
+    const int tile = it.tile;
+    it = ld;
+    if (parts > 1 || it.tile != tile) load_x(it);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last position's loads were repeated: LDS stays theirs until then
 }
 
-// The variants that the launcher picks from: row tiles mt, waves s.
+// The variants that the launcher picks from: s waves.
 template <int MODE, int BITS, bool G128>
-void launch_stream_g(const GroupedArgs& g, int mt, int s, dim3 grid, hipStream_t stream) {
-  constexpr int R = stream_cols(BITS, 1) / 16;
-#define AWQ_CASE(MT, R, L, S) \
-  if (mt == MT && s == S)      \
-    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, MT, R, L, S>), grid, dim3(S * 64), 0, stream, g);
-  AWQ_CASE(1, R, 4, 2)
-  AWQ_CASE(1, R, 4, 4)
-  AWQ_CASE(1, R, 4, 8)
-  AWQ_CASE(2, 2, 2, 2)
-  AWQ_CASE(2, 2, 2, 4)
-  AWQ_CASE(2, 2, 2, 8)
-#undef AWQ_CASE
+void launch_stream_g(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
+  constexpr int R = stream_cols(BITS) / 16, L = kStreamSteps;
+  if (s == 2)
+    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 2>), grid, dim3(128), 0, stream, g);
+  else if (s == 4)
+    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 4>), grid, dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 8>), grid, dim3(512), 0, stream, g);
 }
 
 template <int MODE, int BITS>
-void launch_stream_t(const GroupedArgs& g, int mt, int s, dim3 grid, hipStream_t stream) {
-  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, mt, s, grid, stream);
-  else launch_stream_g<MODE, BITS, false>(g, mt, s, grid, stream);
+void launch_stream_t(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
+  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, s, grid, stream);
+  else launch_stream_g<MODE, BITS, false>(g, s, grid, stream);
 }
 
 }  // namespace awq

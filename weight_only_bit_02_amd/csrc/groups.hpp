@@ -5,10 +5,12 @@
 #pragma once
 
 #include "common.hpp"
+#include "widen.hpp"
 
 namespace awq {
 
 constexpr int kMaxGroups = 512;
+typedef float f32x4w __attribute__((ext_vector_type(4)));
 
 // Inclusive sum over the wave: DPP row shifts, then the row broadcasts.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -77,6 +79,38 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int groups,
     before = __builtin_amdgcn_readlane(incl, kWave - 1);
   }
   return RowTile{0, 0, 0};
+}
+
+// Descriptor of the memory from p on (uniform): raw, offsets up to 2^32.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+}
+
+// 16 bytes per lane from offset `lane_at` + `at` of b to consecutive slots from lds on. (The
+// global_load_lds form counts as a flat access, after which the compiler waits for everything.)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t b, uint4* lds, uint32_t lane_at, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the 16-byte form
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, lane_at, at, 0, 0);
+#endif
+}
+
+// The same as an instruction that the compiler neither counts nor waits for: the caller waits
+// (vmcnt) before the data is read and before the wave ends, and lets no read of LDS that must
+// come before or after pass it. It has no output register.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ u32x4 buffer_words(const void* p) {
+  const uint64_t a = (uint64_t)p;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFF, 0xFFFFFFFFu, 0x00020000u};
+}
+
+__device__ __forceinline__ void dma16_own(u32x4 b, uint4* lds, uint32_t lane_at, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"s"(to), "v"(lane_at), "s"(b), "s"(at)
+               : "memory", "m0");
+#endif
 }
 
 }  // namespace awq

@@ -171,17 +171,18 @@ struct GroupedArgs {
 };
 enum GroupedMode { kPlain = 0, kGated = 1, kLora = 2 };
 
-// The GEMM tiles (big: 256 rows, 128 with 8-bit codes; else 64) and the streaming kernel for
-// few rows per group (grouped_stream.hpp), on tiles of 16 row_tiles (1 or 2) rows, for the
-// sizes that it takes.
+// The streaming kernel for few rows per group (grouped_stream.hpp), for the sizes that it
+// takes, the GEMM (AWQ_GROUPED_GEMM...) and the choice among its tile shapes.
 bool grouped_stream_supported(int64_t weights, int64_t N, int64_t K, int group, int w_bit);
-hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, bool big, hipStream_t stream);
-hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, int row_tiles, hipStream_t stream);
-
-// AWQ_GROUPED_AUTO: by the mean rows per group (experts) or the rows (adapters).
-constexpr int64_t kSkinnyMeanRows = 16;
-constexpr int64_t kGemm64MeanRows = 96;
-constexpr int64_t kLoraGemmMinM = 512;
+hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, hipStream_t stream);
+// AWQ_GROUPED_AUTO streams up to these rows (mean per group of experts; adapters: all) and
+// takes the GEMM beyond: 64 experts x 4096 x 1024, 16 rows each 44 us and 55, 32 rows 67 and
+// 63; 8 x 22016 x 4096 gated 91 and 134, 149 and 149; adapters on 4096 x 4096, 64 rows 23 and
+// 31; on 11008 x 4096 33 and 33.
+constexpr int kSkinnyMeanRows = 16;
+constexpr int kLoraSkinnyRows = 64;
+int choose_grouped_gemm(const GroupedArgs& g, int mode, int w_bit);
+hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, int kernel, hipStream_t stream);
 
 // Adapters: H[i] = scale[a] X[i] A_a^T, a = ids[i]; rows without an adapter are left.
 hipError_t launch_lora_shrink(const uint16_t* X, int n, int64_t K, const uint16_t* A, const float* scale,

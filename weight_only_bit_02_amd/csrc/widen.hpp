@@ -1,5 +1,5 @@
 // Packed codes -> fp16 MFMA operands, shared by the GEMMs that widen their codes in
-// registers (gemm_wide.hip, grouped_gemm.hpp, grouped_skinny.hip).
+// registers (gemm_wide.hip, grouped_gemm.hpp, grouped_stream.hpp).
 #pragma once
 
 #include "common.hpp"

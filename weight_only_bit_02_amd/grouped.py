@@ -26,7 +26,7 @@ from .awq import GROUP, PackedLinear, alloc_packed, quantize_pack
 
 MAX_GROUPS = 512  # AWQ_MAX_GROUPS
 
-_GROUPED_KERNELS = {"auto": 0, "skinny": 1, "gemm64": 2, "gemm": 3}
+_GROUPED_KERNELS = {"auto": 0, "skinny": 1, "gemm64": 2, "gemm128": 3, "gemm256": 4, "gemm64k": 5}
 
 
 def _check(t, dtype, shape, name, device):
