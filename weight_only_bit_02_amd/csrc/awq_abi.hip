@@ -542,7 +542,7 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
   const int mode = gated ? awq::kGated : awq::kPlain;
   const bool streams = awq::grouped_stream_supported(groups, N, K, c.group_size, c.w_bit);
   if (kv == AWQ_GROUPED_AUTO)
-    kv = streams && n_rows <= kSkinnyMaxRows && n_rows <= (int64_t)awq::kSkinnyMeanRows * groups
+    kv = streams && n_rows <= kSkinnyMaxRows && n_rows <= (int64_t)awq::skinny_mean_rows(c.w_bit) * groups
              ? AWQ_GROUPED_SKINNY
              : awq::choose_grouped_gemm(g, mode, c.w_bit);
   if (kv == AWQ_GROUPED_SKINNY && streams) return hip_status(awq::launch_grouped_stream(g, mode, c.w_bit, st));

@@ -4,9 +4,9 @@
 namespace awq {
 
 #define AWQ_STREAM(B)                                                                                     \
-  void launch_stream##B##_plain(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream); \
-  void launch_stream##B##_gated(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream); \
-  void launch_stream##B##_lora(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream);
+  void launch_stream##B##_plain(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream); \
+  void launch_stream##B##_gated(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream); \
+  void launch_stream##B##_lora(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream);
 AWQ_STREAM(3)
 AWQ_STREAM(4)
 AWQ_STREAM(8)
@@ -22,17 +22,24 @@ hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, hipStream_t
   const int64_t outs = mode == kGated ? g.N / 2 : g.N;
   const int64_t parts = mode == kLora ? 1 : g.groups < g.n ? g.groups : g.n;
   const int64_t mt = (g.n + 15 * parts) / 16;  // the most row tiles
-  const int cols = stream_cols(w_bit) / (mode == kGated ? 2 : 1);
-  g.nt = (int)((outs + cols - 1) / cols);
   // the fewest waves that hold all of K: each item then costs the fewest sums
   const int64_t waves = (g.K / kGroup + kStreamSteps - 1) / kStreamSteps;
   const int s = waves <= 2 ? 2 : waves <= 4 ? 4 : 8;
-  const int64_t items = mt * g.nt, blocks = kStreamSlots / s;
-  const dim3 grid((unsigned)(items < blocks ? items : blocks));
+  const int64_t blocks = kStreamSlots / s;
+  auto chunks = [&](bool narrow) -> int64_t {
+    const int cols = stream_cols(w_bit, narrow) / (mode == kGated ? 2 : 1);
+    return (outs + cols - 1) / cols;
+  };
+  // items for half the blocks or fewer: narrower ones (4096 x 4096 with adapters, one row: 13.1 us
+  // with whole items, 11.2; with items for more blocks, 11008 rows of weights: 13.5 and 13.9)
+  const bool narrow = w_bit != 8 && mt * chunks(false) * 2 <= blocks;
+  g.nt = (int)chunks(narrow);
+  const int64_t items = mt * g.nt;
+  const dim3 grid((unsigned)(items < blocks ? (items + 7) / 8 * 8 : blocks));  // a multiple of the XCDs
   auto* const f = w_bit == 8   ? (mode == kPlain ? launch_stream8_plain : mode == kGated ? launch_stream8_gated : launch_stream8_lora)
                   : w_bit == 3 ? (mode == kPlain ? launch_stream3_plain : mode == kGated ? launch_stream3_gated : launch_stream3_lora)
                                : (mode == kPlain ? launch_stream4_plain : mode == kGated ? launch_stream4_gated : launch_stream4_lora);
-  f(g, s, grid, stream);
+  f(g, narrow, s, grid, stream);
   return hipGetLastError();
 }
 

@@ -47,7 +47,6 @@
 
 namespace awq {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define AWQ_INLINE __attribute__((always_inline))
 
@@ -55,9 +54,11 @@ constexpr int kStreamWaves = 8;     // S at most
 constexpr int kStreamSlots = 2048;  // resident waves: two per SIMD
 
 constexpr int kStreamSteps = 4;     // L
+constexpr int kStreamSplit = 64;    // chunks from which on each XCD takes an eighth of them
 
-// Columns of an item: 8-bit codes take twice the LDS.
-constexpr int stream_cols(int w_bit) { return w_bit == 8 ? 32 : 64; }
+// Columns of an item: 8-bit codes take twice the LDS; half where whole ones would leave blocks
+// without an item.
+constexpr int stream_cols(int w_bit, bool narrow) { return w_bit == 8 || narrow ? 32 : 64; }
 
 // Eight bytes at byte `at` of [p, p + bytes), bytes >= 8, at any alignment; those past the end
 // are not read: the load moves back, and the value is shifted when it is used (shifting it here
@@ -166,11 +167,15 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   const int64_t zbytes = (MODE == kLora ? 1 : g.groups) * N * zbw;
   const uint32_t magic = wide_magic();
 
-  // ---- this block's run of items (item = tile * nt + column chunk)
+  // ---- this block's run of items: row tiles by column chunks, tile after tile. XCD blockIdx % 8
+  // takes an eighth of the chunks (kStreamSplit or more), for all tiles, so that the tiles of
+  // one weight find it in its L2 (3 tiles of 8-bit 4096 x 4096, with adapters: 28 us without, 21).
   const int mt = MODE == kLora ? (g.n + BM - 1) / BM
                                : __builtin_amdgcn_readfirstlane(count_tiles<BM>(g.offsets, g.groups, g.n, lane));
-  const int64_t items = (int64_t)mt * nt;
-  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  const int xcds = nt >= kStreamSplit ? 8 : 1, xcd = blockIdx.x % xcds;
+  const int c0 = nt * xcd / xcds, c1 = nt * (xcd + 1) / xcds, nc = c1 - c0;
+  const int64_t items = (int64_t)mt * nc, slots = gridDim.x / xcds, slot = blockIdx.x / xcds;
+  const int64_t i0 = items * slot / slots, i1 = items * (slot + 1) / slots;
   if (i0 >= i1) return;  // uniform over the block
   int left = (int)(i1 - i0) * parts;  // positions still to be loaded
 
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   };
   auto step_of = [&](int part, int j) AWQ_INLINE -> int { return (part * S + wave) * L + j; };
 
-  StreamItem ld{(int)(i0 / nt), (int)(i0 % nt), 0, 0, 0};  // the position being loaded
+  StreamItem ld{(int)(i0 / nc), c0 + (int)(i0 % nc), 0, 0, 0};  // the position being loaded
   auto open_tile = [&]() AWQ_INLINE {
     const RowTile rt = MODE == kLora ? RowTile{0, ld.tile * BM, g.n - ld.tile * BM < BM ? g.n - ld.tile * BM : BM}
                                      : find_tile<BM>(g.offsets, g.groups, g.n, ld.tile, lane);
@@ -222,8 +227,8 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     if (--left <= 0) return;  // the last position's loads are repeated
     if (++ld.part < parts) return;
     ld.part = 0;
-    if (++ld.chunk < nt) return;
-    ld.chunk = 0;
+    if (++ld.chunk < c1) return;
+    ld.chunk = c0;
     ++ld.tile;
     open_tile();
   };
@@ -579,9 +584,9 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
 }
 
 // The variants that the launcher picks from: s waves.
-template <int MODE, int BITS, bool G128>
-void launch_stream_g(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
-  constexpr int R = stream_cols(BITS) / 16, L = kStreamSteps;
+template <int MODE, int BITS, bool G128, int R>
+void launch_stream_r(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
+  constexpr int L = kStreamSteps;
   if (s == 2)
     hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 2>), grid, dim3(128), 0, stream, g);
   else if (s == 4)
@@ -590,10 +595,17 @@ void launch_stream_g(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream)
     hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 8>), grid, dim3(512), 0, stream, g);
 }
 
+template <int MODE, int BITS, bool G128>
+void launch_stream_g(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
+  constexpr int R = stream_cols(BITS, false) / 16, kNarrow = stream_cols(BITS, true) / 16;
+  if (narrow) launch_stream_r<MODE, BITS, G128, kNarrow>(g, s, grid, stream);
+  else launch_stream_r<MODE, BITS, G128, R>(g, s, grid, stream);
+}
+
 template <int MODE, int BITS>
-void launch_stream_t(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
-  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, s, grid, stream);
-  else launch_stream_g<MODE, BITS, false>(g, s, grid, stream);
+void launch_stream_t(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
+  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, narrow, s, grid, stream);
+  else launch_stream_g<MODE, BITS, false>(g, narrow, s, grid, stream);
 }
 
 }  // namespace awq

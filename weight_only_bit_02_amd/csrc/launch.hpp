@@ -176,10 +176,10 @@ enum GroupedMode { kPlain = 0, kGated = 1, kLora = 2 };
 bool grouped_stream_supported(int64_t weights, int64_t N, int64_t K, int group, int w_bit);
 hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, hipStream_t stream);
 // AWQ_GROUPED_AUTO streams up to these rows (mean per group of experts; adapters: all) and
-// takes the GEMM beyond: 64 experts x 4096 x 1024, 16 rows each 44 us and 55, 32 rows 67 and
-// 63; 8 x 22016 x 4096 gated 91 and 134, 149 and 149; adapters on 4096 x 4096, 64 rows 23 and
-// 31; on 11008 x 4096 33 and 33.
-constexpr int kSkinnyMeanRows = 16;
+// takes the GEMM beyond. Streaming and the best GEMM, in us: 64 experts x 4096 x 1024, 24 rows
+// each 46 and 61, 32 rows 67 and 67; 8 x 22016 x 4096 gated 114 and 137, 170 and 155; 8-bit, 64 x
+// 2048 x 1152, 16 rows 44 and 42, 24 rows 55 and 44; adapters on 4096 x 4096, 64 rows 17 and 24.
+constexpr int skinny_mean_rows(int w_bit) { return w_bit == 4 ? 24 : 16; }
 constexpr int kLoraSkinnyRows = 64;
 int choose_grouped_gemm(const GroupedArgs& g, int mode, int w_bit);
 hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, int kernel, hipStream_t stream);

@@ -15,8 +15,8 @@
 //     (the lanes whose ids agree in every bit), so the order never depends on scheduling.
 //
 // Batches of up to kOneBlockPairs pairs run in one block and one launch. Larger ones take
-// two: the first writes each block's count per group, the second sums the counts of the
-// blocks before it (at most kMaxBlocks rows of E + 1 integers, from L2) and places its run.
+// two: the first writes each block's count per group, key by key, the second sums the counts of
+// the blocks before it (at most kMaxBlocks per key, from L2) and places its run.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
 constexpr int64_t kOneBlockTokens = 64;   // route: tokens that one block serves alone
 constexpr int64_t kOneBlockPairs = 8192;  // grouping: pairs that one block serves alone
-constexpr int64_t kMaxBlocks = 256;
+constexpr int64_t kMaxBlocks = 256;       // a multiple of a wave
 
 // Maximum over the wave (a scalar): row shifts, then the row broadcasts, then lane 63.
 __device__ __forceinline__ float wave_max(float v) {
@@ -68,7 +68,7 @@ __device__ __forceinline__ float logit(LT raw, bool& bad) {
 
 // Token t: lane j < top_k leaves with choice j's expert (or -1); weights and ids are written.
 template <typename LT, int V>
-__device__ __forceinline__ void choose(const LT* logits, int64_t ld, int64_t t, int E, int top_k,
+__device__ __forceinline__ int choose(const LT* logits, int64_t ld, int64_t t, int E, int top_k,
                                        bool renorm, float* weights, int32_t* ids, bool& bad,
                                        int lane) {
   constexpr float lowest = -__builtin_huge_valf();
@@ -119,6 +119,7 @@ __device__ __forceinline__ void choose(const LT* logits, int64_t ld, int64_t t, 
     weights[t * top_k + lane] = w;
     ids[t * top_k + lane] = id;
   }
+  return id;
 }
 
 // A group id as a key: itself, or `groups` for anything outside [0, groups).
@@ -155,14 +156,81 @@ __device__ __forceinline__ void block_exclusive(int* count, int n, int* part, in
   __syncthreads();
 }
 
-// Places pairs [p0, p1): next[w][key] (LDS) is the position of wave w's next pair of a key.
+// Runs of up to kThreads kHeld pairs: every thread holds its pairs' keys, so that they are read
+// once, and each wave counts its contiguous part of the run in order, in next[w][key] (LDS). A
+// pair's rank among its wave's pairs of the same key comes with the count: placing it takes the
+// positions of the waves' first pairs alone.
+constexpr int kHeld = 8;
+struct Held {
+  int key[kHeld], rank[kHeld];
+};
+__device__ __forceinline__ int64_t wave_part(int64_t n) {
+  return ((n + kWaves - 1) / kWaves + kWave - 1) / kWave * kWave;
+}
+// from: ids of the run, in global memory or LDS
+__device__ __forceinline__ void hold(Held& h, const int32_t* from, int n, int groups, int tid) {
+  const int part = (int)wave_part(n), w0 = (tid >> 6) * part;
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c) {
+    const int i = w0 + c * kWave + (tid & 63);
+    h.key[c] = c * kWave < part && i < n ? key_of(from[i], groups) : -1;
+  }
+}
+// next: cleared; ends with a barrier
+__device__ __forceinline__ void rank_held(Held& h, int n, int groups, int bits, int* next, int tid) {
+  const int part = (int)wave_part(n), lane = tid & 63;
+  int* const mine = next + (tid >> 6) * (groups + 1);
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c) {
+    const bool in = h.key[c] >= 0;
+    const uint64_t live = __ballot(in);
+    if (c * kWave < part && live) {
+      const uint64_t same = same_key(h.key[c], bits, live);
+      const int before = in ? mine[h.key[c]] : 0;
+      h.rank[c] = before + __popcll(same & below);
+      __builtin_amdgcn_wave_barrier();
+      if (in && (same & below) == 0) mine[h.key[c]] = before + __popcll(same);  // the first of its equals
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __syncthreads();
+}
+// next[w][key]: from the counts of the waves to the positions of their first pairs, given the
+// run's first positions; ends with a barrier
+__device__ __forceinline__ void wave_starts(int* next, const int* start, int keys, int tid) {
+  for (int k = tid; k < keys; k += kThreads) {
+    int at = start[k];
+    for (int w = 0; w < kWaves; ++w) {
+      const int c = next[w * keys + k];
+      next[w * keys + k] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void place_held(const Held& h, int64_t p0, int n, int groups, const int* next,
+                                           int32_t* order, int32_t* pos, int tid) {
+  const int part = (int)wave_part(n), w0 = (tid >> 6) * part;
+  const int* const mine = next + (tid >> 6) * (groups + 1);
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c)
+    if (h.key[c] >= 0) {
+      const int64_t p = p0 + w0 + c * kWave + (tid & 63);
+      const int at = mine[h.key[c]] + h.rank[c];
+      order[at] = (int32_t)p;
+      if (pos) pos[p] = at;
+    }
+}
+
+// The same for runs of any length, walked twice. Places pairs [p0, p1): next[w][key] (LDS) is the position of wave w's next pair of a key.
 // Counting, the sums over the waves and the placement all walk the pairs in order.
 // start[key] (LDS): the position of this block's first pair of the key.
 __device__ __forceinline__ void place(const int32_t* ids, int64_t p0, int64_t p1, int groups, int bits,
                                       int* next, const int* start, int32_t* order, int32_t* pos,
                                       int tid) {
   const int lane = tid & 63, wave = tid >> 6, keys = groups + 1;
-  const int64_t part = ((p1 - p0 + kWaves - 1) / kWaves + kWave - 1) / kWave * kWave;
+  const int64_t part = wave_part(p1 - p0);
   const int64_t w0 = p0 + wave * part < p1 ? p0 + wave * part : p1;
   const int64_t w1 = w0 + part < p1 ? w0 + part : p1;
   for (int i = tid; i < kWaves * keys; i += kThreads) next[i] = 0;
@@ -177,15 +245,7 @@ __device__ __forceinline__ void place(const int32_t* ids, int64_t p0, int64_t p1
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
-  for (int k = tid; k < keys; k += kThreads) {
-    int at = start[k];
-    for (int w = 0; w < kWaves; ++w) {
-      const int c = next[w * keys + k];
-      next[w * keys + k] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
+  wave_starts(next, start, keys, tid);
   for (int64_t p = w0; p < w1; p += kWave) {
     const bool in = p + lane < w1;
     const int key = in ? key_of(ids[p + lane], groups) : 0;
@@ -211,15 +271,28 @@ __device__ __forceinline__ void count_keys(const int32_t* ids, int64_t p0, int64
 }
 
 // LDS: [count: groups + 1][part: waves][next: waves (groups + 1)]
-__device__ __forceinline__ void sort_alone(const int32_t* ids, int64_t n, int groups, int bits, int* lds,
+constexpr int alone_ints(int groups) { return (groups + 1) * (kWaves + 1) + kWaves; }
+__device__ __forceinline__ void sort_alone(const int32_t* from, int n, int groups, int bits, int* lds,
                                            int32_t* offsets, int32_t* order, int32_t* pos, int tid) {
+  const int keys = groups + 1;
   int* const count = lds;
-  int* const part = count + groups + 1;
+  int* const part = count + keys;
   int* const next = part + kWaves;
-  count_keys(ids, 0, n, groups, count, tid);
-  block_exclusive(count, groups + 1, part, tid);
-  for (int k = tid; k <= groups; k += kThreads) offsets[k] = count[k];
-  place(ids, 0, n, groups, bits, next, count, order, pos, tid);
+  Held h;
+  hold(h, from, n, groups, tid);
+  for (int i = tid; i < kWaves * keys; i += kThreads) next[i] = 0;
+  __syncthreads();
+  rank_held(h, n, groups, bits, next, tid);
+  for (int k = tid; k < keys; k += kThreads) {
+    int all = 0;
+    for (int w = 0; w < kWaves; ++w) all += next[w * keys + k];
+    count[k] = all;
+  }
+  __syncthreads();
+  block_exclusive(count, keys, part, tid);
+  for (int k = tid; k < keys; k += kThreads) offsets[k] = count[k];
+  wave_starts(next, count, keys, tid);
+  place_held(h, 0, n, groups, next, order, pos, tid);
 }
 
 template <typename LT, int V, bool ALONE>
@@ -232,23 +305,32 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t t0 = blockIdx.x * per_block;
   const int64_t t1 = t0 + per_block < T ? t0 + per_block : T;
   bool bad = false;
-  for (int64_t t = t0 + wave; t < t1; t += kWaves)
-    choose<LT, V>(logits, ld, t, E, top_k, renorm, weights, ids, bad, lane);
-  if (flags && __ballot(bad) && lane == 0) atomicOr(flags, AWQ_FLAG_NONFINITE_INPUT);
-  __syncthreads();  // the block's ids are written
   if constexpr (ALONE) {
-    sort_alone(ids, T * top_k, E, bits, lds, offsets, order, pos, tid);
+    int* const held = lds + alone_ints(E);  // the ids
+    for (int64_t t = wave; t < T; t += kWaves) {
+      const int id = choose<LT, V>(logits, ld, t, E, top_k, renorm, weights, ids, bad, lane);
+      if (lane < top_k) held[t * top_k + lane] = id;
+    }
+    __syncthreads();
+    sort_alone(held, (int)T * top_k, E, bits, lds, offsets, order, pos, tid);
   } else {
-    count_keys(ids, t0 * top_k, t1 * top_k, E, lds, tid);
-    for (int k = tid; k <= E; k += kThreads) counts[(int64_t)blockIdx.x * (E + 1) + k] = lds[k];
+    for (int k = tid; k <= E; k += kThreads) lds[k] = 0;
+    __syncthreads();
+    for (int64_t t = t0 + wave; t < t1; t += kWaves) {
+      const int id = choose<LT, V>(logits, ld, t, E, top_k, renorm, weights, ids, bad, lane);
+      if (lane < top_k) atomicAdd(&lds[key_of(id, E)], 1);
+    }
+    __syncthreads();
+    for (int k = tid; k <= E; k += kThreads) counts[(int64_t)k * gridDim.x + blockIdx.x] = lds[k];
   }
+  if (flags && __ballot(bad) && lane == 0) atomicOr(flags, AWQ_FLAG_NONFINITE_INPUT);
 }
 
 __global__ void __launch_bounds__(kThreads)
     k_group_alone(const int32_t* ids, int64_t n, int groups, int bits, int32_t* offsets, int32_t* order,
                   int32_t* pos) {
   extern __shared__ int lds[];
-  sort_alone(ids, n, groups, bits, lds, offsets, order, pos, threadIdx.x);
+  sort_alone(ids, (int)n, groups, bits, lds, offsets, order, pos, threadIdx.x);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -257,7 +339,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t p0 = blockIdx.x * per_block, p1 = p0 + per_block < n ? p0 + per_block : n;
   count_keys(ids, p0, p1, groups, lds, threadIdx.x);
   for (int k = threadIdx.x; k <= groups; k += kThreads)
-    counts[(int64_t)blockIdx.x * (groups + 1) + k] = lds[k];
+    counts[(int64_t)k * gridDim.x + blockIdx.x] = lds[k];
 }
 
 // Second launch: every block sums the counts of all blocks (total) and of those before it.
@@ -272,30 +354,46 @@ __global__ void __launch_bounds__(kThreads)
   int* const part = start + keys;
   int* const next = part + kWaves;
   const int blocks = gridDim.x, me = blockIdx.x;
-  for (int i = tid; i < 2 * keys; i += kThreads) lds[i] = 0;
-  __syncthreads();
-  // threads as [slices][keys rounded up to a power of two]: integer sums, any order
-  int wide = 1;
-  while (wide < keys && wide < kThreads) wide <<= 1;
-  for (int k = tid & (wide - 1); k < keys; k += wide) {
+  const int64_t p0 = me * per_block, p1 = p0 + per_block < n ? p0 + per_block : n;
+  const bool held = per_block <= kThreads * kHeld;
+  Held h;
+  if (held) {
+    hold(h, ids + p0, (int)(p1 - p0), groups, tid);
+    for (int i = tid; i < kWaves * keys; i += kThreads) next[i] = 0;
+  }
+  // a wave sums a key's counts of all blocks and of those before this one
+  const int lane = tid & 63;
+#pragma unroll 4
+  for (int k = __builtin_amdgcn_readfirstlane(tid >> 6); k < keys; k += kWaves) {
     int all = 0, before = 0;
-    for (int b = tid / wide; b < blocks; b += kThreads / wide) {
-      const int c = counts[(int64_t)b * keys + k];
+#pragma unroll
+    for (int i = 0; i < kMaxBlocks / kWave; ++i) {
+      const int b = i * kWave + lane;
+      const int c = b < blocks ? counts[(int64_t)k * blocks + b] : 0;
       all += c;
       before += b < me ? c : 0;
     }
-    atomicAdd(&total[k], all);
-    atomicAdd(&start[k], before);
+    all = __builtin_amdgcn_readlane(wave_scan(all), 63);
+    before = __builtin_amdgcn_readlane(wave_scan(before), 63);
+    if (lane == 0) {
+      total[k] = all;
+      start[k] = before;
+    }
   }
   __syncthreads();
+  if (held) rank_held(h, (int)(p1 - p0), groups, bits, next, tid);
   block_exclusive(total, keys, part, tid);
   for (int k = tid; k < keys; k += kThreads) {
     start[k] += total[k];
     if (me == 0) offsets[k] = total[k];
   }
   __syncthreads();
-  const int64_t p0 = me * per_block, p1 = p0 + per_block < n ? p0 + per_block : n;
-  place(ids, p0, p1, groups, bits, next, start, order, pos, tid);
+  if (held) {
+    wave_starts(next, start, keys, tid);
+    place_held(h, p0, (int)(p1 - p0), groups, next, order, pos, tid);
+  } else {
+    place(ids, p0, p1, groups, bits, next, start, order, pos, tid);
+  }
 }
 
 int key_bits(int groups) {  // bits of the keys 0 .. groups
@@ -304,7 +402,7 @@ int key_bits(int groups) {  // bits of the keys 0 .. groups
   return b;
 }
 
-size_t alone_lds(int groups) { return ((size_t)(groups + 1) * (kWaves + 1) + kWaves) * 4; }
+size_t alone_lds(int groups, int ids) { return (size_t)(alone_ints(groups) + ids) * 4; }
 size_t place_lds(int groups) { return ((size_t)(groups + 1) * (kWaves + 2) + kWaves) * 4; }
 
 int64_t group_run(int64_t n) {  // pairs per block of a grouping in two launches
@@ -330,7 +428,7 @@ hipError_t launch_route_v(const void* logits, int64_t ld, int64_t T, int E, int 
                           int* counts, uint32_t* flags, hipStream_t stream) {
   const int bits = key_bits(E);
   if (T <= kOneBlockTokens) {
-    hipLaunchKernelGGL((k_route<LT, V, true>), dim3(1), dim3(kThreads), alone_lds(E), stream,
+    hipLaunchKernelGGL((k_route<LT, V, true>), dim3(1), dim3(kThreads), alone_lds(E, (int)T * top_k), stream,
                        (const LT*)logits, ld, T, T, E, top_k, renorm, bits, weights, ids, offsets, order,
                        pos, counts, flags);
     return hipGetLastError();
@@ -366,7 +464,7 @@ size_t group_rows_workspace(int64_t n, int groups) {
 hipError_t launch_group_rows(const int32_t* ids, int64_t n, int groups, int32_t* offsets,
                              int32_t* order, int32_t* pos, int* counts, hipStream_t stream) {
   if (n <= kOneBlockPairs) {
-    hipLaunchKernelGGL(k_group_alone, dim3(1), dim3(kThreads), alone_lds(groups), stream, ids, n, groups,
+    hipLaunchKernelGGL(k_group_alone, dim3(1), dim3(kThreads), alone_lds(groups, 0), stream, ids, n, groups,
                        key_bits(groups), offsets, order, pos);
     return hipGetLastError();
   }

@@ -4,8 +4,8 @@
 
 namespace awq {
 
-void launch_stream3_plain(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
-  launch_stream_t<kPlain, 3>(g, s, grid, stream);
+void launch_stream3_plain(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
+  launch_stream_t<kPlain, 3>(g, narrow, s, grid, stream);
 }
 
 }  // namespace awq

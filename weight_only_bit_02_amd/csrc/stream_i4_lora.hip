@@ -4,8 +4,8 @@
 
 namespace awq {
 
-void launch_stream4_lora(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
-  launch_stream_t<kLora, 4>(g, s, grid, stream);
+void launch_stream4_lora(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
+  launch_stream_t<kLora, 4>(g, narrow, s, grid, stream);
 }
 
 }  // namespace awq
