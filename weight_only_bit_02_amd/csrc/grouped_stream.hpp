@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   const int64_t items = (int64_t)mt * nc, slots = gridDim.x / xcds, slot = blockIdx.x / xcds;
   const int64_t i0 = items * slot / slots, i1 = items * (slot + 1) / slots;
   if (i0 >= i1) return;  // uniform over the block
-  int left = (int)(i1 - i0) * parts;  // positions still to be loaded
+  int todo = (int)(i1 - i0) * parts;  // positions
 
   // ---- addresses: a lane's offsets in the weight rows, and the rest uniform
   const uint32_t rowq = (uint32_t)(words * 4);
@@ -224,7 +224,6 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     codes = buffer_at(g.qweight + e * N * words);
   };
   auto next = [&]() AWQ_INLINE {
-    if (--left <= 0) return;  // the last position's loads are repeated
     if (++ld.part < parts) return;
     ld.part = 0;
     if (++ld.chunk < c1) return;
@@ -253,8 +252,11 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   // are those of the other buffers, so vmcnt(their number) covers buffer b whatever else was
   // sent in between; the LDS reads end before the block does.
   constexpr int kLater = (NB - 1) * R * 2;
-  auto take_codes = [&](int b, uint32_t (&w)[H][R][BITS]) AWQ_INLINE {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
+  auto take_codes = [&](int b, bool more, uint32_t (&w)[H][R][BITS]) AWQ_INLINE {
+    if (more)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
+    else  // nothing is sent behind the last position's
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -428,20 +430,20 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   // terms start the accumulators, while the item's codes are on their way.
   auto adapters = [&](const StreamItem& it) AWQ_INLINE {
     int src, id;
-    bool todo;
+    bool open;
     const int r = c16;
     src = source(it.row0 + (r < it.rows ? r : it.rows - 1));
     id = r < it.rows ? g.ids[src] : -1;
-    todo = (unsigned)id < (unsigned)g.groups;
+    open = (unsigned)id < (unsigned)g.groups;
     const int blocks = (g.rank + kLoraBlock - 1) / kLoraBlock;
     // the next adapter whose turn is this wave's, -1 after the last
     int turn = 0;
     auto pick = [&]() AWQ_INLINE -> int {
       while (true) {
-        const uint64_t m = __ballot(todo);
+        const uint64_t m = __ballot(open);
         if (!m) return -1;
         const int ad = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)m) - 1);
-        todo = todo && id != ad;
+        open = open && id != ad;
         const bool hit = turn == wave;
         turn = turn + 1 < S ? turn + 1 : 0;
         if (hit) return ad;
@@ -536,7 +538,6 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   };
 
   clear();
-  int todo = left;
   open_tile();
   StreamItem it = ld;
   ScaleZero q;
@@ -545,16 +546,19 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   for (int i = 0; i < L / H; ++i) load_codes(i, i);
   load_x(it);
   while (true) {
-    next();  // ld is a position ahead of it
+    const bool more = todo > 1;
     Fetched f;
     fetch_all(f, q);
-    load_scales(q);
+    if (more) {
+      next();  // ld is a position ahead of it
+      load_scales(q);
+    }
     if (MODE == kLora && it.part == 0) adapters(it);
 #pragma unroll
     for (int i = 0; i < L / H; ++i) {
       uint32_t w[H][R][BITS];
-      take_codes(i, w);
-      load_codes(i, i);
+      take_codes(i, more, w);
+      if (more) load_codes(i, i);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const int s = step_of(it.part, H * i + h);
@@ -580,7 +584,6 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     it = ld;
     if (parts > 1 || it.tile != tile) load_x(it);
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the last position's loads were repeated: LDS stays theirs until then
 }
 
 // The variants that the launcher picks from: s waves.
