@@ -79,14 +79,23 @@ def _workspace(workspace, nbytes, device):
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
+def _stream_of(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle without a Stream object around it (0.1 us instead of 2.7, of the 8 that a call takes).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _launch(name, device, *args):
     """Calls an entry point on the device's current stream, whatever device is current."""
     fn = getattr(_abi.load(), name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, _current_stream(index))
     if status:
         _abi.check(name, status)
 
