@@ -62,7 +62,7 @@ int choose_grouped_gemm(const GroupedArgs& g, int mode, int w_bit) {
                         : rows <= 32  ? 1.05
                         : rows <= 64  ? 1.3
                         : rows <= 128 ? 1.85
-                                      : 3.0;
+                                      : 2.8;
     const double steps = __builtin_ceil((double)g.K / kGK / s.k_waves);
     const double rest = 3 + (mode == kLora && s.k_waves == 1 ? 0.1 * rows : 1);
     const double t = rounds * (step * steps + rest);

@@ -17,6 +17,9 @@
 // bank conflicts. A tile with fewer rows runs a body with fewer row tiles (a power of two), so
 // a group's last tile costs the matrix work of the rows it has.
 //
+// A step is eight slices of 16 channels. While a slice is multiplied, the next one is read and
+// widened between the products, across the barrier too: it stands before the last slice.
+//
 // One barrier per step, with a wait of its own for the DMAs of the step that begins
 // (__syncthreads would wait for those of all steps). The DMAs are written as instructions: of
 // the builtin's the compiler waits for every one in flight before each read of LDS.
@@ -272,50 +275,43 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) acc[a][b] = f32x16w{};
 
-    // Share i of 4 of this wave's step `step` into buffer c, if there is such a step.
-    constexpr int kA4 = (kAT + 3) / 4, kB4 = (kBT + 3) / 4;
+    // A slice's products go in kGroups groups of four (RT > 1). Share i of kShares of this wave's
+    // DMAs of step `step` into buffer c, if there is such a step, at every kEvery-th group. 256
+    // rows send one or two per group (more at once fill the address units' queue, and the products
+    // behind them wait: 256 rows x 4096 x 4096 with adapters 136 us in two shares, 122 so); fewer
+    // rows are shorter of time than of issue slots and send two halves early (128 rows 73 and 76).
+    constexpr int kGroups = RT >= 4 ? RT / 2 : 1, kSends = kAT + kBT;
+    constexpr int kShares = RT == 8 ? 6 * kGroups : 2, kEvery = RT == 8 ? 1 : 2 * kGroups;
     auto send = [&](auto c, int step, int i) __attribute__((always_inline)) {
       if (step >= nsteps) return;
       const uint32_t at = (uint32_t)(step * KW + kw);
       uint4* const dst = ring + decltype(c)::value * kBuf;
 #pragma unroll
-      for (int k = i * kA4; k < (i + 1) * kA4 && k < kAT; ++k)
-        dma16_own(X, &dst[(part * kAT + k) * 64], aoff[k], at * 256);
-#pragma unroll
-      for (int k = i * kB4; k < (i + 1) * kB4 && k < kBT; ++k)
-        dma16_own(W, &dst[BM * 16 + (part * kBT + k) * 64], boff[k], at * (kQ * 16));
-    };
-    ScaleZero sz[NS];
-    auto prologue = [&](auto c) __attribute__((always_inline)) {
-      constexpr int b = decltype(c)::value;
-      if constexpr (b < NS - 1) {
-        load_sz(sz[b], b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) send(c, b, i);
+      for (int k = i * kSends / kShares; k < (i + 1) * kSends / kShares; ++k) {
+        if (k < kAT)
+          dma16_own(X, &dst[(part * kAT + k) * 64], aoff[k], at * 256);
+        else
+          dma16_own(W, &dst[BM * 16 + (part * kBT + k - kAT) * 64], boff[k - kAT], at * (kQ * 16));
       }
     };
-    prologue(std::integral_constant<int, 0>{});
-    prologue(std::integral_constant<int, 1>{});
-    prologue(std::integral_constant<int, 2>{});
-    prologue(std::integral_constant<int, 3>{});
-
-    // One K step from buffer C; the step NS - 1 ahead goes into the buffer of the step before.
-    auto body = [&](auto bufc, int step) __attribute__((always_inline)) {
-      constexpr int C = decltype(bufc)::value, F = (C + NS - 1) % NS;
-      using Free = std::integral_constant<int, F>;
-      // all but the DMAs of the NS - 2 steps after this one have landed (other loads in between
-      // only make the wait longer) and the last step's reads are done, in every wave of the ring
+    // Step `step`'s data has landed: all but the DMAs of the NS - 2 steps after it (other loads in
+    // between only make the wait longer), in every wave of the ring, and the reads so far are done.
+    auto arrive = [&](int step) __attribute__((always_inline)) {
       if (step + NS - 2 < nsteps)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * (kAT + kBT)) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * kSends) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       if constexpr (KW == 1) asm volatile("s_barrier" ::: "memory");
-      const uint4* ab = ring + C * kBuf;
-      const uint4* bb = ab + BM * 16;
-      const ScaleZero& cur = sz[C];
-      load_sz(sz[F], step + NS - 1);
-      __builtin_amdgcn_sched_barrier(0);  // keep the scale loads at the top of the step
-      half2w zz[2][kZ], zz64[2][kZ], s2[2][kZ];
+    };
+
+    // State of a step: zeros and scales of the lane's columns, widened to pairs; its code words, per
+    // column: 4- and 8-bit, the quarters kQ / 2 kh ..; 3-bit, low-plane words 4 kh .. (quarter kh)
+    // and high-plane words 8 + 2 kh, 9 + 2 kh
+    constexpr int kQL = BITS == 3 ? 1 : kQ / 2;
+    half2w zz[2][kZ], zz64[2][kZ], s2[2][kZ];
+    uint4 bq[2][kQL];
+    uint2 bh[2];
+    auto open_step = [&](const ScaleZero& cur, const uint4* bb, int step) __attribute__((always_inline)) {
       const int hi = g64 ? kh : (step * KW + kw) & 1;  // zero nibble: group of 128 (step) or 64 (2 step + kh)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -331,11 +327,6 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
           zz64[b][i] = -__builtin_bit_cast(half2w, z64 | (z64 << 16));
           s2[b][i] = __builtin_bit_cast(half2w, cur.sc[b][i] | (cur.sc[b][i] << 16));
         }
-      // this lane's code words of the step, per column: 4- and 8-bit, the quarters kQ / 2 kh ..;
-      // 3-bit, low-plane words 4 kh .. (quarter kh) and high-plane words 8 + 2 kh, 9 + 2 kh
-      constexpr int kQL = BITS == 3 ? 1 : kQ / 2;
-      uint4 bq[2][kQL];
-      uint2 bh[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int col = part * 64 + b * 32 + m32;
@@ -348,54 +339,97 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
           for (int h = 0; h < kQL; ++h) bq[b][h] = bb[(kQL * kh + h) * BN + col];
         }
       }
-      auto frags = [&](int s, half8w (&A)[RT], half8w (&B)[2]) __attribute__((always_inline)) {
-        const int c = kh * 8 + s;
-        const int zi = G32 ? s >> 2 : 0;  // slices 0-3 lie in the half's first 32 channels
-#pragma unroll
-        for (int a = 0; a < RT; ++a) {
-          const int r = a * 32 + m32;
-          A[a] = __builtin_bit_cast(half8w, ab[r * 16 + (c ^ (r & 15))]);
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if constexpr (BITS == 8) {
-            const uint4 q = bq[b][s >> 1];  // slice s: words 2 s, 2 s + 1 of the lane half's 16
-            B[b] = (s & 1) ? widen_word8(q.z, q.w, zz[b][zi], s2[b][zi], magic8)
-                           : widen_word8(q.x, q.y, zz[b][zi], s2[b][zi], magic8);
-          } else if constexpr (BITS == 3) {
-            // slice s = channel pairs 4 s .. 4 s + 3 of the half: low word s / 2 (fields
-            // 4 (s % 2) ..), high word s / 4 (bits 4 (s % 4) ..)
-            const uint4 q = bq[b][0];
-            const uint32_t lo = (s >> 1) == 0 ? q.x : (s >> 1) == 1 ? q.y : (s >> 1) == 2 ? q.z : q.w;
-            const uint32_t hiw = (s >> 2) ? bh[b].y : bh[b].x;
-            B[b] = widen_word3(lo, hiw, 4 * (s & 1), 4 * (s & 3), zz[b][zi], s2[b][zi], magic);
-          } else {
-            const uint4 q = bq[b][s >> 2];
-            const uint32_t w = (s & 3) == 0 ? q.x : (s & 3) == 1 ? q.y : (s & 3) == 2 ? q.z : q.w;
-            B[b] = widen_word(w, zz[b][zi], zz64[b][zi], s2[b][zi], magic);
-          }
-        }
-      };
-      half8w A0[RT], B0[2], A1[RT], B1[2];
-      frags(0, A0, B0);
-#pragma unroll
-      for (int s = 0; s < kGK / 16; s += 2) {
-        __builtin_amdgcn_sched_barrier(0);
-        send(Free{}, step + NS - 1, s >> 1);  // a quarter of the transfers
-        __builtin_amdgcn_sched_barrier(0);
-        frags(s + 1, A1, B1);
-#pragma unroll
-        for (int a = 0; a < RT; ++a)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A0[a], B0[b], acc[a][b], 0, 0, 0);
-        if (s + 2 < kGK / 16) frags(s + 2, A0, B0);
-#pragma unroll
-        for (int a = 0; a < RT; ++a)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A1[a], B1[b], acc[a][b], 0, 0, 0);
+    };
+    auto rows_of = [&](const uint4* ab, int s, int a) __attribute__((always_inline)) -> half8w {
+      const int r = a * 32 + m32;
+      return __builtin_bit_cast(half8w, ab[r * 16 + ((kh * 8 + s) ^ (r & 15))]);
+    };
+    auto columns_of = [&](int s, int b) __attribute__((always_inline)) -> half8w {
+      const int zi = G32 ? s >> 2 : 0;  // slices 0-3 lie in the half's first 32 channels
+      if constexpr (BITS == 8) {
+        const uint4 q = bq[b][s >> 1];  // slice s: words 2 s, 2 s + 1 of the lane half's 16
+        return (s & 1) ? widen_word8(q.z, q.w, zz[b][zi], s2[b][zi], magic8)
+                       : widen_word8(q.x, q.y, zz[b][zi], s2[b][zi], magic8);
+      } else if constexpr (BITS == 3) {
+        // slice s = channel pairs 4 s .. 4 s + 3 of the half: low word s / 2 (fields
+        // 4 (s % 2) ..), high word s / 4 (bits 4 (s % 4) ..)
+        const uint4 q = bq[b][0];
+        const uint32_t lo = (s >> 1) == 0 ? q.x : (s >> 1) == 1 ? q.y : (s >> 1) == 2 ? q.z : q.w;
+        const uint32_t hiw = (s >> 2) ? bh[b].y : bh[b].x;
+        return widen_word3(lo, hiw, 4 * (s & 1), 4 * (s & 3), zz[b][zi], s2[b][zi], magic);
+      } else {
+        const uint4 q = bq[b][s >> 2];
+        const uint32_t w = (s & 3) == 0 ? q.x : (s & 3) == 1 ? q.y : (s & 3) == 2 ? q.z : q.w;
+        return widen_word(w, zz[b][zi], zz64[b][zi], s2[b][zi], magic);
       }
+    };
+    // One slice, from group `at` of the step on: the products of A and B, and between them slice ns
+    // of the step at ab into nA and nB, and the shares of the DMAs of step `step` into buffer c. (Left to itself the compiler
+    // widens in one piece while the matrix cores wait.)
+    auto slice = [&](const half8w (&A)[RT], const half8w (&B)[2], half8w (&nA)[RT], half8w (&nB)[2],
+                     const uint4* ab, int ns, auto c, int step, int at) __attribute__((always_inline)) {
+      constexpr int kR = RT / kGroups, kV = BITS == 3 ? 9 : 6;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        if ((at + q) % kEvery == 0 && (at + q) / kEvery < kShares) send(c, step, (at + q) / kEvery);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int a = q * kR; a < (q + 1) * kR; ++a) nA[a] = rows_of(ab, ns, a);
+        if (q == 0) nB[0] = columns_of(ns, 0);
+        if (q == kGroups / 2) nB[1] = columns_of(ns, 1);
+#pragma unroll
+        for (int a = q * kR; a < (q + 1) * kR; ++a)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[a], B[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * kR; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
+          if (i % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+          __builtin_amdgcn_sched_group_barrier(0x002, kGroups > 1 ? kV : 2 * kV, 0);  // VALU
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+    ScaleZero sz[NS];
+    half8w A0[RT], B0[2], A1[RT], B1[2];
+    auto prologue = [&](auto c) __attribute__((always_inline)) {
+      constexpr int b = decltype(c)::value;
+      if constexpr (b < NS) load_sz(sz[b], b);
+      if constexpr (b < NS - 1) {
+#pragma unroll
+        for (int i = 0; i < kShares; ++i) send(c, b, i);
+      }
+    };
+    prologue(std::integral_constant<int, 0>{});
+    prologue(std::integral_constant<int, 1>{});
+    prologue(std::integral_constant<int, 2>{});
+    prologue(std::integral_constant<int, 3>{});
+    prologue(std::integral_constant<int, 4>{});
+    arrive(0);
+    open_step(sz[0], ring + BM * 16, 0);
+#pragma unroll
+    for (int a = 0; a < RT; ++a) A0[a] = rows_of(ring, 0, a);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) B0[b] = columns_of(0, b);
+
+    // One K step from buffer C, whose first slice is in registers; the step NS - 1 ahead goes into
+    // the buffer of the step before. Before the last slice's products the next step is opened.
+    auto body = [&](auto bufc, int step) __attribute__((always_inline)) {
+      constexpr int C = decltype(bufc)::value, F = (C + NS - 1) % NS, N1 = (C + 1) % NS;
+      const uint4* const ab = ring + C * kBuf;
+      constexpr std::integral_constant<int, F> free;
+#pragma unroll
+      for (int s = 0; s < kGK / 16 - 2; s += 2) {
+        slice(A0, B0, A1, B1, ab, s + 1, free, step + NS - 1, s * kGroups);
+        slice(A1, B1, A0, B0, ab, s + 2, free, step + NS - 1, (s + 1) * kGroups);
+      }
+      slice(A0, B0, A1, B1, ab, kGK / 16 - 1, free, step + NS - 1, 6 * kGroups);
+      arrive(step + 1);  // (past the last: nothing is in flight, and what is opened is not used)
+      load_sz(sz[C], step + NS);
+      open_step(sz[N1], ring + N1 * kBuf + BM * 16, step + 1);
+      slice(A1, B1, A0, B0, ring + N1 * kBuf, 0, free, nsteps, 7 * kGroups);
     };
     int step = 0;
     auto at = [&](auto c) __attribute__((always_inline)) {
