@@ -12,10 +12,10 @@
 // per tile. Both operands go global -> LDS by 16-byte DMA, up to NS - 1 steps ahead in a ring
 // of NS buffers that fills LDS (a step of a 64-row tile is multiplied in a quarter of the time
 // that its operands take to arrive: with two buffers 256 x 4096 x 4096 took 64 us, a step each
-// memory latency). A's DMA takes a row address per lane, so gathering costs nothing. A row's
-// 16 chunks are stored in slots c ^ (row % 16) and codes quarter-major: both are read without
-// bank conflicts. A tile with fewer rows runs a body with fewer row tiles (a power of two), so
-// a group's last tile costs the matrix work of the rows it has.
+// memory latency; with five 46). A's DMA takes a row address per lane, so gathering costs
+// nothing. A row's 16 chunks are stored in slots c ^ (row % 16) and codes quarter-major: both
+// are read without bank conflicts. A tile with fewer rows runs a body with fewer row tiles (a
+// power of two), so a group's last tile costs the matrix work of the rows it has.
 //
 // A step is eight slices of 16 channels. While a slice is multiplied, the next one is read and
 // widened between the products, across the barrier too: it stands before the last slice.
@@ -25,15 +25,28 @@
 // the builtin's the compiler waits for every one in flight before each read of LDS.
 //
 // RTM = 8 (not with 8-bit codes: LDS holds no more) serves large groups, 4 middling ones or
-// grids that would leave CUs idle, 2 small ones.
+// grids that would leave CUs idle, 2 small ones. KW = 4: 64 columns, K steps dealt to the four
+// waves, each with a ring of its own and no barrier, sums joined in LDS in the waves' order: four
+// times the blocks for batches whose tiles would leave the chip idle, at four times A's traffic
+// (64 rows x 4096 x 4096 with adapters 61 us -> 24). grouped_gemm.hip picks.
 //
-// Operand values and their order along K are those of the 256-row GEMM, so an expert's rows
-// equal the plain linear's bit for bit where that runs its GEMM.
+// What bounds it: large groups, the issue of one wave per SIMD (128 products of 32 cycles and
+// about 590 other instructions of 4 a step) and the chip's power: 8 experts x 22016 x 4096 gated,
+// 8192 rows, 1534 us, 963 TFLOP/s (a library fp16 product of 8192^3 reaches 1323). Middling
+// groups, the widening, whose cost does not depend on the rows. K of few steps, a tile's start:
+// offsets, row indices, first operands, 4 to 5 us before the first product.
+//
+// Operand values ((q - z) sc rounded to fp16 once) and, for KW = 1, their order along K are those
+// of the 256-row GEMM, so an expert's rows equal the plain linear's bit for bit where that runs
+// its GEMM. The rounding costs 2^-12 relative per weight at most, some 1.8e-4 of a sum of many
+// random terms, beside 2.1e-4 of the output's own rounding; the gated form, which has it in both
+// factors, comes to 3.3e-4 where exact weights give 2.1e-4. (Scaling the sums in fp32 instead, as
+// grouped_stream.hpp does, takes a second set of sums: 256 rows have no registers for it.)
 //
 // Adapters (MODE kLora): the rows of one batch, optionally through `order` (then Y is
-// scattered back through it). After the K loop each 32-row tile adds, for every adapter
-// among its rows, H B_a^T (H = scale X A_a^T from the first product's kernel, as fp16 hi
-// + lo under a power of two), rows of other adapters masked.
+// scattered back through it). After the K loop the rows' adapters are walked one by one, H B_a^T
+// (H = scale X A_a^T from the first product's kernel, as fp16 hi + lo under a power of two) is
+// added to their own rows, and the next adapter's B is on its way meanwhile.
 #pragma once
 
 #include <type_traits>

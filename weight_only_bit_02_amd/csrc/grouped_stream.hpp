@@ -35,6 +35,12 @@
 //   - A chunk that would pass the last weight row starts earlier instead and computes some
 //     columns twice, to the same values.
 //
+// What bounds it: the widening and the stream together; large launches reach three quarters of
+// what a copy reaches. 64 experts x 4096 x 1024, 384 rows: 33 us, 4.3 TB/s (without the
+// multiplications 30, without the loads 28); 8 experts x 22016 x 4096 gated, 64 rows: 78 us, 4.7
+// TB/s; 8 experts x 2048 x 2048 gated, a row each: 9 us, of which the chain offsets, row, first
+// codes, sums is most. 3-bit codes cost more instructions per byte: 64 x 2048 x 2048, 512 rows, 35 us.
+//
 // Gated: tiles 0 .. R / 2 - 1 are gate rows, the rest their up rows, so a lane's sums hold
 // both and the epilogue needs no exchange. Adapters: as in grouped_gemm.hpp; the waves share
 // the adapters among a tile's rows.

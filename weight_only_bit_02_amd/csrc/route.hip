@@ -17,6 +17,9 @@
 // Batches of up to kOneBlockPairs pairs run in one block and one launch. Larger ones take
 // two: the first writes each block's count per group, key by key, the second sums the counts of
 // the blocks before it (at most kMaxBlocks per key, from L2) and places its run.
+//
+// Bound by latency: one token, 8 of 64 experts: 5.2 us; 8191 tokens, 8 of 128: 9.3 + 8.7 us (the
+// choices' chain of maxima; the counts of 256 blocks); 2048 rows by 32 adapters: 4.9 us.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
