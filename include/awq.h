@@ -400,7 +400,9 @@ typedef enum awq_grouped_kernel {
  *            as awq_quantize_pack writes it (packing the stacked [groups N][K] does)
  *   Y        fp16 [n_rows][N] out, in group order; rows from offsets[groups] on are left
  *            as they were
- *   1 <= n_rows < 2^30; x_rows K <= 2^31, one weight's codes below 4 GiB. Formats, flags and accuracy as awq_linear_w4a16.
+ *   1 <= n_rows < 2^30, x_rows K <= 2^31, one weight's codes below 4 GiB, (n_rows / 64 +
+ *   groups + 1) (N / 128 + 1) < 2^24 (GEMM64K: n_rows / 32, N / 32); else BAD_SHAPE. Formats,
+ *   flags and accuracy as awq_linear_w4a16.
  *   _gated_silu: each weight is a gate|up pair (N even), Y fp16 [n_rows][N/2], as
  *   awq_linear_w4a16_gated_silu.
  */
@@ -426,7 +428,8 @@ awq_status awq_linear_w4a16_grouped_gated_silu(const void* X, int64_t x_rows,
  *   P fp16 [T top_k][N] (group order); weights fp32 [T][top_k], pos int32 [T top_k] and
  *   offsets int32 [groups + 1] as awq_moe_route writes them; add fp16 [T][N] or NULL (a
  *   shared expert, the residual); Y fp16 [T][N] out, may equal add.
- *   1 <= T, 1 <= top_k <= AWQ_MAX_TOP_K, T top_k < 2^30, 1 <= N < 2^31, T N < 2^37.
+ *   1 <= T, 1 <= top_k <= AWQ_MAX_TOP_K, T top_k < 2^30, 1 <= N < 2^31, T N < 2^35
+ *   (2^32 where N is no multiple of 8).
  */
 awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* pos,
                            const int32_t* offsets, int32_t groups, int64_t T, int32_t top_k,
@@ -440,15 +443,15 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
  *   X fp16 [M][K], packed weight and Y fp16 [M][N] as awq_linear_w4a16
  *   A fp16 [adapters][rank][K], B fp16 [adapters][N][rank], lora_scale fp32 [adapters];
  *   rank a multiple of 8 up to AWQ_MAX_LORA_RANK (smaller adapters padded with zero rows
- *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; M >= 1, M K <= 2^31, codes below
- *   4 GiB
+ *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; M >= 1, M K and rank K
+ *   <= 2^31, codes below 4 GiB, (M / 64 + 2) (N / 128 + 1) < 2^24 (GEMM64K: M / 32, N / 32)
  *   ids      int32 [M]
  *   order    int32 [M] or NULL: a permutation of the rows that brings those of one adapter
  *            together (awq_group_rows); it changes the speed of large mixed batches only
  *   workspace device scratch of awq_linear_w4a16_lora_workspace_size(M, rank) bytes,
- *            16-byte aligned (X A^T in fp32)
+ *            16-byte aligned (X A^T)
  *   flags    NONFINITE_INPUT: an Inf or NaN in X, the group scales, A or B
- *   X A^T is accumulated and kept in fp32; for the second product its rows are split into
+ *   X A^T is accumulated in fp32; for the second product its rows are split into
  *   fp16 hi + lo after scaling by a power of two (22 significant bits).
  */
 size_t awq_linear_w4a16_lora_workspace_size(int64_t M, int32_t rank);

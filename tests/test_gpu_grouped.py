@@ -238,3 +238,21 @@ def test_combine_in_place_and_wrong_positions():
     assert not awq.moe_combine(P, w, g).any()
     g.pos.fill_(-4)
     assert not awq.moe_combine(P, w, g).any()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("w_bit,group", [(4, 128), (4, 32), (8, 64), (3, 128)])
+@pytest.mark.parametrize("K", [128, 256, 640, 1664, 4480])
+def test_numbers_of_k_steps(K, w_bit, group, kernel):
+    """From a single K step, fewer than the waves and buffers that share them, to several rounds."""
+    w, Wd = _experts(4, 72, K, group, w_bit, seed=K)
+    _run(w, Wd, [5, 0, 33, 70], False, kernel, None, 3, seed=K + 1)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("w_bit,K", [(4, 128), (4, 640), (8, 384), (3, 256)])
+@pytest.mark.parametrize("kernel", ["skinny", "gemm64k", "auto"])
+def test_many_column_chunks(kernel, w_bit, K, gated):
+    """Enough columns that every XCD takes its share of the chunks, the last one partly filled."""
+    w, Wd = _experts(3, 4216, K, 128, w_bit, seed=40 + w_bit)
+    _run(w, Wd, [17, 0, 40], gated, kernel, 2, 2, seed=41)

@@ -159,3 +159,11 @@ def test_flags():
         args[i] = t.copy()
         args[i].reshape(-1)[-1] = np.nan
         assert flag(*args) == 1
+
+
+@pytest.mark.parametrize("w_bit", [4, 8, 3])
+@pytest.mark.parametrize("M", [1, 16, 50, 64, 65, 200, 600])
+def test_wide_weights(M, w_bit):
+    """Many column chunks; every kernel that the rows of a batch lead to."""
+    case = _case(4216, 384, 5, 24, 128, w_bit, seed=50 + M)
+    _check(case, si.activations(M, 384, offset=M), _ids("mixed", M, 5, M), "auto")

@@ -125,3 +125,16 @@ def test_route_runs_are_identical():
     a, b = awq.moe_route(x, 8), awq.moe_route(x, 8)
     for s, t in ((a.weights, b.weights), (a.ids, b.ids), (a.groups.order, b.groups.order)):
         assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("groups", [3, 400])
+def test_group_rows_of_a_very_large_batch(groups):
+    """More rows per block than its threads hold at once."""
+    n = 2_200_003
+    ids = np.random.default_rng(groups).integers(-1, groups + 1, n).astype(np.int32)
+    _check_groups(awq.group_rows(to_dev(ids), groups), ids, groups)
+
+
+def test_route_of_a_very_large_batch():
+    x = np.random.default_rng(1).standard_normal((70001, 40)).astype(np.float32)
+    _check_route(_route(to_dev(x), 32, True), x, 32, True, 40)

@@ -113,6 +113,24 @@ def test_lora(lib):
     assert call(cfg=C.byref(_abi.config(w_bit=2))) == UNSUPPORTED
 
 
+def test_limits_of_grids_and_offsets(lib):
+    def linear(n, N, K, kernel):
+        return lib.awq_linear_w4a16_grouped(FAKE, n, FAKE, None, n, 1, 4, FAKE, FAKE, FAKE, N, K, None, FAKE, None, kernel,
+                                            None)
+    assert linear(1 << 22, 1 << 20, 128, 0) == SHAPE              # 2^29 tiles
+    assert linear(1 << 20, 1 << 16, 128, 5) == SHAPE              # 2^26 of the narrowest ones
+
+    def lora(M, N, K, rank):
+        return lib.awq_linear_w4a16_lora(FAKE, M, FAKE, FAKE, FAKE, N, K, None, FAKE, FAKE, FAKE, 2, rank, FAKE, None, FAKE,
+                                         FAKE, 1 << 40, None, 0, None)
+    assert lora(1, 8, 1 << 26, 64) == SHAPE                       # one adapter's A of 2^32 values
+    assert lora(1 << 23, 1 << 20, 128, 8) == SHAPE
+
+    def combine(T, N):
+        return lib.awq_moe_combine(FAKE, FAKE, FAKE, FAKE, 4, T, 2, N, None, FAKE, None)
+    assert combine(1 << 20, (1 << 12) + 1) == SHAPE and combine(1 << 20, 1 << 15) == SHAPE
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     x = torch.zeros(4, 8, dtype=torch.float16)
     ids = torch.zeros(4, dtype=torch.int32)

@@ -97,10 +97,11 @@ bool good_rank(int32_t r) { return r >= 8 && r <= AWQ_MAX_LORA_RANK && r % 8 == 
 bool good_workspace(const void* p, size_t have, size_t need) {
   return need == 0 || (p && have >= need && aligned16(p));
 }
-// Row tiles of 32 rows of the GEMM choices.
-// Every tiling's block count stays in 31 bits (the narrowest: 64 rows x 128 outputs).
-bool grouped_grid_ok(int64_t n, int64_t N, int64_t groups) {
-  return (n / 64 + groups + 1) < ((int64_t)1 << 30) / (N / 128 + 1);
+// A launch has fewer than 2^32 threads: fewer than 2^24 blocks of 256. The narrowest tiles are 64
+// rows x 128 outputs, of GEMM64K 32 x 32 (which AUTO takes for few blocks only).
+bool grouped_grid_ok(int64_t n, int64_t N, int64_t groups, int kernel) {
+  const int64_t rows = kernel == AWQ_GROUPED_GEMM64K ? 32 : 64, outs = kernel == AWQ_GROUPED_GEMM64K ? 32 : 128;
+  return n / rows + groups + 1 < ((int64_t)1 << 24) / (N / outs + 1);
 }
 
 // Largest M that AWQ_LINEAR_AUTO serves with a GEMV-class kernel (above it, the MFMA
@@ -513,7 +514,8 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
       !good_groups(groups) || (gated && N % 2 != 0))
     return AWQ_ERR_BAD_SHAPE;
   if (order ? fan < 1 || x_rows < (n_rows + fan - 1) / fan : x_rows < n_rows) return AWQ_ERR_BAD_SHAPE;
-  if (x_rows > kMaxElements / K || !good_weight(N, K, c.w_bit) || !grouped_grid_ok(n_rows, N, groups)) return AWQ_ERR_BAD_SHAPE;
+  if (x_rows > kMaxElements / K || !good_weight(N, K, c.w_bit) || !grouped_grid_ok(n_rows, N, groups, kv))
+    return AWQ_ERR_BAD_SHAPE;
   if (kv == AWQ_GROUPED_SKINNY && n_rows > kSkinnyMaxRows) return AWQ_ERR_BAD_SHAPE;
   if (!aligned16(X) || !aligned16(offsets) || (order && !aligned16(order)) || !aligned16(qweight) ||
       !aligned16(scales) || !aligned16(zeros) || !aligned16(Y) || (flags && !aligned4(flags)))
@@ -576,7 +578,7 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
                            int64_t N, const void* add, void* Y, void* stream) {
   if (!P || !weights || !pos || !offsets || !Y) return AWQ_ERR_NULL_POINTER;
   if (!good_groups(groups) || T < 1 || top_k < 1 || top_k > AWQ_MAX_TOP_K || T >= kMaxRows / top_k ||
-      N < 1 || N >= kMaxDim || T > ((int64_t)1 << 37) / N)
+      N < 1 || N >= kMaxDim || T >= ((int64_t)1 << (N % 8 == 0 ? 35 : 32)) / N)
     return AWQ_ERR_BAD_SHAPE;
   if (!aligned16(P) || !aligned16(weights) || !aligned16(pos) || !aligned16(offsets) ||
       (add && !aligned16(add)) || !aligned16(Y))
@@ -604,7 +606,8 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
     return AWQ_ERR_NULL_POINTER;
   if (!supported(c) || kv < AWQ_GROUPED_AUTO || kv > AWQ_GROUPED_GEMM64K) return AWQ_ERR_UNSUPPORTED;
   if (M < 1 || M >= kMaxRows || !good_nk(N, K) || !good_groups(adapters) || !good_rank(rank) ||
-      M > kMaxElements / K || !good_weight(N, K, c.w_bit) || !grouped_grid_ok(M, N, 1))
+      M > kMaxElements / K || rank > kMaxElements / K || !good_weight(N, K, c.w_bit) ||
+      !grouped_grid_ok(M, N, 1, kv))
     return AWQ_ERR_BAD_SHAPE;
   if (kv == AWQ_GROUPED_SKINNY && M > AWQ_LORA_SKINNY_MAX_M) return AWQ_ERR_BAD_SHAPE;
   if (!good_workspace(workspace, workspace_bytes, awq_linear_w4a16_lora_workspace_size(M, rank)))

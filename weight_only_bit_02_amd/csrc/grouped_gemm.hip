@@ -83,7 +83,7 @@ hipError_t launch_grouped_gemm(GroupedArgs g, int mode, int w_bit, int kernel, h
   const int64_t mt = (g.n + (bm - 1) * parts) / bm;
   g.nt = (int)((outs + cols - 1) / cols);
   const int64_t blocks = (mt * g.nt + 7) / 8 * 8;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks >= (int64_t)1 << 24) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks);
   auto* const f = w_bit == 8   ? (mode == kPlain ? launch_grouped8_plain : mode == kGated ? launch_grouped8_gated : launch_grouped8_lora)
                   : w_bit == 3 ? (mode == kPlain ? launch_grouped3_plain : mode == kGated ? launch_grouped3_gated : launch_grouped3_lora)
