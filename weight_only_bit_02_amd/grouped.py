@@ -33,7 +33,7 @@ def _check(t, dtype, shape, name, device):
     """The address of a tensor that is what the call needs; these run on every call of a
     decoding step, so what is right takes one pass and only a wrong tensor is looked at again."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -87,9 +87,14 @@ def _stream_of(index):
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
+@functools.lru_cache(maxsize=None)
+def _function(name):
+    return getattr(_abi.load(), name)
+
+
 def _launch(name, device, *args):
     """Calls an entry point on the device's current stream, whatever device is current."""
-    fn = getattr(_abi.load(), name)
+    fn = _function(name)
     index = device.index
     if torch.cuda.current_device() == index:
         status = fn(*args, _current_stream(index))
