@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
   // this wave among those that share its ring, among those along the columns and along K
   const int part = KW == 1 ? wave : 0, kw = KW == 1 ? 0 : wave;
   uint4* const ring = lds + kw * (NS * kBuf);
+  const uint32_t ring_at = lds_address(lds) + kw * (NS * kBuf * 16);
 
   // ---- this block's tile: XCD blockIdx % 8 takes a contiguous run of the tiles there are
   const int mt = MODE == kLora ? (g.n + BM - 1) / BM : __builtin_amdgcn_readfirstlane(count_tiles<BM>(g.offsets, g.groups, g.n, lane));
@@ -298,13 +299,13 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
     auto send = [&](auto c, int step, int i) __attribute__((always_inline)) {
       if (step >= nsteps) return;
       const uint32_t at = (uint32_t)(step * KW + kw);
-      uint4* const dst = ring + decltype(c)::value * kBuf;
+      const uint32_t to = ring_at + decltype(c)::value * (kBuf * 16);
 #pragma unroll
       for (int k = i * kSends / kShares; k < (i + 1) * kSends / kShares; ++k) {
         if (k < kAT)
-          dma16_own(X, &dst[(part * kAT + k) * 64], aoff[k], at * 256);
+          dma16_own(X, to + (part * kAT + k) * 1024, aoff[k], at * 256);
         else
-          dma16_own(W, &dst[BM * 16 + (part * kBT + k - kAT) * 64], boff[k - kAT], at * (kQ * 16));
+          dma16_own(W, to + BM * 256 + (part * kBT + k - kAT) * 1024, boff[k - kAT], at * (kQ * 16));
       }
     };
     // Step `step`'s data has landed: all but the DMAs of the NS - 2 steps after it (other loads in

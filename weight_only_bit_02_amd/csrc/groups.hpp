@@ -94,11 +94,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t b, uint4* lds, uint
 #endif
 }
 
-// The same as an instruction that the compiler neither counts nor waits for: the caller waits
-// (vmcnt) before the data is read and before the wave ends, and lets no read of LDS that must
-// come before or after pass it. It has no output register. The wait states are those that the
-// assembler leaves to the writer: one after m0, five after a vector instruction that wrote b or
-// at (1% of a GEMM's time, were they left out).
+// The same as an instruction that the compiler neither counts nor waits for, to the LDS address
+// `to` (uniform): the caller waits (vmcnt) before the data is read and before the wave ends, and
+// lets no read of LDS that must come before or after pass it. It has no output register. The wait
+// states are those that the assembler leaves to the writer: one after m0, five after a vector
+// instruction that wrote b or at (1% of a GEMM's time, were they left out).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ u32x4 buffer_words(const void* p) {
@@ -106,12 +106,14 @@ __device__ __forceinline__ u32x4 buffer_words(const void* p) {
   return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFF, 0xFFFFFFFFu, 0x00020000u};
 }
 
-__device__ __forceinline__ void dma16_own(u32x4 b, uint4* lds, uint32_t lane_at, uint32_t at) {
+__device__ __forceinline__ uint32_t lds_address(uint4* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)p);
+}
+
+__device__ __forceinline__ void dma16_own(u32x4 b, uint32_t to, uint32_t lane_at, uint32_t at) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               ::"s"(to), "v"(lane_at), "s"(b), "s"(at)
-               : "memory", "m0");
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(lane_at), "s"(b), "s"(at), "{m0}"(to)
+               : "memory");
 #endif
 }
 

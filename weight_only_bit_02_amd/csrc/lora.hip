@@ -66,11 +66,12 @@ __global__ void __launch_bounds__(kS * 64)
   }
   const u32x4 xs = buffer_words(X), as = buffer_words(A + (int64_t)ad * rank * K);
   uint4* const ring = lds + wave * (NS * kStep);
+  const uint32_t ring_at = lds_address(lds) + wave * (NS * kStep * 16);
   const int steps = ((int)(K / kC) - wave + kS - 1) / kS;  // this wave's: wave, wave + kS, ...
   auto send = [&](int step, int buf) __attribute__((always_inline)) {
     const uint32_t k = (uint32_t)(step * kS + wave) * (kC * 2);
 #pragma unroll
-    for (int i = 0; i < kSends; ++i) dma16_own(i < 2 ? xs : as, ring + buf * kStep + i * 64, at[i], k);
+    for (int i = 0; i < kSends; ++i) dma16_own(i < 2 ? xs : as, ring_at + (buf * kStep + i * 64) * 16, at[i], k);
   };
   for (int i = 0; i < NS && i < steps; ++i) send(i, i);
   f32x4s acc0{}, acc1{};

@@ -366,7 +366,6 @@ __global__ void __launch_bounds__(kThreads)
   }
   // a wave sums a key's counts of all blocks and of those before this one
   const int lane = tid & 63;
-#pragma unroll 4
   for (int k = __builtin_amdgcn_readfirstlane(tid >> 6); k < keys; k += kWaves) {
     int all = 0, before = 0;
 #pragma unroll
