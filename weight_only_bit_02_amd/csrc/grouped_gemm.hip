@@ -38,10 +38,10 @@ int columns_of(int mode, int k_waves) { return kGN / k_waves / (mode == kGated ?
 // 256 at a time. The groups' sizes are not known here: a fifth more rows than the mean in the
 // largest tiles and half a tile lost per group. What the rule picks between, in us (GEMM64,
 // 128, 256, 64K; the first two lines experts by mean rows per group, the others adapters):
-//   8 x 4096 x 4096    16: 40 39 42 30     96: 51 67 67 71    512: 245 214 235 309
-//   64 x 4096 x 1024   16: 61 56 57 96     96: 137 100 97 244 512: 620 454 419 1075
-//   4096 x 4096 rows   64: 62 62 61 32   1024: 70 91 147 92  4096: 228 190 176 299
-//   11008 x 4096 rows 192: 62 86 140 69   512: 116 90 147 127
+//   8 x 4096 x 4096    64: 47 59 61 54     96: 51 61 62 69    512: 236 199 218 285
+//   64 x 4096 x 1024   64: 116 96 94 187   96: 146 107 104 259 512: 631 465 402 1107
+//   4096 x 4096 rows   65: 54 70 73 24   1024: 60 72 138 84  4096: 219 172 177 302
+//   11008 x 4096 rows 192: 54 73 130 61   512: 104 75 139 115
 int choose_grouped_gemm(const GroupedArgs& g, int mode, int w_bit) {
   const int kernels[] = {AWQ_GROUPED_GEMM128, AWQ_GROUPED_GEMM64, AWQ_GROUPED_GEMM256, AWQ_GROUPED_GEMM64K};
   const double outs = (double)(mode == kGated ? g.N / 2 : g.N);
