@@ -35,7 +35,7 @@ int columns_of(int mode, int k_waves) { return kGN / k_waves / (mode == kGated ?
 // The tile shape that a batch of n rows in `groups` groups should take the least time with.
 // Microseconds of a K step measured on full and half-full chips at 4-bit codes, by the rows
 // that a block multiplies, and of the rest of a tile (launch, first loads, stores); blocks run
-// 256 at a time. The groups' sizes are not known here: a fifth more rows than the mean in the
+// 256 at a time. The groups' sizes are not known here: a quarter more rows than the mean in the
 // largest tiles and half a tile lost per group. What the rule picks between, in us (GEMM64,
 // 128, 256, 64K; the first two lines experts by mean rows per group, the others adapters):
 //   8 x 4096 x 4096    64: 47 59 61 54     96: 51 61 62 69    512: 236 199 218 285
