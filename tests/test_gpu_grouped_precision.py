@@ -1,0 +1,77 @@
+"""Channels whose weights are exactly zero (codes equal to the zero point) add exactly nothing,
+however large their activations: the error of a result is bounded by the products that make it."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import weight_only_bit_02_amd as awq
+from tests.grouped_ref import gated_reference, linear_bound, linear_reference, lora_reference
+from tests.gpu_util import DEV, host, to_dev
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [(4, 128), (4, 64), (4, 32), (8, 128), (8, 32), (3, 128), (3, 64)]
+KERNELS = ["skinny", "gemm64", "gemm64k", "auto"]
+M, N = 13, 48
+
+
+def _case(K, w_bit, group, large, seed):
+    """Normal weights, channels 5 and 8 i of every group of 128 zero but for one row; row 3 all zero; row 4
+    nothing but a large weight on channel 1, where X is zero. Activations of the zero channels are large."""
+    g = np.random.default_rng(seed)
+    W = (g.standard_normal((N, K)) * 0.02).astype(np.float16)
+    zero = np.array([c for c in range(K) if c % 128 in (5, 24, 42, 127)])
+    W[:, zero] = 0
+    W[3] = 0
+    W[4] = 0
+    W[4, 1::32] = 2.0
+    qw, sc, zb, _ = oracle.quantize_pack(W, group=group, w_bit=w_bit)
+    q, z, s = oracle.unpack(qw, sc, zb, K)
+    Wd = oracle.dequantize(q, z, s)
+    assert not Wd[:, zero].any() and not Wd[3].any()
+    X = g.standard_normal((M, K)).astype(np.float16)
+    X[:, zero] = (large * (1 + g.random((M, len(zero)))) * np.where(g.random((M, len(zero))) < 0.5, -1, 1)).astype(np.float16)
+    X[:, 1::32] = 0
+    return (to_dev(qw.view(np.int32)), to_dev(sc), to_dev(zb)), Wd, X
+
+
+def _inside(Y, y, bound):
+    bad = np.abs(Y - y) > bound
+    assert not bad.any(), (np.argwhere(bad)[:5].tolist(), Y[bad][:5], y[bad][:5], bound[bad][:5])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("w_bit,group", FORMATS)
+@pytest.mark.parametrize("K,large", [(128, 300), (128, 30000), (256, 3000), (1152, 30000)])
+def test_experts(K, large, w_bit, group, kernel):
+    (qw, sc, zb), Wd, X = _case(K, w_bit, group, large, seed=K + w_bit)
+    groups = awq.group_rows(torch.zeros(M, dtype=torch.int32, device=DEV), 1)
+    w = awq.PackedExperts(qw[None], sc[None], zb[None], 1, N, K, group, w_bit)
+    x = to_dev(X)
+    y, S = linear_reference(X, Wd)
+    Y = host(awq.linear_w4a16_grouped(x, w, groups, kernel=kernel)).astype(np.float64)
+    assert not Y[:, 3:5].any()
+    _inside(Y, y, linear_bound(y, S, K))
+    h, bound = gated_reference(X, Wd)
+    _inside(host(awq.linear_w4a16_grouped_gated_silu(x, w, groups, kernel=kernel)).astype(np.float64), h, bound)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("w_bit,group", FORMATS)
+@pytest.mark.parametrize("K,large", [(128, 3000), (1152, 30000)])
+def test_adapters(K, large, w_bit, group, kernel):
+    (qw, sc, zb), Wd, X = _case(K, w_bit, group, large, seed=K + w_bit)
+    g = np.random.default_rng(1)
+    A = (g.standard_normal((2, 8, K)) / np.sqrt(K)).astype(np.float16)
+    A[:, :, np.abs(X).max(0) > 100] = 0
+    B = (g.standard_normal((2, N, 8)) * 0.1).astype(np.float16)
+    scale = np.array([0.5, -1.0], np.float32)
+    ids = np.arange(M, dtype=np.int32) % 3 - 1
+    Y = host(awq.linear_w4a16_lora(to_dev(X), awq.PackedLinear(qw, sc, zb, N, K, group, w_bit),
+                                   awq.LoraAdapters(to_dev(A), to_dev(B), to_dev(scale)), to_dev(ids),
+                                   kernel=kernel)).astype(np.float64)
+    y, bound = lora_reference(X, Wd, A, B, scale, ids)
+    _inside(Y, y, bound)
+    assert not Y[ids < 0, 3].any()

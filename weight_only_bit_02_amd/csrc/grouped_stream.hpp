@@ -25,11 +25,10 @@
 //   - Scales and zeros of the L steps are loaded one weight row per lane, all steps at once
 //     (2 bytes per group would ask for a cache line each), and handed to the lanes that need
 //     them by ds_bpermute. Their addresses have the alignment of their type only.
-//   - 128-channel groups: the codes enter the matrix cores as they are widened, with the bias of
-//     their exponent (bias_of), the partial tile of a step starts from -sum(bias x) - z sum(x)
-//     (both from products with constants when X is loaded), and the scale multiplies it in fp32.
-//     The fp32 partial sums are then up to 1024 |sum(x)| instead of |sum((q - z) x)|: an error
-//     of 2^-24 1024 |sum(x)| per step, some 1e-5 of the step's sum |x (q - z)| at most.
+//   - 128-channel groups: the operand is q - z, exact in fp16, and the scale multiplies a step's
+//     partial tile in fp32. (Codes under the bias of their exponent, with the bias and z taken off
+//     in the fp32 sums, would save the subtraction of two channels at a time, but then a channel
+//     whose code equals its zero leaves the rounding of 1024 |x| in a sum that it is no part of.)
 //     Smaller groups: a lane's channels lie in one group but the lanes of a slice do not, so
 //     the operand carries the scale ((q - z) sc, rounded to fp16 once).
 //   - A chunk that would pass the last weight row starts earlier instead and computes some
@@ -113,33 +112,6 @@ __device__ __forceinline__ half8w centered(const uint32_t (&w)[BITS], int s, con
       d[p] = __builtin_bit_cast(half2w, widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic)) + z.z1024;
   }
   return half8w{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
-}
-
-// The same as bias + q, bias_of<BITS>() by pair: one shift per word of 4-bit codes and one
-// v_and_or_b32 (v_perm_b32) per pair of channels.
-template <int BITS>
-__device__ __forceinline__ half8w biased(const uint32_t (&w)[BITS], int s, uint32_t magic) {
-  uint32_t d[4];
-  if constexpr (BITS == 4) {
-    const uint32_t w0 = w[s], w8 = w[s] >> 8;
-    d[0] = (w0 & 0x000F000Fu) | magic;
-    d[1] = (w0 & 0x00F000F0u) | 0x54005400u;
-    d[2] = (w8 & 0x000F000Fu) | magic;
-    d[3] = (w8 & 0x00F000F0u) | 0x54005400u;
-  } else if constexpr (BITS == 8) {
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      d[p] = __builtin_amdgcn_perm(0x64646464u, w[2 * s + (p >> 1)], p & 1 ? 0x04030402u : 0x04010400u);
-  } else {
-#pragma unroll
-    for (int p = 0; p < 4; ++p) d[p] = widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic);
-  }
-  return __builtin_bit_cast(half8w, uint4{d[0], d[1], d[2], d[3]});
-}
-template <int BITS>
-__device__ __forceinline__ half8w bias_of() {
-  const _Float16 a = 1024, b = BITS == 4 ? 64 : 1024;
-  return half8w{a, a, b, b, a, a, b, b};
 }
 
 // A position of the walk: an item (row tile x column chunk) and a part of K. Uniform.
@@ -328,7 +300,6 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   };
 
   half8w a[L][4];  // this wave's part of the tile's rows of X
-  f32x4w xs[L], xb[L];  // 128-channel groups: per step, -sum(x) and -sum(bias x)
   auto load_x = [&](const StreamItem& it) AWQ_INLINE {
     const int r = c16;  // rows past the last read the last one, never stored
     int xr = it.rows > 0 ? source(it.row0 + (r < it.rows ? r : it.rows - 1)) : 0;
@@ -341,19 +312,6 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
       for (int i = 0; i < 4; ++i) {
         a[j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * 8);
         if (s >= nsteps) a[j][i] = half8w{};  // steps past the last add nothing
-      }
-    }
-    if constexpr (G128) {
-      const _Float16 o = -1;
-      const half8w ones{o, o, o, o, o, o, o, o}, bias = -bias_of<BITS>();
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        xs[j] = xb[j] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          xs[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][i], ones, xs[j], 0, 0, 0);
-          xb[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][i], bias, xb[j], 0, 0, 0);
-        }
       }
     }
   };
@@ -386,19 +344,19 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   auto multiply_128 = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
     f32x4w d[R];
     float f[R];
+    ZeroPair zp[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint32_t sc = q.sc[r][j / 2] >> (16 * (j & 1));
       f[r] = on ? h2f((uint16_t)sc) : 0.0f;
-      const float z = (float)(BITS == 8 ? (q.z[r][0] >> (8 * j)) & 0xFF : (q.z[r][0] >> (4 * j)) & 0xF);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[r][i] = __builtin_fmaf(z, xs[j][i], xb[j][i]);
+      zp[r] = zero_pair(BITS == 8 ? (q.z[r][0] >> (8 * j)) & 0xFF : (q.z[r][0] >> (4 * j)) & 0xF);
+      d[r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const half8w v = biased<BITS>(w[r], s, magic);
+        const half8w v = centered<BITS>(w[r], s, zp[r], magic);
         d[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], v, d[r], 0, 0, 0);
       }
 #pragma unroll
