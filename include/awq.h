@@ -400,7 +400,7 @@ typedef enum awq_grouped_kernel {
  *            as awq_quantize_pack writes it (packing the stacked [groups N][K] does)
  *   Y        fp16 [n_rows][N] out, in group order; rows from offsets[groups] on are left
  *            as they were
- *   1 <= n_rows < 2^30, x_rows K <= 2^31, one weight's codes below 4 GiB, (n_rows / 64 +
+ *   1 <= n_rows < 2^30, x_rows K < 2^31, one weight's codes below 4 GiB, (n_rows / 64 +
  *   groups + 1) (N / 128 + 1) < 2^24 (GEMM64K: n_rows / 32, N / 32); else BAD_SHAPE. Formats,
  *   flags and accuracy as awq_linear_w4a16.
  *   _gated_silu: each weight is a gate|up pair (N even), Y fp16 [n_rows][N/2], as
@@ -444,7 +444,7 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
  *   A fp16 [adapters][rank][K], B fp16 [adapters][N][rank], lora_scale fp32 [adapters];
  *   rank a multiple of 8 up to AWQ_MAX_LORA_RANK (smaller adapters padded with zero rows
  *   of A); 1 <= adapters <= AWQ_MAX_GROUPS; M >= 1, M K and rank K
- *   <= 2^31, codes below 4 GiB, (M / 64 + 2) (N / 128 + 1) < 2^24 (GEMM64K: M / 32, N / 32)
+ *   < 2^31, codes below 4 GiB, (M / 64 + 2) (N / 128 + 1) < 2^24 (GEMM64K: M / 32, N / 32)
  *   ids      int32 [M]
  *   order    int32 [M] or NULL: a permutation of the rows that brings those of one adapter
  *            together (awq_group_rows); it changes the speed of large mixed batches only

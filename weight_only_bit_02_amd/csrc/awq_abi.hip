@@ -86,7 +86,8 @@ ClipLayout clip_layout(int64_t T, int64_t N, int64_t K, int n_shrink, int group)
 
 // Limits of the expert and adapter calls.
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and rows are kept in 32 bits
-constexpr int64_t kMaxElements = (int64_t)1 << 31;  // of X: offsets in it are kept in 32 bits
+constexpr int64_t kMaxElements = ((int64_t)1 << 31) - 1;  // of X and of an adapter's A: their bytes end
+                                                          // below 2^32 - 1, the most a descriptor covers
 constexpr int64_t kSkinnyMaxRows = 65536;           // its grid: one row of blocks per row tile
 
 // One weight's codes are addressed with 32-bit offsets too.

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256) k_grouped(GroupedArgs g) {
     constexpr int kAT = 2 * RT * KW;  // A transfers per wave and step
     // A DMA map: wave transfer i fills slots (part * kAT + i) * 64 + lane: row r = (part * kAT
     // + i) * 4 + lane / 16, slot lane % 16 <- chunk (lane % 16) ^ (r % 16), as offsets in X (the
-    // host admits X up to 2^32 bytes). Rows past the last read the last one.
+    // host admits X below 2^32 bytes). Rows past the last read the last one.
     uint32_t aoff[kAT];
 #pragma unroll
     for (int i = 0; i < kAT; ++i) {

@@ -81,7 +81,8 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int groups,
   return RowTile{0, 0, 0};
 }
 
-// Descriptor of the memory from p on (uniform): raw, offsets up to 2^32.
+// Descriptor of the memory from p on (uniform): raw, bytes up to 2^32 - 1 (a dword
+// that holds the last one reads as zero).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
 }
