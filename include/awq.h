@@ -401,8 +401,10 @@ typedef enum awq_grouped_kernel {
  *   Y        fp16 [n_rows][N] out, in group order; rows from offsets[groups] on are left
  *            as they were
  *   1 <= n_rows < 2^30, x_rows K < 2^31, one weight's codes below 4 GiB, (n_rows / 64 +
- *   groups + 1) (N / 128 + 1) < 2^24 (GEMM64K: n_rows / 32, N / 32); else BAD_SHAPE. Formats,
- *   flags and accuracy as awq_linear_w4a16.
+ *   groups + 1) (N / 128 + 1) < 2^24 (GEMM64K: n_rows / 32, N / 32); else BAD_SHAPE. Formats
+ *   and accuracy as awq_linear_w4a16.
+ *   flags    NONFINITE_INPUT: an Inf or NaN in the group scales or in X; without order, in the
+ *            rows of X before offsets[groups] (those behind are never read), with it in any row
  *   _gated_silu: each weight is a gate|up pair (N even), Y fp16 [n_rows][N/2], as
  *   awq_linear_w4a16_gated_silu.
  */

@@ -523,9 +523,11 @@ static awq_status grouped_common(const void* X, int64_t x_rows, const int32_t* o
     return AWQ_ERR_MISALIGNED;
   hipStream_t st = (hipStream_t)stream;
   if (flags) {
-    const hipError_t e = awq::launch_nonfinite_scan((const uint16_t*)X, x_rows * K,
-                                                    (const uint16_t*)scales,
-                                                    groups * N * (K / c.group_size), flags, st);
+    // X in group order: rows behind the last group's are no input (a linear before this one leaves
+    // them as they were); how many there are stands on the device
+    const hipError_t e = awq::launch_nonfinite_scan((const uint16_t*)X, (order ? x_rows : n_rows) * K,
+                                                    (const uint16_t*)scales, groups * N * (K / c.group_size),
+                                                    flags, st, order ? nullptr : offsets + groups, K);
     if (e != hipSuccess) return AWQ_ERR_HIP;
   }
   awq::GroupedArgs g{};

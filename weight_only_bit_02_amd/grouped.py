@@ -261,7 +261,8 @@ def linear_w4a16_grouped(X: torch.Tensor, w: PackedExperts, groups: RowGroups, f
                          kernel: str = "auto") -> torch.Tensor:
     """awq_linear_w4a16_grouped: every expert's linear on its rows, Y [n][N] in group order.
     X holds the rows in group order, or (fan = choices per token) one row per token, taken
-    through groups.order. Rows without a group are left as they are in out."""
+    through groups.order. Rows without a group are left as they are in out; X in group order
+    need not hold any there, and flags does not look at them."""
     return _grouped("awq_linear_w4a16_grouped", X, w, groups, fan, w.N, out, flags, kernel)
 
 
