@@ -148,7 +148,8 @@ hipError_t launch_combine(const uint16_t* P, const float* weights, const int32_t
                           uint16_t* Y, hipStream_t stream);
 
 // 32 values of scale X A^T for one row, as the second product's matrix cores take them:
-// v = f (hi + lo) with f a power of two and the largest |hi| in [1, 2), zeros past the rank.
+// v = f (hi + lo) with f a power of two and the largest finite |hi| in [1, 2) ([2, 4) from 2^127
+// on), zeros past the rank.
 constexpr int kLoraBlock = 32;
 struct LoraRow {
   uint16_t hi[kLoraBlock], lo[kLoraBlock];

@@ -119,11 +119,13 @@ __global__ void __launch_bounds__(kS * 64)
   const float sc = scale[ad];
   v0 = j0 < rank ? sc * v0 : 0.0f;
   v1 = j1 < rank ? sc * v1 : 0.0f;
-  float mx = fmaxf(__builtin_fabsf(v0), __builtin_fabsf(v1));
+  const bool finite0 = __builtin_isfinite(v0), finite1 = __builtin_isfinite(v1);
+  float mx = fmaxf(finite0 ? __builtin_fabsf(v0) : 0.0f, finite1 ? __builtin_fabsf(v1) : 0.0f);
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-  const uint32_t ex = __builtin_bit_cast(uint32_t, mx) >> 23;
-  const bool fit = ex >= 1 && ex < 253;  // zero, tiny or not finite: as it is
+  // the row's power of two, by its largest finite value (2^126 at most: its inverse is normal)
+  const uint32_t of_mx = __builtin_bit_cast(uint32_t, mx) >> 23, ex = of_mx < 253 ? of_mx : 253;
+  const bool fit = ex >= 1;  // zero or tiny: as it is
   const float up = fit ? __builtin_bit_cast(float, (254u - ex) << 23) : 1.0f;
   const int to = __shfl(src, row), of = __shfl(id, row);
   if (of != ad) return;
@@ -131,8 +133,8 @@ __global__ void __launch_bounds__(kS * 64)
   const _Float16 h0 = (_Float16)(v0 * up), h1 = (_Float16)(v1 * up);
   h->hi[c16] = __builtin_bit_cast(uint16_t, h0);
   h->hi[16 + c16] = __builtin_bit_cast(uint16_t, h1);
-  h->lo[c16] = f2h_bits(v0 * up - (float)h0);
-  h->lo[16 + c16] = f2h_bits(v1 * up - (float)h1);
+  h->lo[c16] = finite0 ? f2h_bits(v0 * up - (float)h0) : 0;  // (Inf - Inf)
+  h->lo[16 + c16] = finite1 ? f2h_bits(v1 * up - (float)h1) : 0;
   if (c16 == 0) h->f = fit ? __builtin_bit_cast(float, ex << 23) : 1.0f;
 }
 
