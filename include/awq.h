@@ -452,7 +452,8 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
  *            together (awq_group_rows); it changes the speed of large mixed batches only
  *   workspace device scratch of awq_linear_w4a16_lora_workspace_size(M, rank) bytes,
  *            16-byte aligned (X A^T)
- *   flags    NONFINITE_INPUT: an Inf or NaN in X, the group scales, A or B
+ *   flags    NONFINITE_INPUT: an Inf or NaN in X, the group scales, A, B or lora_scale (all
+ *            adapters, rows or not)
  *   X A^T is accumulated in fp32; for the second product its rows are split into
  *   fp16 hi + lo after scaling by a power of two (22 significant bits).
  */

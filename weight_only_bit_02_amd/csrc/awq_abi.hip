@@ -626,7 +626,7 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
                                    N * (K / c.group_size), flags, st);
     if (e == hipSuccess)
       e = awq::launch_nonfinite_scan((const uint16_t*)A, (int64_t)adapters * rank * K, (const uint16_t*)B,
-                                     (int64_t)adapters * rank * N, flags, st);
+                                     (int64_t)adapters * rank * N, flags, st, nullptr, 0, lora_scale, adapters);
     if (e != hipSuccess) return AWQ_ERR_HIP;
   }
   e = awq::launch_lora_shrink((const uint16_t*)X, (int)M, K, (const uint16_t*)A, lora_scale, adapters,

@@ -110,11 +110,11 @@ hipError_t launch_gemm_wide(const uint16_t* X, int64_t M, const uint32_t* qweigh
                             int group, int w_bit, uint16_t* Y, bool gated, hipStream_t stream);
 
 // Data conditions of the linear path: OR AWQ_FLAG_NONFINITE_INPUT into *flags when a
-// (n fp16 values, n % 8 == 0) or b (m fp16 values) holds an Inf or a NaN. live (device): only
-// the first *live rows of `row` values of a are looked at.
+// (n fp16 values, n % 8 == 0), b (m fp16 values) or c (k fp32 values) holds an Inf or a NaN.
+// live (device): only the first *live rows of `row` values of a are looked at.
 hipError_t launch_nonfinite_scan(const uint16_t* a, int64_t n, const uint16_t* b, int64_t m,
                                  uint32_t* flags, hipStream_t stream, const int32_t* live = nullptr,
-                                 int64_t row = 0);
+                                 int64_t row = 0, const float* c = nullptr, int64_t k = 0);
 
 // f2: out = fp16(A / s) along columns (axis 1, len(s) = cols) or rows (axis 0,
 // len(s) = rows); cols % 8 == 0; out may alias A.
