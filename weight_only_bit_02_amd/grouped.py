@@ -212,15 +212,20 @@ def quantize_pack_experts(W: torch.Tensor, s: torch.Tensor | None = None, zero_p
     dev = _first(W, (torch.float16,), 3, "W")
     E, N, K = W.shape
     _check(W, torch.float16, (E, N, K), "W", dev)
-    if s is not None and s.dim() != 1:
-        _check(s, torch.float16, (E, K), "s", dev)
-        parts = [quantize_pack(W[e], s[e], flags, zero_point=zero_point, group_size=group_size, w_bit=w_bit)
-                 for e in range(E)]
-        qweight, scales, zeros = (torch.stack(t) for t in zip(*((p.qweight, p.scales, p.zeros) for p in parts)))
-    else:
-        p = quantize_pack(W.view(E * N, K), s, flags, out=alloc_packed(E * N, K, dev, group_size, w_bit),
-                          zero_point=zero_point, group_size=group_size, w_bit=w_bit)
-        qweight, scales, zeros = (t.view(E, N, -1) for t in (p.qweight, p.scales, p.zeros))
+    each = isinstance(s, torch.Tensor) and s.dim() != 1
+    if s is not None:
+        _check(s, torch.float16, (E, K) if each else (K,), "s", dev)
+    if flags is not None:
+        _check(flags, torch.int32, getattr(flags, "shape", None), "flags", dev)
+    with torch.cuda.device(dev):  # quantize_pack launches on the current device
+        if each:
+            parts = [quantize_pack(W[e], s[e], flags, zero_point=zero_point, group_size=group_size, w_bit=w_bit)
+                     for e in range(E)]
+            qweight, scales, zeros = (torch.stack(t) for t in zip(*((p.qweight, p.scales, p.zeros) for p in parts)))
+        else:
+            p = quantize_pack(W.view(E * N, K), s, flags, out=alloc_packed(E * N, K, dev, group_size, w_bit),
+                              zero_point=zero_point, group_size=group_size, w_bit=w_bit)
+            qweight, scales, zeros = (t.view(E, N, -1) for t in (p.qweight, p.scales, p.zeros))
     return PackedExperts(qweight, scales, zeros, E, N, K, group_size, w_bit)
 
 
