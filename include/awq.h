@@ -430,8 +430,8 @@ awq_status awq_linear_w4a16_grouped_gated_silu(const void* X, int64_t x_rows,
  *   P fp16 [T top_k][N] (group order); weights fp32 [T][top_k], pos int32 [T top_k] and
  *   offsets int32 [groups + 1] as awq_moe_route writes them; add fp16 [T][N] or NULL (a
  *   shared expert, the residual); Y fp16 [T][N] out, may equal add.
- *   1 <= T, 1 <= top_k <= AWQ_MAX_TOP_K, T top_k < 2^30, 1 <= N < 2^31, T N < 2^35
- *   (2^32 where N is no multiple of 8).
+ *   1 <= T, 1 <= top_k <= AWQ_MAX_TOP_K, T top_k < 2^30, 1 <= N < 2^31, T N <= 2^35
+ *   - 1024 (2^32 - 128 where N is no multiple of 8).
  */
 awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* pos,
                            const int32_t* offsets, int32_t groups, int64_t T, int32_t top_k,

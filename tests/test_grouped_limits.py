@@ -26,3 +26,9 @@ def test_largest_x(lib, kernel):
     lora = lambda M, K, rank: lib.awq_linear_w4a16_lora(FAKE, M, FAKE, FAKE, FAKE, 16, K, None, FAKE, FAKE, FAKE, 2, rank,
                                                         FAKE, None, FAKE, FAKE, 1 << 40, None, kernel, None)
     assert lora(1 << 17, 1 << 14, 8) == SHAPE and lora(1, 1 << 23, 256) == SHAPE
+
+
+@pytest.mark.parametrize("T,N", [((1 << 29) - 1, 64), ((1 << 28) - 1, 128), ((1 << 30) - 1, 4), ((1 << 32) // 65, 65)])
+def test_combine_of_more_blocks_than_a_launch(lib, T, N):
+    """T N just below 2^35 (2^32): its whole blocks of threads are 2^32 threads."""
+    assert lib.awq_moe_combine(FAKE, FAKE, FAKE, FAKE, 4, T, 1, N, None, FAKE, None) == SHAPE

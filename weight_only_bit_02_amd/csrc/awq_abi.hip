@@ -580,8 +580,10 @@ awq_status awq_moe_combine(const void* P, const float* weights, const int32_t* p
                            const int32_t* offsets, int32_t groups, int64_t T, int32_t top_k,
                            int64_t N, const void* add, void* Y, void* stream) {
   if (!P || !weights || !pos || !offsets || !Y) return AWQ_ERR_NULL_POINTER;
+  // a launch has fewer than 2^32 threads, whole blocks of 128: of 8 values each, or of one
+  const int64_t most = (((int64_t)1 << 32) - 128) * (N % 8 == 0 ? 8 : 1);
   if (!good_groups(groups) || T < 1 || top_k < 1 || top_k > AWQ_MAX_TOP_K || T >= kMaxRows / top_k ||
-      N < 1 || N >= kMaxDim || T >= ((int64_t)1 << (N % 8 == 0 ? 35 : 32)) / N)
+      N < 1 || N >= kMaxDim || T > most / N)
     return AWQ_ERR_BAD_SHAPE;
   if (!aligned16(P) || !aligned16(weights) || !aligned16(pos) || !aligned16(offsets) ||
       (add && !aligned16(add)) || !aligned16(Y))
