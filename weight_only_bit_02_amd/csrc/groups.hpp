@@ -9,7 +9,6 @@
 
 namespace awq {
 
-constexpr int kMaxGroups = 512;
 typedef float f32x4w __attribute__((ext_vector_type(4)));
 
 // Inclusive sum over the wave: DPP row shifts, then the row broadcasts.

@@ -404,8 +404,15 @@ int key_bits(int groups) {  // bits of the keys 0 .. groups
   return b;
 }
 
-size_t alone_lds(int groups, int ids) { return (size_t)(alone_ints(groups) + ids) * 4; }
-size_t place_lds(int groups) { return ((size_t)(groups + 1) * (kWaves + 2) + kWaves) * 4; }
+constexpr size_t alone_lds(int groups, int ids) { return (size_t)(alone_ints(groups) + ids) * 4; }
+constexpr size_t place_lds(int groups) { return ((size_t)(groups + 1) * (kWaves + 2) + kWaves) * 4; }
+
+// The limits of the entry points that the kernels rely on.
+static_assert(AWQ_MAX_GROUPS <= 8 * kWave, "choose() holds at most eight logits a lane");
+static_assert(AWQ_MAX_TOP_K <= kWave, "a lane holds one choice");
+constexpr size_t kLaunchLds = 64 * 1024;  // dynamic LDS that a launch gets without asking
+static_assert(alone_lds(AWQ_MAX_GROUPS, (int)kOneBlockTokens * AWQ_MAX_TOP_K) <= kLaunchLds, "LDS of one block");
+static_assert(place_lds(AWQ_MAX_GROUPS) <= kLaunchLds, "LDS of the placement");
 
 int64_t group_run(int64_t n) {  // pairs per block of a grouping in two launches
   const int64_t r = (n + kMaxBlocks - 1) / kMaxBlocks;
