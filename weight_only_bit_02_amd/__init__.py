@@ -9,6 +9,8 @@ from .awq import (  # noqa: F401
     search_scales,
 )
 from .grouped import (  # noqa: F401
-    LoraAdapters, PackedExperts, Routing, RowGroups, group_rows, linear_w4a16_grouped,
-    linear_w4a16_grouped_gated_silu, linear_w4a16_lora, moe_combine, moe_route, quantize_pack_experts,
+    LoraAdapters, PackedExperts, Routing, RowGroups, group_rows, group_rows_workspace_size,
+    linear_w4a16_grouped, linear_w4a16_grouped_gated_silu, linear_w4a16_lora,
+    linear_w4a16_lora_workspace_size, moe_combine, moe_route, moe_route_workspace_size,
+    quantize_pack_experts,
 )

@@ -138,10 +138,21 @@ def _alloc_groups(n, groups, device):
     return RowGroups(torch.empty(groups + 1, **i32), torch.empty(n, **i32), torch.empty(n, **i32))
 
 
+def group_rows_workspace_size(n: int, n_groups: int) -> int:
+    """Bytes of workspace (a uint8 tensor) that group_rows takes for n rows; 0: none."""
+    return _workspace_size("awq_group_rows_workspace_size", n, n_groups)
+
+
+def moe_route_workspace_size(T: int, E: int) -> int:
+    """Bytes of workspace (a uint8 tensor) that moe_route takes for logits [T][E]; 0: none."""
+    return _workspace_size("awq_moe_route_workspace_size", T, E)
+
+
 def group_rows(ids: torch.Tensor, n_groups: int, out: RowGroups | None = None,
                workspace: torch.Tensor | None = None) -> RowGroups:
     """awq_group_rows: int32 ids [n] (outside [0, n_groups): no group) to the rows in group
-    order, stable; rows without a group come last."""
+    order, stable; rows without a group come last. workspace: group_rows_workspace_size bytes,
+    one for each of the calls that overlap."""
     dev = _first(ids, (torch.int32,), 1, "ids")
     n = ids.shape[0]
     ip = _check(ids, torch.int32, (n,), "ids", dev)
@@ -150,7 +161,7 @@ def group_rows(ids: torch.Tensor, n_groups: int, out: RowGroups | None = None,
     op = _check(out.offsets, torch.int32, (n_groups + 1,), "out.offsets", dev)
     rp = _check(out.order, torch.int32, (n,), "out.order", dev)
     pp = _check(out.pos, torch.int32, (n,), "out.pos", dev)
-    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_group_rows_workspace_size", n, n_groups), dev)
+    wp, wn, _keep = _workspace(workspace, group_rows_workspace_size(n, n_groups), dev)
     _launch("awq_group_rows", dev, ip, n, n_groups, op, rp, pp, wp, wn)
     return out
 
@@ -158,7 +169,8 @@ def group_rows(ids: torch.Tensor, n_groups: int, out: RowGroups | None = None,
 def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Routing | None = None,
               flags: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> Routing:
     """awq_moe_route: router logits [T][E] (fp16 or fp32; rows may be strided) to the top_k
-    experts of each token, their softmax weights, and the pairs in expert order."""
+    experts of each token, their softmax weights, and the pairs in expert order. workspace:
+    moe_route_workspace_size bytes, one for each of the calls that overlap."""
     dev = _first(logits, (torch.float16, torch.float32), 2, "logits")
     T, E = logits.shape
     ld = logits.stride(0) if T > 1 else E
@@ -174,7 +186,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: R
     op = _check(out.groups.offsets, torch.int32, (E + 1,), "out.groups.offsets", dev)
     rp = _check(out.groups.order, torch.int32, (n,), "out.groups.order", dev)
     pp = _check(out.groups.pos, torch.int32, (n,), "out.groups.pos", dev)
-    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_moe_route_workspace_size", T, E), dev)
+    wp, wn, _keep = _workspace(workspace, moe_route_workspace_size(T, E), dev)
     _launch("awq_moe_route", dev, logits.data_ptr(), 0 if logits.dtype == torch.float16 else 1, T, E, ld,
             top_k, int(bool(renormalize)), wtp, ip, op, rp, pp, wp, wn, _flags(flags, dev))
     return out
@@ -313,6 +325,11 @@ class LoraAdapters:
     scale: torch.Tensor  # fp32 [adapters]
 
 
+def linear_w4a16_lora_workspace_size(M: int, rank: int) -> int:
+    """Bytes of workspace (a uint8 tensor) that linear_w4a16_lora takes for M rows."""
+    return _workspace_size("awq_linear_w4a16_lora_workspace_size", M, rank)
+
+
 def linear_w4a16_lora(X: torch.Tensor, w: PackedLinear, lora: LoraAdapters, ids: torch.Tensor,
                       groups: RowGroups | None = None, out: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, flags: torch.Tensor | None = None,
@@ -320,8 +337,8 @@ def linear_w4a16_lora(X: torch.Tensor, w: PackedLinear, lora: LoraAdapters, ids:
     """awq_linear_w4a16_lora: Y = X deq(W)^T + scale[a] (X A_a^T) B_a^T with a = ids[i] for
     row i (int32; outside [0, adapters): the linear alone). groups (group_rows(ids, adapters))
     brings the rows of an adapter together: worth it for large batches of mixed rows, kept
-    by the caller over the layers of a step. workspace: awq_linear_w4a16_lora_workspace_size
-    bytes; calls that overlap need one each."""
+    by the caller over the layers of a step. workspace: linear_w4a16_lora_workspace_size
+    bytes, one for each of the calls that overlap."""
     dev = _first(X, (torch.float16,), 2, "X")
     M, K = X.shape
     if K != w.K:
@@ -339,7 +356,7 @@ def linear_w4a16_lora(X: torch.Tensor, w: PackedLinear, lora: LoraAdapters, ids:
     if out is None:
         out = torch.empty((M, w.N), dtype=torch.float16, device=dev)
     yp = _check(out, torch.float16, (M, w.N), "out", dev)
-    wp, wn, _keep = _workspace(workspace, _workspace_size("awq_linear_w4a16_lora_workspace_size", M, rank), dev)
+    wp, wn, _keep = _workspace(workspace, linear_w4a16_lora_workspace_size(M, rank), dev)
     _launch("awq_linear_w4a16_lora", dev, xp, M, qp, sp, zp, w.N, K, _config(w.group, w.w_bit), ap, bp, cp, L,
             rank, ip, rp, yp, wp, wn, _flags(flags, dev), _GROUPED_KERNELS[kernel])
     return out
