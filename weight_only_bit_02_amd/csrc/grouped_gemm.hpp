@@ -30,18 +30,19 @@
 // times the blocks for batches whose tiles would leave the chip idle, at four times A's traffic
 // (64 rows x 4096 x 4096 with adapters 61 us -> 24). grouped_gemm.hip picks.
 //
-// What bounds it: large groups, the issue of one wave per SIMD (128 products of 32 cycles and
-// about 590 other instructions of 4 a step) and the chip's power: 8 experts x 22016 x 4096 gated,
-// 8192 rows, 1534 us, 963 TFLOP/s (a library fp16 product of 8192^3 reaches 1323). Middling
+// What bounds it: large groups, the issue of one wave per SIMD (matrix cores 45% busy, vector
+// instructions 23%) and the chip's power: 8 experts x 22016 x 4096 gated, 8192 rows, 1601 us in a
+// row of them, 923 TFLOP/s (a library fp16 product of 8192^3 reaches 1323). Middling
 // groups, the widening, whose cost does not depend on the rows. K of few steps, a tile's start:
 // offsets, row indices, first operands, 4 to 5 us before the first product.
 //
 // Operand values ((q - z) sc rounded to fp16 once) and, for KW = 1, their order along K are those
 // of the 256-row GEMM, so an expert's rows equal the plain linear's bit for bit where that runs
-// its GEMM. The rounding costs 2^-12 relative per weight at most, some 1.8e-4 of a sum of many
-// random terms, beside 2.1e-4 of the output's own rounding; the gated form, which has it in both
-// factors, comes to 3.3e-4 where exact weights give 2.1e-4. (Scaling the sums in fp32 instead, as
-// grouped_stream.hpp does, takes a second set of sums: 256 rows have no registers for it.)
+// its GEMM. The rounding costs 2^-11 relative per weight at most, some 1.8e-4 of a sum of many
+// random terms, beside 2.1e-4 of the output's own rounding (2.7 to 2.9e-4 together); the gated
+// form, which has it in both factors, comes to 3.3e-4 where exact weights give 2.1e-4. (Scaling the
+// sums in fp32 instead, as grouped_stream.hpp does, takes a second set of sums: 256 rows have no
+// registers for it.)
 //
 // Adapters (MODE kLora): the rows of one batch, optionally through `order` (then Y is
 // scattered back through it). After the K loop the rows' adapters are walked one by one, H B_a^T

@@ -31,7 +31,7 @@ hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, hipStream_t
     return (outs + cols - 1) / cols;
   };
   // items for half the blocks or fewer: narrower ones (4096 x 4096 with adapters, one row: 13.1 us
-  // with whole items, 11.2; with items for more blocks, 11008 rows of weights: 13.5 and 13.9)
+  // with whole items, 11.2 so; with items for more blocks, 11008 rows of weights, 13.5 and 13.9)
   const bool narrow = w_bit != 8 && mt * chunks(false) * 2 <= blocks;
   g.nt = (int)chunks(narrow);
   const int64_t items = mt * g.nt;

@@ -13,8 +13,8 @@
 //   - Codes go global -> LDS by 16-byte DMA, eight neighbouring lanes on 128 contiguous bytes of
 //     a weight row, a whole cache line per request: the matrix cores want neighbouring lanes on
 //     neighbouring rows, and loading in that order straight into registers costs an L1 access
-//     per lane (12.1 M instead of 4.3 M for 64 experts x 4096 x 1024 on 384 rows), loading 64
-//     bytes per row twice the requests in flight for the same bytes. The buffers belong to one
+//     per lane (this way 64 experts x 4096 x 1024 on 384 rows, 145 MB, take 4.1 M in all), loading
+//     64 bytes per row twice the requests in flight for the same bytes. The buffers belong to one
 //     wave, so there is no barrier: a buffer is refilled as soon as its codes are in registers,
 //     and a wave keeps 16 KB in flight. Pieces are stored so that the reads have no bank
 //     conflicts. The waits are written out (take_codes, meet): left to itself the compiler
@@ -35,10 +35,10 @@
 //     columns twice, to the same values.
 //
 // What bounds it: the widening and the stream together; large launches reach three quarters of
-// what a copy reaches. 64 experts x 4096 x 1024, 384 rows: 33 us, 4.3 TB/s (without the
-// multiplications 30, without the loads 28); 8 experts x 22016 x 4096 gated, 64 rows: 78 us, 4.7
-// TB/s; 8 experts x 2048 x 2048 gated, a row each: 9 us, of which the chain offsets, row, first
-// codes, sums is most. 3-bit codes cost more instructions per byte: 64 x 2048 x 2048, 512 rows, 35 us.
+// what a copy reaches, more with 8-bit codes. 64 experts x 4096 x 1024, 384 rows: 36.5 us, 3.9
+// TB/s; 8 experts x 22016 x 4096 gated, 64 rows: 81 us, 4.6 TB/s; 8 experts x 2048 x 2048 gated, a
+// row each: 9.2 us, of which the chain offsets, row, first codes, sums is most. 3-bit codes cost
+// more instructions per byte: 64 x 2048 x 2048, 512 rows, 37 us.
 //
 // Gated: tiles 0 .. R / 2 - 1 are gate rows, the rest their up rows, so a lane's sums hold
 // both and the epilogue needs no exchange. Adapters: as in grouped_gemm.hpp; the waves share
