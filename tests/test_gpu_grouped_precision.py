@@ -75,3 +75,20 @@ def test_adapters(K, large, w_bit, group, kernel):
     y, bound = lora_reference(X, Wd, A, B, scale, ids)
     _inside(Y, y, bound)
     assert not Y[ids < 0, 3].any()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("w_bit,group", FORMATS)
+@pytest.mark.parametrize("K", [128, 1152])
+def test_infinite_activation(K, w_bit, group, kernel):
+    """An Inf on a channel of positive (negative) weights is an Inf of its sign in the outputs, not a NaN."""
+    (qw, sc, zb), Wd, X = _case(K, w_bit, group, 0, seed=K)
+    X[5, 33], X[7, 65] = np.inf, -np.inf
+    y = np.where(np.isnan(X.astype(np.float64) @ Wd.T), np.nan, linear_reference(X, Wd)[0])
+    w = awq.PackedExperts(qw[None], sc[None], zb[None], 1, N, K, group, w_bit)
+    groups = awq.group_rows(torch.zeros(M, dtype=torch.int32, device=DEV), 1)
+    Y = host(awq.linear_w4a16_grouped(to_dev(X), w, groups, kernel=kernel)).astype(np.float64)
+    rows = [5, 7]
+    assert np.isinf(y[rows]).sum() > N  # weights that are not zero
+    assert np.array_equal(Y[rows], y[rows], equal_nan=True)
+    assert np.isfinite(np.delete(Y, rows, 0)).all()
