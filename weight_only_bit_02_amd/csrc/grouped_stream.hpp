@@ -19,18 +19,18 @@
 //     and a wave keeps 16 KB in flight. Pieces are stored so that the reads have no bank
 //     conflicts. The waits are written out (take_codes, meet): left to itself the compiler
 //     drains every load in flight before each read, barrier and loop end.
-//   - v_mfma_f32_16x16x32_f16: lane l works on weight row l % 16 and on the 32 channels
-//     [32 kg, 32 kg + 32), kg = l / 16, of a step: 16 bytes of 4-bit codes per weight row,
-//     widened 8 channels at a time to exact q - z.
+//   - v_mfma_f32_16x16x32_f16: lane l works on weight row l % 16 and on 32 channels of a step, by
+//     kg = l / 16: with 128-channel groups on [32 kg, 32 kg + 32), 16 bytes of 4-bit codes per weight
+//     row; with smaller ones on [32 i + 8 kg, 32 i + 8 kg + 8), i = 0 .. 3, so that the channels of
+//     a product (slice i) lie in one group. The codes are widened 8 channels at a time.
 //   - Scales and zeros of the L steps are loaded one weight row per lane, all steps at once
 //     (2 bytes per group would ask for a cache line each), and handed to the lanes that need
 //     them by ds_bpermute. Their addresses have the alignment of their type only.
-//   - 128-channel groups: the operand is q - z, exact in fp16, and the scale multiplies a step's
-//     partial tile in fp32. (Codes under the bias of their exponent, with the bias and z taken off
-//     in the fp32 sums, would save the subtraction of two channels at a time, but then a channel
-//     whose code equals its zero leaves the rounding of 1024 |x| in a sum that it is no part of.)
-//     Smaller groups: a lane's channels lie in one group but the lanes of a slice do not, so
-//     the operand carries the scale ((q - z) sc, rounded to fp16 once).
+//   - The operand is q - z, exact in fp16, and the scale multiplies a group's partial tile in fp32.
+//     (Codes under the bias of their exponent, with the bias and z taken off in the fp32 sums, would
+//     save the subtraction of two channels at a time, but then a channel whose code equals its zero
+//     leaves the rounding of 1024 |x| in a sum that it is no part of; operands that carry the scale,
+//     fp16((q - z) sc), have a rounding more than the plain linear for few rows.)
 //   - A chunk that would pass the last weight row starts earlier instead and computes some
 //     columns twice, to the same values.
 //
@@ -90,9 +90,14 @@ __device__ __forceinline__ ZeroPair zero_pair(uint32_t z) {
   return ZeroPair{__builtin_bit_cast(half2w, a | (a << 16)), __builtin_bit_cast(half2w, b | (b << 16))};
 }
 
+// A lane's code words of a step: its 32 channels in order; 3-bit codes in slices of their own
+// (small groups): per slice the low planes' fields in bits 0-7 of each half, the high plane's in
+// bits 8-11.
+constexpr int stream_words(int bits, int groups) { return bits == 3 && groups > 1 ? 4 : bits; }
+
 // Codes of 8 channels (slice s of a lane's 32) as exact q - z.
-template <int BITS>
-__device__ __forceinline__ half8w centered(const uint32_t (&w)[BITS], int s, const ZeroPair& z,
+template <int BITS, int W>
+__device__ __forceinline__ half8w centered(const uint32_t (&w)[W], int s, const ZeroPair& z,
                                            uint32_t magic) {
   half2w d[4];
   if constexpr (BITS == 4) {
@@ -109,7 +114,9 @@ __device__ __forceinline__ half8w centered(const uint32_t (&w)[BITS], int s, con
   } else {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-      d[p] = __builtin_bit_cast(half2w, widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic)) + z.z1024;
+      d[p] = __builtin_bit_cast(half2w, W == 4 ? widen3_pair(w[s], w[s], p, 8 + p, magic)
+                                               : widen3_pair(w[s >> 1], w[2], 4 * (s & 1) + p, 4 * s + p, magic)) +
+             z.z1024;
   }
   return half8w{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
 }
@@ -119,8 +126,8 @@ struct StreamItem {
   int tile, chunk, part, row0, rows;
 };
 
-// G128: 128-channel groups (else 64 or 32).
-template <int MODE, int BITS, bool G128, int R, int L, int S>
+// GS: groups of a step of 128 channels (1, 2, 4).
+template <int MODE, int BITS, int GS, int R, int L, int S>
 __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2)))
     k_stream(GroupedArgs g) {
   constexpr int BM = 16, kCols = MODE == kGated ? 8 * R : 16 * R;
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   const int64_t N = g.N, K = g.K, nh = N / 2;
   const int outs = (int)(MODE == kGated ? nh : N);
   const int nsteps = (int)(K / kGroup), nt = g.nt, parts = (nsteps + S * L - 1) / (S * L);
-  const int gsh = G128 ? 2 : g.group == 64 ? 1 : 0, per = 4 >> gsh;  // groups of a step: 1, 2, 4
+  constexpr int W = stream_words(BITS, GS);
   const int64_t Gs = K / g.group, zbw = BITS == 8 ? Gs : (Gs + 1) / 2, words = K * BITS / 32;
   const int64_t sbytes = (MODE == kLora ? 1 : g.groups) * N * Gs * 2;
   const int64_t zbytes = (MODE == kLora ? 1 : g.groups) * N * zbw;
@@ -226,77 +233,134 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
         dma16(codes, buffer(b) + (r * 2 + d) * 64, vq[r][d], at);
   };
   // Buffer b's codes into registers: this lane's 32 channels of weight row c16 of every tile and
-  // step (3-bit: two low-plane words and one of the high plane). The DMAs sent after buffer b's
-  // are those of the other buffers, so vmcnt(their number) covers buffer b whatever else was
-  // sent in between; the LDS reads end before the block does.
+  // step (stream_words). The DMAs sent after buffer b's are those of the other buffers, so
+  // vmcnt(their number) covers buffer b whatever else was sent in between; the LDS reads end before
+  // the block does.
   constexpr int kLater = (NB - 1) * R * 2;
-  auto take_codes = [&](int b, bool more, uint32_t (&w)[H][R][BITS]) AWQ_INLINE {
+  const int swz = c16 >> 1;
+  auto take_codes = [&](int b, bool more, uint32_t (&w)[H][R][W]) AWQ_INLINE {
     if (more)
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
     else  // nothing is sent behind the last position's
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int h = 0; h < H; ++h)
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)buffer(b);
+    if constexpr (BITS == 3) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint32_t base = (uint32_t)(uintptr_t)(lds_void*)(buffer(b) + r * 128);
-        if constexpr (BITS == 3) {
-          const uint32_t at = base + (c16 * 24 + h * 12) * 4;
-          uint2 lo;
-          asm volatile("ds_read_b64 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-                       : "=&v"(lo), "=&v"(w[h][r][2])
-                       : "v"(at + kg * 8), "v"(at + 32 + kg * 4)
-                       : "memory");
-          w[h][r][0] = lo.x;
-          w[h][r][1] = lo.y;
-        } else if constexpr (BITS == 8) {
-          const uint32_t row = base + c16 * 128;
-          u32x4 v0, v1;
-          asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-                       : "=&v"(v0), "=&v"(v1)
-                       : "v"(row + ((2 * kg) ^ (c16 >> 1)) * 16), "v"(row + ((2 * kg + 1) ^ (c16 >> 1)) * 16)
-                       : "memory");
+        const uint32_t row = at + r * 2048 + c16 * 96;
+        if constexpr (GS == 1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[h][r][i] = v0[i];
-            w[h][r][4 + i] = v1[i];
+          for (int h = 0; h < H; ++h) {
+            uint2 lo;
+            asm volatile("ds_read_b64 %0, %2\n\tds_read_b32 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(lo), "=&v"(w[h][r][2])
+                         : "v"(row + h * 48 + kg * 8), "v"(row + h * 48 + 32 + kg * 4)
+                         : "memory");
+            w[h][r][0] = lo.x;
+            w[h][r][1] = lo.y;
           }
+        } else {
+          // slice i of a step: half of low word 2 i + kg / 2 and a quarter of high word i
+          uint2 lo[4];
+          u32x4 hi[2];
+          asm volatile(
+              "ds_read2_b32 %0, %6 offset0:0 offset1:2\n\tds_read2_b32 %1, %6 offset0:4 offset1:6\n\t"
+              "ds_read2_b32 %2, %6 offset0:12 offset1:14\n\tds_read2_b32 %3, %6 offset0:16 offset1:18\n\t"
+              "ds_read_b128 %4, %7\n\tds_read_b128 %5, %7 offset:48\n\ts_waitcnt lgkmcnt(0)"
+              : "=&v"(lo[0]), "=&v"(lo[1]), "=&v"(lo[2]), "=&v"(lo[3]), "=&v"(hi[0]), "=&v"(hi[1])
+              : "v"(row + (kg >> 1) * 4), "v"(row + 32)
+              : "memory");
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t low = (i & 1 ? lo[2 * h + (i >> 1)].y : lo[2 * h + (i >> 1)].x) >> (8 * (kg & 1));
+              const uint32_t high = __builtin_amdgcn_alignbit(hi[h][i], hi[h][i], (4 * kg - 8) & 31);
+              w[h][r][i] = (low & 0xF0FFF0FFu) | (high & 0x0F000F00u);
+            }
         }
       }
-    if constexpr (BITS == 4) {
-      // both steps of two tiles per block: four reads in flight
+    } else {
+      // both steps (8-bit: the step) of two tiles per block: their reads in flight together
 #pragma unroll
       for (int r = 0; r < R; r += 2) {
-        const uint32_t row = (uint32_t)(uintptr_t)(lds_void*)(buffer(b) + r * 128) + c16 * 128;
-        u32x4 v[4];
-        asm volatile(
-            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:2048\n\t"
-            "ds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
-            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
-            : "v"(row + (kg ^ (c16 >> 1)) * 16), "v"(row + ((4 + kg) ^ (c16 >> 1)) * 16)
-            : "memory");
+        const uint32_t row = at + r * 2048 + c16 * 128;
+        if constexpr (BITS == 8 && GS == 1) {
+          u32x4 v[4];
+          asm volatile(
+              "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:2048\n\t"
+              "ds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+              : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+              : "v"(row + ((2 * kg) ^ swz) * 16), "v"(row + ((2 * kg + 1) ^ swz) * 16)
+              : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[i & 1][r + (i >> 1)][k] = v[i][k];
+            for (int k = 0; k < 4; ++k) w[0][r + (i >> 1)][4 * (i & 1) + k] = v[i][k];
+        } else if constexpr (BITS == 8) {
+          // slice i: 8 bytes of piece 2 i + kg / 2
+          const uint32_t half = row + (kg & 1) * 8;
+          u32x4 v[4];
+          asm volatile(
+              "ds_read2st64_b64 %0, %4 offset0:0 offset1:4\n\tds_read2st64_b64 %1, %5 offset0:0 offset1:4\n\t"
+              "ds_read2st64_b64 %2, %6 offset0:0 offset1:4\n\tds_read2st64_b64 %3, %7 offset0:0 offset1:4\n\t"
+              "s_waitcnt lgkmcnt(0)"
+              : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+              : "v"(half + ((kg >> 1) ^ swz) * 16), "v"(half + ((2 + (kg >> 1)) ^ swz) * 16),
+                "v"(half + ((4 + (kg >> 1)) ^ swz) * 16), "v"(half + ((6 + (kg >> 1)) ^ swz) * 16)
+              : "memory");
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[0][r + (k >> 1)][2 * i + (k & 1)] = v[i][k];
+        } else if constexpr (GS == 1) {
+          u32x4 v[4];
+          asm volatile(
+              "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:2048\n\t"
+              "ds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+              : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+              : "v"(row + (kg ^ swz) * 16), "v"(row + ((4 + kg) ^ swz) * 16)
+              : "memory");
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[i & 1][r + (i >> 1)][k] = v[i][k];
+        } else {
+          // slice i of step h: word kg of piece 4 h + i
+          const uint32_t word = row + kg * 4;
+          uint2 v[8];
+          asm volatile(
+              "ds_read2st64_b32 %0, %8 offset0:0 offset1:8\n\tds_read2st64_b32 %1, %9 offset0:0 offset1:8\n\t"
+              "ds_read2st64_b32 %2, %10 offset0:0 offset1:8\n\tds_read2st64_b32 %3, %11 offset0:0 offset1:8\n\t"
+              "ds_read2st64_b32 %4, %12 offset0:0 offset1:8\n\tds_read2st64_b32 %5, %13 offset0:0 offset1:8\n\t"
+              "ds_read2st64_b32 %6, %14 offset0:0 offset1:8\n\tds_read2st64_b32 %7, %15 offset0:0 offset1:8\n\t"
+              "s_waitcnt lgkmcnt(0)"
+              : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+              : "v"(word + (0 ^ swz) * 16), "v"(word + (1 ^ swz) * 16), "v"(word + (2 ^ swz) * 16),
+                "v"(word + (3 ^ swz) * 16), "v"(word + (4 ^ swz) * 16), "v"(word + (5 ^ swz) * 16),
+                "v"(word + (6 ^ swz) * 16), "v"(word + (7 ^ swz) * 16)
+              : "memory");
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w[i >> 2][r][i & 3] = v[i].x;
+            w[i >> 2][r + 1][i & 3] = v[i].y;
+          }
+        }
       }
     }
   };
   struct ScaleZero {
-    Eight sc[G128 ? 1 : L], z[!G128 && BITS == 8 ? 2 : 1];  // as many as the group size asks for
+    Eight sc[L * GS * 2 / 8], z[BITS == 8 && GS == 4 ? 2 : 1];
   };
   auto load_scales = [&](ScaleZero& q) AWQ_INLINE {
     int s = step_of(ld.part, 0);
     s = s < nsteps ? s : 0;
     const int64_t n = expert_row + first(ld.chunk) + my_row;
-    const int64_t as = (n * Gs + s * per) * 2, az = n * zbw + (BITS == 8 ? s * per : s * per / 2);
-    q.sc[0] = load8(g.scales, as, sbytes);
-    q.z[0] = load8(g.zeros, az, zbytes);
-    if constexpr (!G128) {  // the most that 32-channel groups need
+    const int64_t as = (n * Gs + s * GS) * 2, az = n * zbw + (BITS == 8 ? s * GS : s * GS / 2);
 #pragma unroll
-      for (int i = 1; i < L; ++i) q.sc[i] = load8(g.scales, as + 8 * i, sbytes);
-      if constexpr (BITS == 8) q.z[1] = load8(g.zeros, az + 8, zbytes);
-    }
+    for (int i = 0; i < L * GS * 2 / 8; ++i) q.sc[i] = load8(g.scales, as + 8 * i, sbytes);
+    q.z[0] = load8(g.zeros, az, zbytes);
+    if constexpr (BITS == 8 && GS == 4) q.z[1] = load8(g.zeros, az + 8, zbytes);
   };
 
   half8w a[L][4];  // this wave's part of the tile's rows of X
@@ -304,13 +368,14 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     const int r = c16;  // rows past the last read the last one, never stored
     int xr = it.rows > 0 ? source(it.row0 + (r < it.rows ? r : it.rows - 1)) : 0;
     if (MODE != kLora && g.order) xr = (int)((unsigned)xr / (unsigned)g.fan);
-    const uint16_t* const x = g.X + (int64_t)xr * K + kg * 32;
+    constexpr int kOwn = GS == 1 ? 32 : 8, kSlice = GS == 1 ? 8 : 32;  // channels between lanes, between slices
+    const uint16_t* const x = g.X + (int64_t)xr * K + kg * kOwn;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       const int s = step_of(it.part, j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        a[j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * 8);
+        a[j][i] = *reinterpret_cast<const half8w*>(x + (s < nsteps ? s : nsteps - 1) * kGroup + i * kSlice);
         if (s >= nsteps) a[j][i] = half8w{};  // steps past the last add nothing
       }
     }
@@ -321,74 +386,68 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
   };
-  // A slice's scales and zeros of this lane's weight row of tile r, fetched from the lane that
-  // loaded them.
-  struct Fetched {
-    uint32_t sc[R][G128 ? L / 2 : 2 * L], z[R][G128 ? 1 : BITS == 8 ? L : 2];
+  // The scales and zeros of the wave's steps as this lane loaded them, and their 32-bit words for
+  // this lane's weight row of tile r, from the lane that loaded that: all at once where they are few
+  // (128-channel groups), else when they are used (all of them would take the registers of a tile).
+  constexpr int kScaleWords = L * GS / 2, kZeroWords = BITS == 8 ? L * GS / 4 : (L * GS + 7) / 8;
+  struct Steps {
+    uint64_t sc[(kScaleWords + 1) / 2], z[(kZeroWords + 1) / 2];
+    uint32_t sc_of[GS == 1 ? R : 1][kScaleWords], z_of[GS == 1 ? R : 1][kZeroWords];
   };
-  auto fetch_all = [&](Fetched& f, const ScaleZero& q) AWQ_INLINE {
-    auto get = [&](const Eight* e, int at, int r) AWQ_INLINE -> uint32_t {
-      const uint32_t v = (uint32_t)(e[at / 2].value() >> (32 * (at & 1)));
-      return (uint32_t)__builtin_amdgcn_ds_bpermute((r * 16 + c16) * 4, (int)v);
-    };
+  auto fetch = [&](const uint64_t* e, int word, int r) AWQ_INLINE -> uint32_t {
+    return (uint32_t)__builtin_amdgcn_ds_bpermute((r * 16 + c16) * 4, (int)(uint32_t)(e[word / 2] >> (32 * (word & 1))));
+  };
+  auto take_scales = [&](Steps& f, const ScaleZero& q) AWQ_INLINE {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int i = 0; i < (kScaleWords + 1) / 2; ++i) f.sc[i] = q.sc[i].value();
 #pragma unroll
-      for (int i = 0; i < (G128 ? L / 2 : 2 * L); ++i) f.sc[r][i] = get(q.sc, i, r);
+    for (int i = 0; i < (kZeroWords + 1) / 2; ++i) f.z[i] = q.z[i].value();
+    if constexpr (GS == 1) {
 #pragma unroll
-      for (int i = 0; i < (G128 ? 1 : BITS == 8 ? L : 2); ++i) f.z[r][i] = get(q.z, i, r);
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < kScaleWords; ++i) f.sc_of[r][i] = fetch(f.sc, i, r);
+#pragma unroll
+        for (int i = 0; i < kZeroWords; ++i) f.z_of[r][i] = fetch(f.z, i, r);
+      }
     }
   };
-  // Step j of the wave's slice, codes w; on: the step exists. The R weight tiles are independent
+  auto scale_word = [&](const Steps& f, int word, int r) AWQ_INLINE -> uint32_t {
+    return GS == 1 ? f.sc_of[GS == 1 ? r : 0][word] : fetch(f.sc, word, r);
+  };
+  auto zero_word = [&](const Steps& f, int word, int r) AWQ_INLINE -> uint32_t {
+    return GS == 1 ? f.z_of[GS == 1 ? r : 0][word] : fetch(f.z, word, r);
+  };
+  // Step j of the wave's part, codes w; on: the step exists. The R weight tiles are independent
   // chains, walked side by side.
-  auto multiply_128 = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
-    f32x4w d[R];
-    float f[R];
-    ZeroPair zp[R];
+  auto multiply = [&](const uint32_t (&w)[R][W], int j, bool on, const Steps& q) AWQ_INLINE {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t sc = q.sc[r][j / 2] >> (16 * (j & 1));
-      f[r] = on ? h2f((uint16_t)sc) : 0.0f;
-      zp[r] = zero_pair(BITS == 8 ? (q.z[r][0] >> (8 * j)) & 0xFF : (q.z[r][0] >> (4 * j)) & 0xF);
-      d[r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int gi = 0; gi < GS; ++gi) {
+      const int at = j * GS + gi;  // the group among those of the wave's steps
+      f32x4w d[R];
+      float f[R];
+      ZeroPair zp[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const half8w v = centered<BITS>(w[r], s, zp[r], magic);
-        d[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], v, d[r], 0, 0, 0);
+        const uint32_t sc = scale_word(q, at / 2, r) >> (16 * (at & 1));
+        f[r] = on ? h2f((uint16_t)sc) : 0.0f;
+        zp[r] = zero_pair(BITS == 8 ? (zero_word(q, at / 4, r) >> (8 * (at & 3))) & 0xFF : (zero_word(q, at / 8, r) >> (4 * (at & 7))) & 0xF);
+        d[r] = f32x4w{0.0f, 0.0f, 0.0f, 0.0f};
       }
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int s = gi * 4 / GS; s < (gi + 1) * 4 / GS; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(f[r], d[r][i], acc[r][i]);
-  };
-  auto multiply_small = [&](const uint32_t (&w)[R][BITS], int j, bool on, const Fetched& q) AWQ_INLINE {
-    // this lane's group of the step: per j + (kg >> gsh) within the slice
-    half2w c[R];
-    ZeroPair zp[R];
+        for (int r = 0; r < R; ++r)
+          d[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], centered<BITS>(w[r], s, zp[r], magic), d[r], 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      // (both forms' words first: choosing between their places would put the array in memory)
-      const uint32_t a1 = q.sc[r][j], a2 = q.sc[r][2 * j], a3 = q.sc[r][2 * j + 1];
-      const uint32_t z1 = q.z[r][BITS == 8 ? j / 2 : 0], z2 = q.z[r][BITS == 8 ? j : j / 2];
-      uint32_t sc = gsh == 1 ? a1 : kg & 2 ? a3 : a2;
-      sc >>= 16 * (gsh == 1 ? kg >> 1 : kg & 1);
-      const uint32_t z = BITS == 8 ? (gsh == 1 ? z1 >> (16 * (j & 1) + 8 * (kg >> 1)) : z2 >> (8 * kg))
-                                   : (gsh == 1 ? z1 >> (8 * j + 4 * (kg >> 1)) : z2 >> (16 * (j & 1) + 4 * kg));
-      sc = on ? sc & 0xFFFF : 0;
-      c[r] = __builtin_bit_cast(half2w, sc | (sc << 16));
-      zp[r] = zero_pair(z & (BITS == 8 ? 0xFF : 0xF));
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(f[r], d[r][i], acc[r][i]);
     }
+    if constexpr (GS > 1) {  // (left to itself the compiler takes the sums a step later and spills the partial tiles)
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const half8w v = centered<BITS>(w[r], s, zp[r], magic) *
-                         half8w{c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1], c[r][0], c[r][1]};
-        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[j][s], v, acc[r], 0, 0, 0);
-      }
+      for (int r = 0; r < R; ++r) asm volatile("" : "+v"(acc[r]));
+    }
   };
   // Adapters among the tile's rows in order of their first row, shared by the waves: their
   // terms start the accumulators, while the item's codes are on their way.
@@ -511,8 +570,8 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   load_x(it);
   while (true) {
     const bool more = todo > 1;
-    Fetched f;
-    fetch_all(f, q);
+    Steps f;
+    take_scales(f, q);
     if (more) {
       next();  // ld is a position ahead of it
       load_scales(q);
@@ -520,7 +579,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     if (MODE == kLora && it.part == 0) adapters(it);
 #pragma unroll
     for (int i = 0; i < L / H; ++i) {
-      uint32_t w[H][R][BITS];
+      uint32_t w[H][R][W];
       take_codes(i, more, w);
       if (more) load_codes(i, i);
 #pragma unroll
@@ -533,13 +592,10 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int k = 0; k < BITS; ++k) w[0][r][k] = w[H - 1][r][k];
+              for (int k = 0; k < W; ++k) w[0][r][k] = w[H - 1][r][k];
           }
         }
-        if constexpr (G128)
-          multiply_128(w[h], H * i + h, s < nsteps, f);
-        else
-          multiply_small(w[h], H * i + h, s < nsteps, f);
+        multiply(w[h], H * i + h, s < nsteps, f);
       }
     }
     if (it.part == parts - 1) finish(it);
@@ -551,28 +607,29 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
 }
 
 // The variants that the launcher picks from: s waves.
-template <int MODE, int BITS, bool G128, int R>
+template <int MODE, int BITS, int GS, int R>
 void launch_stream_r(const GroupedArgs& g, int s, dim3 grid, hipStream_t stream) {
   constexpr int L = kStreamSteps;
   if (s == 2)
-    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 2>), grid, dim3(128), 0, stream, g);
+    hipLaunchKernelGGL((k_stream<MODE, BITS, GS, R, L, 2>), grid, dim3(128), 0, stream, g);
   else if (s == 4)
-    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 4>), grid, dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((k_stream<MODE, BITS, GS, R, L, 4>), grid, dim3(256), 0, stream, g);
   else
-    hipLaunchKernelGGL((k_stream<MODE, BITS, G128, R, L, 8>), grid, dim3(512), 0, stream, g);
+    hipLaunchKernelGGL((k_stream<MODE, BITS, GS, R, L, 8>), grid, dim3(512), 0, stream, g);
 }
 
-template <int MODE, int BITS, bool G128>
+template <int MODE, int BITS, int GS>
 void launch_stream_g(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
   constexpr int R = stream_cols(BITS, false) / 16, kNarrow = stream_cols(BITS, true) / 16;
-  if (narrow) launch_stream_r<MODE, BITS, G128, kNarrow>(g, s, grid, stream);
-  else launch_stream_r<MODE, BITS, G128, R>(g, s, grid, stream);
+  if (narrow) launch_stream_r<MODE, BITS, GS, kNarrow>(g, s, grid, stream);
+  else launch_stream_r<MODE, BITS, GS, R>(g, s, grid, stream);
 }
 
 template <int MODE, int BITS>
 void launch_stream_t(const GroupedArgs& g, bool narrow, int s, dim3 grid, hipStream_t stream) {
-  if (g.group == 128) launch_stream_g<MODE, BITS, true>(g, narrow, s, grid, stream);
-  else launch_stream_g<MODE, BITS, false>(g, narrow, s, grid, stream);
+  if (g.group == 128) launch_stream_g<MODE, BITS, 1>(g, narrow, s, grid, stream);
+  else if (g.group == 64) launch_stream_g<MODE, BITS, 2>(g, narrow, s, grid, stream);
+  else launch_stream_g<MODE, BITS, 4>(g, narrow, s, grid, stream);
 }
 
 }  // namespace awq
