@@ -30,9 +30,9 @@
 // times the blocks for batches whose tiles would leave the chip idle, at four times A's traffic
 // (64 rows x 4096 x 4096 with adapters 61 us -> 24). grouped_gemm.hip picks.
 //
-// What bounds it: large groups, the issue of one wave per SIMD (matrix cores 45% busy, vector
-// instructions 23%) and the chip's power: 8 experts x 22016 x 4096 gated, 8192 rows, 1601 us in a
-// row of them, 923 TFLOP/s (a library fp16 product of 8192^3 reaches 1323). Middling
+// What bounds it: large groups, the issue of one wave per SIMD (matrix cores 44% busy, vector
+// instructions 23%) and the chip's power: 8 experts x 22016 x 4096 gated, 8192 rows, 1586 us in a
+// row of them, 932 TFLOP/s (a library fp16 product of 8192^3 reaches 1323). Middling
 // groups, the widening, whose cost does not depend on the rows. K of few steps, a tile's start:
 // offsets, row indices, first operands, 4 to 5 us before the first product.
 //

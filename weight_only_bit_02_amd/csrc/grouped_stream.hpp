@@ -35,10 +35,11 @@
 //     columns twice, to the same values.
 //
 // What bounds it: the widening and the stream together; large launches reach three quarters of
-// what a copy reaches, more with 8-bit codes. 64 experts x 4096 x 1024, 384 rows: 36.5 us, 3.9
+// what a copy reaches, more with 8-bit codes. 64 experts x 4096 x 1024, 384 rows: 36.3 us, 4.0
 // TB/s; 8 experts x 22016 x 4096 gated, 64 rows: 81 us, 4.6 TB/s; 8 experts x 2048 x 2048 gated, a
-// row each: 9.2 us, of which the chain offsets, row, first codes, sums is most. 3-bit codes cost
-// more instructions per byte: 64 x 2048 x 2048, 512 rows, 37 us.
+// row each: 9.3 us, of which the chain offsets, row, first codes, sums is most. 3-bit codes cost
+// more instructions per byte: 64 x 2048 x 2048, 512 rows, 37 us. Groups of 64 and 32 cost more scales
+// and partial tiles: 64 x 4096 x 1024, 512 rows, 4-bit, 34, 37 and 41 us.
 //
 // Gated: tiles 0 .. R / 2 - 1 are gate rows, the rest their up rows, so a lane's sums hold
 // both and the epilogue needs no exchange. Adapters: as in grouped_gemm.hpp; the waves share
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
   __shared__ __attribute__((aligned(16))) uint4 st2[NB > 2 ? S : 1][NB > 2 ? kBuf : 1];
   __shared__ __attribute__((aligned(16))) uint4 st3[NB > 2 ? S : 1][NB > 2 ? kBuf : 1];
   __shared__ __attribute__((aligned(16))) f32x4w red[S * R * 64];
-  static_assert(L == 2 || L == 4, "steps of a wave");
+  static_assert(L == 4, "the scales and zeros of four steps are loaded eight bytes at a time");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, kg = lane >> 4;
   const int64_t N = g.N, K = g.K, nh = N / 2;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     }
   };
   struct ScaleZero {
-    Eight sc[L * GS * 2 / 8], z[BITS == 8 && GS == 4 ? 2 : 1];
+    Eight sc[GS], z[BITS == 8 && GS == 4 ? 2 : 1];  // eight bytes: the scales of a group of all four steps
   };
   auto load_scales = [&](ScaleZero& q) AWQ_INLINE {
     int s = step_of(ld.part, 0);
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(S * 64) __attribute__((amdgpu_waves_per_eu(2))
     const int64_t n = expert_row + first(ld.chunk) + my_row;
     const int64_t as = (n * Gs + s * GS) * 2, az = n * zbw + (BITS == 8 ? s * GS : s * GS / 2);
 #pragma unroll
-    for (int i = 0; i < L * GS * 2 / 8; ++i) q.sc[i] = load8(g.scales, as + 8 * i, sbytes);
+    for (int i = 0; i < GS; ++i) q.sc[i] = load8(g.scales, as + 8 * i, sbytes);
     q.z[0] = load8(g.zeros, az, zbytes);
     if constexpr (BITS == 8 && GS == 4) q.z[1] = load8(g.zeros, az + 8, zbytes);
   };

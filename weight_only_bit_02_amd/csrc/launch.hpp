@@ -180,10 +180,10 @@ bool grouped_stream_supported(int64_t weights, int64_t N, int64_t K, int group, 
 hipError_t launch_grouped_stream(GroupedArgs g, int mode, int w_bit, hipStream_t stream);
 // AWQ_GROUPED_AUTO streams up to these rows (mean per group of experts; adapters: all) and
 // takes the GEMM beyond. Streaming and the best GEMM, in us: 64 experts x 4096 x 1024, 24 rows
-// each 53 and 60, 32 rows 69 and 63; 8 x 22016 x 4096 gated 122 and 130, 175 and 150; 64 x 2048 x
-// 2048 gated, 16 rows 46 and 46, 24 rows 59 and 47; 8-bit, 64 x 2048 x 1152, 16 rows 45 and 41, 24
-// rows 57 and 43; 3-bit, 64 x 2048 x 2048, 16 rows 53 and 53, 24 rows 68 and 57; adapters on 4096 x
-// 4096, 64 rows 17 and 23, on 11008 x 4096, 16 rows 18 and 21, 64 rows 29 and 26.
+// each 53 and 60, 32 rows 68 and 62; 8 x 22016 x 4096 gated 123 and 129, 178 and 144; 64 x 2048 x
+// 2048 gated, 16 rows 45 and 43, 24 rows 59 and 47; 8-bit, 64 x 2048 x 1152, 16 rows 45 and 42, 24
+// rows 56 and 43; 3-bit, 64 x 2048 x 2048, 16 rows 53 and 53, 24 rows 67 and 57; adapters on 4096 x
+// 4096, 64 rows 17 and 23, on 11008 x 4096, 16 rows 18 and 21, 64 rows 30 and 26.
 constexpr int skinny_mean_rows(int w_bit) { return w_bit == 4 ? 24 : 16; }
 constexpr int kLoraSkinnyRows = 64;
 int choose_grouped_gemm(const GroupedArgs& g, int mode, int w_bit);

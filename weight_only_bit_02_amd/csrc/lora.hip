@@ -11,7 +11,7 @@
 // stored so that the reads have no bank conflicts. The sums are fp32; a row's 32 values then
 // leave as fp16 hi + lo under one power of two: 22 significant bits of the largest, for the
 // matrix cores of the second product. Bound by latency (ids, first step, sums): one row x 4096,
-// rank 16: 4.3 us; 48 rows of 32 adapters, rank 32: 7.4; 2048 rows in runs, rank 16: 8.4.
+// rank 16: 4.5 us; 48 rows of 32 adapters, rank 32: 7.1; 2048 rows in runs, rank 16: 8.3.
 #include "common.hpp"
 #include "groups.hpp"
 #include "launch.hpp"

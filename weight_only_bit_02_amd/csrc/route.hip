@@ -18,9 +18,9 @@
 // two: the first writes each block's count per group, key by key, the second sums the counts of
 // the blocks before it (at most kMaxBlocks per key, from L2) and places its run.
 //
-// Bound by latency: one token, 8 of 64 experts: 5.2 us; 2048 rows by 32 adapters: 4.9 us. 8191
-// tokens, 8 of 128: 9.2 us for the choice, by its 423 instructions a token (eight maxima in turn),
-// and 9.2 for the placement (every block sums the counts of all 256).
+// Bound by latency: one token, 8 of 64 experts: 5.3 us; 2048 rows by 32 adapters: 4.8 us. 8191
+// tokens, 8 of 128: 10.1 us for the choice, by its 423 instructions a token (eight maxima in turn),
+// and 8.6 for the placement (every block sums the counts of all 256).
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
