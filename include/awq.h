@@ -466,6 +466,110 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
                                  void* workspace, size_t workspace_bytes, uint32_t* flags,
                                  awq_grouped_kernel kernel, void* stream);
 
+/*
+ * ---------------------------------------------------------------- key / value cache
+ * The attention of a decoder layer beside its packed linears, with keys and values held in
+ * 4 bits in pages that sequences take as they grow. The q|k|v linear's output goes through
+ * awq_kv_append, which rotates queries and keys by position and puts the keys and values
+ * into the cache; awq_attention_kv4 attends over the cache, the appended tokens among
+ * them; the o linear takes its output. All sizes of the sequences stand on the device: a
+ * captured graph serves growing sequences.
+ *
+ * Format: per token, head and group of group_size channels one 16-bit parameter: the fp16
+ * bits of a scale of 7 significant bits (the low four are zero) with the zero z in the low
+ * four; value = (code - z) scale, exact in fp16. Codes, 4 bits:
+ *   k_codes  [pages][kv_heads][page_size][D/2] bytes, D = head_dim. A token's row is D/8 words
+ *            of 32 bits: word h (D/32) + s holds channels 32 s + 8 h + i, i = 0..7, with nibble
+ *            order as in qweight (nibble j holds i = (0,2,4,6,1,3,5,7)[j])
+ *   v_codes  the same size; 16 tokens together, as 16-bit words [4][16][D/64][4]: word
+ *            (h, c, w, i) holds token 4 h + i's channels c + 16 (4 w + j) in nibble j
+ *   k_params, v_params  16-bit [pages][kv_heads][D/group_size][page_size]
+ * head_dim 64, 128 or 256; group_size 32, 64 or 128, at most head_dim; page_size a power of
+ * two from 16 to 4096 (else AWQ_ERR_UNSUPPORTED). The cache may pass 4 GiB.
+ */
+#define AWQ_MAX_HEADS 1024
+#define AWQ_MAX_SEQUENCES 65536
+
+typedef struct awq_kv_cache {
+  void *k_codes, *k_params, *v_codes, *v_params; /* device, 16-byte aligned */
+  int64_t pages;
+  int32_t page_size, kv_heads, head_dim, group_size;
+} awq_kv_cache;
+
+/* A batch of rows (tokens), those of one sequence together, the newest tokens of each:
+ * row rows[s] + i of sequence s is the token at position lengths[s] - n + i of its n rows.
+ *   rows        int32 [seqs + 1]  rows[0] = 0; rows from rows[seqs] on belong to none: their
+ *                                 outputs are left as they were
+ *   lengths     int32 [seqs]      tokens of the sequence in the cache, those of its rows among
+ *                                 them; 0: an empty sequence
+ *   page_table  int32 [seqs][max_pages]  the page of each page_size tokens; outside
+ *                                 [0, pages): no page (not written, not attended to)
+ *   n_rows      rows of the tensors, below 2^22; max_rows: no sequence has more (n_rows is
+ *               always right; a smaller bound lets short rows take a shorter path)
+ * A row before position 0 is no token: nothing is written for it, it attends to nothing.
+ * A page that two sequences share is to be written by neither. */
+typedef struct awq_kv_batch {
+  const int32_t *rows, *lengths, *page_table;
+  int64_t n_rows;
+  int32_t seqs, max_pages, max_rows;
+} awq_kv_batch;
+
+/*
+ * awq_kv_append -- the rows' keys and values into the cache, rotated by position.
+ *   k, v     fp16 [n_rows][k_ld], [n_rows][v_ld]: kv_heads x head_dim values a row (parts of
+ *            the q|k|v linear's rows; the row strides are multiples of 8)
+ *   q        fp16 [n_rows][q_ld] or NULL: q_heads x head_dim values a row, rotated to q_out
+ *            (fp16 [n_rows][q_out_ld]; may be q itself with the same stride)
+ *   cos_sin  fp32 [positions][rotary_dim] or NULL (no rotation; q is then NULL): cos of the
+ *            position's rotary_dim / 2 angles, then sin. Positions from `positions` on take
+ *            the last row. rotary_dim: a multiple of 16 up to head_dim, the first channels
+ *   interleaved = 0: channels i and i + rotary_dim / 2 are a pair; 1: 2 i and 2 i + 1
+ *     (a, b) -> (a cos - b sin, b cos + a sin), in fp64, rounded to fp32, then to fp16
+ *   Keys and values x of a group, in fp32 with round-to-nearest-even:
+ *     lo = min(0, min x), hi = max(0, max x); scale = (hi - lo) / 15 rounded up to 7
+ *     significant bits, within [2^-14, 4352]; z = clamp(rint(-lo / scale), 0, 15);
+ *     code = clamp(rint(x / scale) + z, 0, 15).
+ *   flags    NONFINITE_INPUT (Inf or NaN in the rows' q, k or v: the group is unspecified),
+ *            OVERFLOW (a rotated value passed fp16), SCALE_CLAMPED
+ */
+awq_status awq_kv_append(const awq_kv_cache* cache, const awq_kv_batch* batch, const void* k,
+                         int64_t k_ld, const void* v, int64_t v_ld, const void* q, int64_t q_ld,
+                         int32_t q_heads, void* q_out, int64_t q_out_ld, const float* cos_sin,
+                         int64_t positions, int32_t rotary_dim, int32_t interleaved,
+                         uint32_t* flags, void* stream);
+
+/*
+ * awq_kv_read -- the values that the cache holds for the batch's rows (exact):
+ *   k, v  fp16 [n_rows][kv_heads][head_dim] out; zeros for a row that has no page. Whole
+ *         sequences: rows with n = lengths[s].
+ */
+awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, void* k, void* v,
+                       void* stream);
+
+/*
+ * awq_attention_kv4 -- attention of the batch's rows over their sequences in the cache:
+ *     out[r][h] = sum_t softmax_t(scale q[r][h] . k_t) v_t,  k, v of head h / (q_heads / kv_heads)
+ *   over the tokens t < lengths[s] that have a page; causal = 1: t <= the row's position p;
+ *   window > 0: t > p - window. A row without a token: zeros (lse -inf).
+ *   q        fp16 [n_rows][q_ld], out fp16 [n_rows][out_ld]: q_heads x head_dim values a row,
+ *            strides multiples of 8; q_heads a multiple of kv_heads
+ *   scale    above 0 (1 / sqrt(head_dim) as a rule)
+ *   lse      fp32 [n_rows][q_heads] or NULL: log of the sum of exp(scale q . k_t)
+ *   workspace device scratch of awq_attention_kv4_workspace_size bytes (max_tokens = max_pages
+ *            page_size), 16-byte aligned; 0 where nothing is split. One for each of the
+ *            calls that overlap
+ *   Scores, softmax and sums in fp32. An Inf or NaN in q reaches its own row and head only.
+ *   n_rows q_heads < 2^24, (n_rows q_heads / kv_heads / 16 + seqs) kv_heads (max_tokens / 256
+ *   + 1) < 2^31 (else BAD_SHAPE).
+ */
+size_t awq_attention_kv4_workspace_size(int64_t n_rows, int32_t seqs, int32_t max_rows,
+                                        int64_t max_tokens, int32_t q_heads, int32_t kv_heads,
+                                        int32_t head_dim);
+awq_status awq_attention_kv4(const void* q, int64_t q_ld, int32_t q_heads,
+                             const awq_kv_cache* cache, const awq_kv_batch* batch, float scale,
+                             int32_t causal, int64_t window, void* out, int64_t out_ld, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Largest M served by a GEMV-class kernel under AWQ_LINEAR_AUTO with 4-bit codes (64, or
  * the value of the AWQ_GEMV_MAX_M environment variable clamped to 0..64, read at library
  * load). */

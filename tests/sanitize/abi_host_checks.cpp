@@ -104,6 +104,23 @@ int main() {
   EXPECT(awq_peak_read_stream(F, 4095, Fu, 4, nullptr), 2);
   EXPECT(awq_peak_mfma(0, (float*)F, 16, nullptr), 2);
 
+  // key / value cache
+  awq_kv_cache kc{F, F, F, F, 10, 16, 2, 128, 128};
+  awq_kv_batch kb{(int32_t*)F, (int32_t*)F, (int32_t*)F, 5, 2, 100, 5};
+  const size_t kv = awq_attention_kv4_workspace_size(5, 2, 5, 1600, 4, 2, 128);
+  if (kv == 0) ++failures;
+  EXPECT(awq_attention_kv4(F, 512, 4, &kc, &kb, 0.1f, 1, 0, F, 512, nullptr, F, kv - 1, nullptr), AWQ_ERR_WORKSPACE);
+  EXPECT(awq_attention_kv4(F, 512, 4, &kc, &kb, 0.1f, 1, -1, F, 512, nullptr, F, kv, nullptr), AWQ_ERR_BAD_SHAPE);
+  EXPECT(awq_attention_kv4_workspace_size((1 << 22) - 1, 65536, 1, (1 << 30) - 1, 1024, 1, 256), 0);
+  EXPECT(awq_kv_append(&kc, &kb, F, INT64_MAX, F, 256, nullptr, 0, 0, nullptr, 0, nullptr, 0, 0, 0, nullptr, nullptr),
+         AWQ_ERR_BAD_SHAPE);
+  EXPECT(awq_kv_append(&kc, &kb, F, 256, F, 256, F, 512, 4, F, 512, nullptr, 0, 0, 0, nullptr, nullptr), AWQ_ERR_NULL_POINTER);
+  kb.max_pages = INT32_MAX;
+  EXPECT(awq_kv_read(&kc, &kb, F, F, nullptr), AWQ_ERR_BAD_SHAPE);
+  kb.max_pages = 100;
+  kc.page_size = INT32_MIN;
+  EXPECT(awq_kv_read(&kc, &kb, F, F, nullptr), AWQ_ERR_UNSUPPORTED);
+
   free(cfg);
   free(bad);
   if (failures) {

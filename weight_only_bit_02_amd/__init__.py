@@ -14,3 +14,6 @@ from .grouped import (  # noqa: F401
     linear_w4a16_lora_workspace_size, moe_combine, moe_route, moe_route_workspace_size,
     quantize_pack_experts,
 )
+from .kv import (  # noqa: F401
+    KVBatch, KVCache, Rotary, alloc_kv_cache, attention_kv4, attention_kv4_workspace_size, kv_append, kv_read,
+)

@@ -29,10 +29,24 @@ class AwqConfig(C.Structure):
                 ("n_grid", C.c_int32)]
 
 
+class KvCache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("k_params", C.c_void_p), ("v_codes", C.c_void_p),
+                ("v_params", C.c_void_p), ("pages", C.c_int64), ("page_size", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("group_size", C.c_int32)]
+
+
+class KvBatch(C.Structure):
+    _fields_ = [("rows", C.c_void_p), ("lengths", C.c_void_p), ("page_table", C.c_void_p),
+                ("n_rows", C.c_int64), ("seqs", C.c_int32), ("max_pages", C.c_int32),
+                ("max_rows", C.c_int32)]
+
+
 P = C.c_void_p
 I64 = C.c_int64
 I32 = C.c_int32
 CFG = C.POINTER(AwqConfig)
+KVC = C.POINTER(KvCache)
+KVB = C.POINTER(KvBatch)
 
 # name -> (restype, argtypes); every name here is exported by the library
 SIGNATURES = {
@@ -65,6 +79,11 @@ SIGNATURES = {
     "awq_linear_w4a16_lora_workspace_size": (C.c_size_t, [I64, I32]),
     "awq_linear_w4a16_lora": (C.c_int, [P, I64, P, P, P, I64, I64, CFG, P, P, P, I32, I32, P, P, P, P,
                                         C.c_size_t, P, C.c_int, P]),
+    # key / value cache
+    "awq_kv_append": (C.c_int, [KVC, KVB, P, I64, P, I64, P, I64, I32, P, I64, P, I64, I32, I32, P, P]),
+    "awq_kv_read": (C.c_int, [KVC, KVB, P, P, P]),
+    "awq_attention_kv4_workspace_size": (C.c_size_t, [I64, I32, I32, I64, I32, I32, I32]),
+    "awq_attention_kv4": (C.c_int, [P, I64, I32, KVC, KVB, C.c_float, I32, I64, P, I64, P, P, C.c_size_t, P]),
     "awq_gemv_max_m": (C.c_int32, []),
     # calibration probes (include/awq_peaks.h)
     "awq_peak_read_stream": (C.c_int, [P, C.c_size_t, P, C.c_int32, P]),

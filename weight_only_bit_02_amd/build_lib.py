@@ -29,7 +29,8 @@ SOURCES = [  # the slowest units (GEMM instantiations, the searches) first: they
     "gemm_i8_plain.hip", "gemm_i8_gated.hip", "gemm_i4_plain.hip", "gemm_i4_gated.hip",
     "gemm_i4_plain_g32.hip", "gemm_i4_gated_g32.hip", "search.hip", "gemm_wide.hip", "gemv.hip", "gemv_mfma.hip",
     "gemv8.hip", "gemv3.hip", "quant_pack.hip", "stats.hip", "fold.hip", "check.hip", "peaks.hip", "gemm.hip",
-    "grouped_gemm.hip", "grouped_stream.hip", "lora.hip", "route.hip", "combine.hip", "awq_abi.hip"]
+    "grouped_gemm.hip", "grouped_stream.hip", "lora.hip", "route.hip", "combine.hip",
+    "kv_attend_128.hip", "kv_attend_256.hip", "kv_attend_64.hip", "kv_attend.hip", "kv_append.hip", "awq_abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -49,7 +50,7 @@ FLAGS = [
 # arithmetic (the group quantizer, the statistic, the candidate scales, the fold): no
 # contraction of a multiply and an add into an FMA anywhere in them, not only inside the
 # functions that say so with a pragma.
-EXACT_UNITS = {"quant_pack.hip", "stats.hip", "search.hip", "fold.hip", "check.hip"}
+EXACT_UNITS = {"quant_pack.hip", "stats.hip", "search.hip", "fold.hip", "check.hip", "kv_append.hip"}
 
 
 def _compile(src: str, verbose: bool) -> str:

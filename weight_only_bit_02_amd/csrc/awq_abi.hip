@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "awq.h"
+#include "kv_cache.hpp"
 #include "launch.hpp"
 
 // Workspace of awq_search_scales_noalloc: a static device array, one copy per GPU for as
@@ -88,6 +89,7 @@ ClipLayout clip_layout(int64_t T, int64_t N, int64_t K, int n_shrink, int group)
 constexpr int64_t kMaxRows = (int64_t)1 << 30;      // positions and rows are kept in 32 bits
 constexpr int64_t kMaxElements = ((int64_t)1 << 31) - 1;  // of X and of an adapter's A: their bytes end
                                                           // below 2^32 - 1, the most a descriptor covers
+constexpr int64_t kMaxKvRows = (int64_t)1 << 22;    // rows of a batch of the cache's calls
 constexpr int64_t kSkinnyMaxRows = 65536;           // its grid: one row of blocks per row tile
 
 // One weight's codes are addressed with 32-bit offsets too.
@@ -657,6 +659,139 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
   if (kv == AWQ_GROUPED_SKINNY && streams) return hip_status(awq::launch_grouped_stream(g, awq::kLora, c.w_bit, st));
   if (kv == AWQ_GROUPED_SKINNY) kv = AWQ_GROUPED_GEMM64;
   return hip_status(awq::launch_grouped_gemm(g, awq::kLora, c.w_bit, kv, st));
+}
+
+// ------------------------------------------------------------------ the 4-bit key / value cache
+
+static awq_status kv_view(const awq_kv_cache* cache, const awq_kv_batch* batch, awq::KvView& v) {
+  if (!cache || !batch || !cache->k_codes || !cache->k_params || !cache->v_codes || !cache->v_params ||
+      !batch->rows || !batch->lengths || !batch->page_table)
+    return AWQ_ERR_NULL_POINTER;
+  if ((cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) ||
+      (cache->group_size != 32 && cache->group_size != 64 && cache->group_size != 128) ||
+      cache->group_size > cache->head_dim || cache->page_size < 16 || cache->page_size > 4096 ||
+      (cache->page_size & (cache->page_size - 1)) != 0)
+    return AWQ_ERR_UNSUPPORTED;
+  if (cache->pages < 1 || cache->pages >= kMaxDim || cache->kv_heads < 1 || cache->kv_heads > AWQ_MAX_HEADS ||
+      batch->n_rows < 1 || batch->n_rows >= kMaxKvRows || batch->seqs < 1 || batch->seqs > AWQ_MAX_SEQUENCES ||
+      batch->max_pages < 1 || batch->max_pages >= kMaxRows / cache->page_size || batch->max_rows < 1 ||
+      batch->max_rows > batch->n_rows)
+    return AWQ_ERR_BAD_SHAPE;
+  if (!aligned16(cache->k_codes) || !aligned16(cache->k_params) || !aligned16(cache->v_codes) ||
+      !aligned16(cache->v_params) || !aligned16(batch->rows) || !aligned16(batch->lengths) ||
+      !aligned16(batch->page_table))
+    return AWQ_ERR_MISALIGNED;
+  v = awq::KvView{};
+  v.k_codes = (uint8_t*)cache->k_codes;
+  v.v_codes = (uint8_t*)cache->v_codes;
+  v.k_params = (uint16_t*)cache->k_params;
+  v.v_params = (uint16_t*)cache->v_params;
+  v.rows = batch->rows;
+  v.lengths = batch->lengths;
+  v.table = batch->page_table;
+  v.pages = cache->pages;
+  for (int p = cache->page_size; p > 1; p >>= 1) ++v.page_shift;
+  v.heads = cache->kv_heads;
+  v.dim = cache->head_dim;
+  v.group = cache->group_size;
+  v.seqs = batch->seqs;
+  v.max_pages = batch->max_pages;
+  v.n_rows = (int)batch->n_rows;
+  return AWQ_OK;
+}
+
+// A launch has fewer than 2^32 threads: 8 channels each.
+static bool kv_grid_ok(int64_t n_rows, int64_t heads, int dim) {
+  return n_rows <= (((int64_t)1 << 26) - 4) / ((heads * dim + 511) / 512);
+}
+
+// Rows `ld` values apart hold `heads` heads: 16-byte pieces.
+static bool good_ld(int64_t ld, int64_t heads, int dim) { return ld >= heads * dim && ld % 8 == 0 && ld < kMaxDim; }
+
+awq_status awq_kv_append(const awq_kv_cache* cache, const awq_kv_batch* batch, const void* k, int64_t k_ld,
+                         const void* v, int64_t v_ld, const void* q, int64_t q_ld, int32_t q_heads, void* q_out,
+                         int64_t q_out_ld, const float* cos_sin, int64_t positions, int32_t rotary_dim,
+                         int32_t interleaved, uint32_t* flags, void* stream) {
+  awq::KvView c;
+  if (!k || !v || (q != nullptr) != (q_out != nullptr) || (q && !cos_sin)) return AWQ_ERR_NULL_POINTER;
+  const awq_status s = kv_view(cache, batch, c);
+  if (s != AWQ_OK) return s;
+  if (interleaved != 0 && interleaved != 1) return AWQ_ERR_UNSUPPORTED;
+  if (!good_ld(k_ld, c.heads, c.dim) || !good_ld(v_ld, c.heads, c.dim)) return AWQ_ERR_BAD_SHAPE;
+  if (q && (q_heads < 1 || q_heads > AWQ_MAX_HEADS || !good_ld(q_ld, q_heads, c.dim) ||
+            !good_ld(q_out_ld, q_heads, c.dim)))
+    return AWQ_ERR_BAD_SHAPE;
+  if (!kv_grid_ok(c.n_rows, (q ? q_heads : 0) + 2 * (int64_t)c.heads, c.dim)) return AWQ_ERR_BAD_SHAPE;
+  if (cos_sin && (positions < 1 || positions >= kMaxDim || rotary_dim < 16 || rotary_dim > c.dim || rotary_dim % 16 != 0))
+    return AWQ_ERR_BAD_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) ||
+      (cos_sin && !aligned16(cos_sin)) || (flags && !aligned4(flags)))
+    return AWQ_ERR_MISALIGNED;
+  return hip_status(awq::launch_kv_append(c, (const uint16_t*)q, q_ld, q ? q_heads : 0, (uint16_t*)q_out, q_out_ld,
+                                          (const uint16_t*)k, k_ld, (const uint16_t*)v, v_ld, cos_sin, positions,
+                                          cos_sin ? rotary_dim : 0, interleaved != 0, flags, (hipStream_t)stream));
+}
+
+awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, void* k, void* v, void* stream) {
+  awq::KvView c;
+  if (!k || !v) return AWQ_ERR_NULL_POINTER;
+  const awq_status s = kv_view(cache, batch, c);
+  if (s != AWQ_OK) return s;
+  if (!kv_grid_ok(c.n_rows, 2 * (int64_t)c.heads, c.dim)) return AWQ_ERR_BAD_SHAPE;
+  if (!aligned16(k) || !aligned16(v)) return AWQ_ERR_MISALIGNED;
+  return hip_status(awq::launch_kv_read(c, (uint16_t*)k, (uint16_t*)v, (hipStream_t)stream));
+}
+
+// Rows of 64 lanes and of blocks, and units of the work list, stay below 2^31.
+static bool attend_sizes_ok(int64_t n_rows, int32_t seqs, int32_t max_rows, int64_t max_tokens, int32_t q_heads,
+                            int32_t kv_heads, int32_t head_dim) {
+  if (n_rows < 1 || n_rows >= kMaxKvRows || seqs < 1 || seqs > AWQ_MAX_SEQUENCES || max_rows < 1 ||
+      max_rows > n_rows || max_tokens < 1 || max_tokens >= kMaxRows || kv_heads < 1 || q_heads < kv_heads ||
+      q_heads > AWQ_MAX_HEADS || q_heads % kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) || n_rows >= ((int64_t)1 << 24) / q_heads)
+    return false;
+  const int64_t tiles = n_rows * (q_heads / kv_heads) / 16 + seqs;
+  return tiles * kv_heads < kMaxDim / (max_tokens / 256 + 1);
+}
+
+size_t awq_attention_kv4_workspace_size(int64_t n_rows, int32_t seqs, int32_t max_rows, int64_t max_tokens,
+                                        int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  if (!attend_sizes_ok(n_rows, seqs, max_rows, max_tokens, q_heads, kv_heads, head_dim)) return 0;
+  return awq::attend_plan(n_rows, seqs, max_rows, max_tokens, q_heads / kv_heads, kv_heads, head_dim).bytes;
+}
+
+awq_status awq_attention_kv4(const void* q, int64_t q_ld, int32_t q_heads, const awq_kv_cache* cache,
+                             const awq_kv_batch* batch, float scale, int32_t causal, int64_t window, void* out,
+                             int64_t out_ld, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  awq::KvView c;
+  if (!q || !out) return AWQ_ERR_NULL_POINTER;
+  const awq_status s = kv_view(cache, batch, c);
+  if (s != AWQ_OK) return s;
+  if ((causal != 0 && causal != 1) || !(scale > 0.0f && scale < 1e30f)) return AWQ_ERR_UNSUPPORTED;
+  const int64_t max_tokens = (int64_t)batch->max_pages * cache->page_size;
+  if (!attend_sizes_ok(batch->n_rows, batch->seqs, batch->max_rows, max_tokens, q_heads, c.heads, c.dim) ||
+      !good_ld(q_ld, q_heads, c.dim) || !good_ld(out_ld, q_heads, c.dim) || window < 0)
+    return AWQ_ERR_BAD_SHAPE;
+  const awq::AttendPlan p = awq::attend_plan(batch->n_rows, batch->seqs, batch->max_rows, max_tokens,
+                                             q_heads / c.heads, c.heads, c.dim);
+  if (!good_workspace(workspace, workspace_bytes, p.bytes)) return AWQ_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(out) || (lse && !aligned4(lse))) return AWQ_ERR_MISALIGNED;
+  awq::AttendArgs a{};
+  a.q = (const uint16_t*)q;
+  a.out = (uint16_t*)out;
+  a.lse = lse;
+  a.q_ld = q_ld;
+  a.out_ld = out_ld;
+  a.q_heads = q_heads;
+  a.share = q_heads / c.heads;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  a.causal = causal;
+  a.window = window >= kMaxRows ? 0 : (int)window;  // positions stay below
+  a.blocks = p.blocks;
+  a.part = (float*)((char*)workspace + p.part);
+  a.part_ml = (float2*)((char*)workspace + p.part_ml);
+  return hip_status(awq::launch_attend(c, a, p, (hipStream_t)stream));
 }
 
 }  // extern "C"
