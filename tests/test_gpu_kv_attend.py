@@ -109,6 +109,70 @@ def test_lengths_beyond_the_table():
     assert np.all(np.abs(host(y) - want) <= bound)
 
 
+@pytest.mark.parametrize("D,group,share", [(64, 32, 8), (64, 64, 1), (128, 128, 8), (128, 32, 2), (256, 128, 4), (256, 32, 3)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50), (False, 130)])
+def test_tiles(D, group, share, causal, window):
+    """More rows than a wave's, a block's and a work list's piece; short sequences among them."""
+    attend(D, group, 16, 1, share, [150, 1, 67, 9], [170, 600, 700, 9], causal=causal, window=window, seed=D + group)
+
+
+def test_tiles_holes():
+    attend(128, 64, 16, 1, 4, [40, 100], [200, 100], seed=6, holes=[(0, 0), (0, 5), (0, 12), (1, 0), (1, 1), (1, 2), (1, 6)])
+    attend(64, 64, 32, 1, 2, [60], [290], seed=7, holes=[(0, p) for p in range(9)])
+    attend(256, 64, 16, 1, 2, [60], [290], seed=8, holes=[(0, 1), (0, 17)])
+
+
+def test_tiles_rows_before_the_sequence():
+    attend(128, 128, 16, 1, 4, [90, 80, 70], [30, 0, 1], seed=9)
+
+
+@pytest.mark.parametrize("D,heads,share,n,lengths,window", [
+    (128, 8, 4, [700, 1300], [700, 2000], 0),      # pieces of items, joined
+    (128, 32, 4, [700, 1300], [700, 2000], 0),     # whole items
+    (128, 2, 1, [257, 1, 300], [5000, 4000, 301], 0),
+    (64, 2, 8, [130, 256], [9000, 300], 1000),
+    (256, 2, 2, [64, 500], [3001, 777], 0),
+])
+def test_prompts(D, heads, share, n, lengths, window):
+    """Long ones, against 64-bit products on the GPU of the values that the cache holds."""
+    rng = np.random.default_rng(12)
+    b, pages, table, rows = batch_of(awq, n, lengths, 64, rng)
+    dev = awq.alloc_kv_cache(pages, heads, D, DEV)
+    T = int(rows[-1])
+    whole = awq.KVBatch(to_dev(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)), b.lengths, b.page_table)
+    gen = torch.Generator(DEV).manual_seed(1)
+    kv = torch.randn(sum(lengths), 2 * heads, D, generator=gen, device=DEV).half()
+    awq.kv_append(dev, whole, kv[:, :heads], kv[:, heads:])
+    q = torch.randn(T, heads * share, D, generator=gen, device=DEV).half()
+    lse = torch.empty(T, heads * share, device=DEV)
+    y = awq.attention_kv4(q, dev, b, window=window, lse=lse)
+    assert torch.equal(y, awq.attention_kv4(q, dev, b, window=window))
+    k, v = (x.double() for x in awq.kv_read(dev, whole, sum(lengths)))
+    ends = np.cumsum(lengths)
+    for s in range(len(n)):
+        r = slice(int(ends[s]) - lengths[s], int(ends[s]))
+        p = torch.arange(lengths[s] - n[s], lengths[s], device=DEV)[:, None]
+        t = torch.arange(lengths[s], device=DEV)
+        see = (t <= p) & (t > p - (window or 1 << 30))
+        for h in range(heads * share):
+            kk, vv = k[r, h // share].contiguous(), v[r, h // share].contiguous()
+            x = q[rows[s]:rows[s + 1], h].double()
+            sc = (x @ kk.t().contiguous() / math.sqrt(D)).masked_fill(~see, -math.inf)
+            size = (x.abs() @ kk.abs().t().contiguous() / math.sqrt(D)).amax(1, keepdim=True)
+            want_lse = torch.logsumexp(sc, 1)
+            w = torch.exp(sc - want_lse[:, None])
+            want, spread = w @ vv, w @ vv.abs()
+            # the bound of kv_ref.attention
+            e = (D + 8) * 2.0 ** -24 * size + 2.0 ** -21 + see.sum(1, keepdim=True) * 2.0 ** -24
+            least = 2.0 ** -24 * vv.abs().sum(0) * torch.exp(sc.amax(1) - want_lse)[:, None]
+            off = (2 * e + 2.0 ** -11) * spread + least
+            bound = off + 2.0 ** -11 * (want.abs() + off) + 2.0 ** -25
+            got = y[rows[s]:rows[s + 1], h].double()
+            assert bool(((got - want).abs() <= bound).all()), (s, h)
+            got = lse[rows[s]:rows[s + 1], h].double()
+            assert bool(((got - want_lse).abs() <= e[:, 0] + 2.0 ** -22 * (2 * want_lse.abs() + 12)).all()), (s, h)
+
+
 @pytest.mark.parametrize("q_gain,k_gain,v_gain", [(30, 8, 1), (0, 1, 1), (1e-4, 1, 100), (1, 1, 2000), (1, 1, 1e-3)])
 def test_ranges(q_gain, k_gain, v_gain):
     """One token that takes all, equal probabilities, large and small values."""

@@ -784,14 +784,10 @@ awq_status awq_attention_kv4(const void* q, int64_t q_ld, int32_t q_heads, const
   a.out_ld = out_ld;
   a.q_heads = q_heads;
   a.share = q_heads / c.heads;
-  a.scale = scale;
   a.scale_log2 = scale * 1.44269504088896341f;
   a.causal = causal;
   a.window = window >= kMaxRows ? 0 : (int)window;  // positions stay below
-  a.blocks = p.blocks;
-  a.part = (float*)((char*)workspace + p.part);
-  a.part_ml = (float2*)((char*)workspace + p.part_ml);
-  return hip_status(awq::launch_attend(c, a, p, (hipStream_t)stream));
+  return hip_status(awq::launch_attend(c, a, p, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

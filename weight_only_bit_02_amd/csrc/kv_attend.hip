@@ -1,43 +1,86 @@
-// Attention over the 4-bit cache: workspace and launches (kernels: kv_attend.hpp).
-#include "kv_attend.hpp"
+// Attention over the 4-bit cache: workspace and launches (kernels: kv_attend.hpp, kv_attend_tiles.hpp).
+#include "kv_attend_tiles.hpp"
 
 namespace awq {
 
-#define AWQ_DECLARE(D)                                                                                    \
-  hipError_t attend_stream_##D(const KvView& v, const AttendArgs& a, int tiles, hipStream_t stream);      \
-  hipError_t attend_join_##D(const KvView& v, const AttendArgs& a, int tile, hipStream_t stream);
+#define AWQ_DECLARE(D)                                                                                        \
+  hipError_t attend_stream_##D(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream); \
+  hipError_t attend_tiles_##D(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream);  \
+  hipError_t attend_join_##D(const AttendArgs& a, int tile, hipStream_t stream);
 AWQ_DECLARE(64)
 AWQ_DECLARE(128)
 AWQ_DECLARE(256)
 #undef AWQ_DECLARE
 
 namespace {
-constexpr int kMostBlocks = 1024;  // four blocks a CU
+
+constexpr int kFew = 64;
+constexpr int kStreamBlocks = 1024;  // four blocks a CU
+constexpr int kTileBlocks = 256;     // one block a CU
+constexpr int64_t kDirectItems = 512;
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Room for the sums of items that are split.
+void part_room(AttendPart& p, int dim, size_t& bytes) {
+  if (!p.join) return;
+  const size_t rows = (size_t)2 * p.blocks * p.tile;
+  p.part = bytes;
+  bytes += align256(rows * dim * sizeof(float));
+  p.part_ml = bytes;
+  bytes += align256(rows * sizeof(float2));
+  p.split = bytes;
+  bytes += align256(p.blocks * sizeof(AttendSplit));
+}
+
 }  // namespace
 
 AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim) {
   AttendPlan p{};
-  p.tiles = (int64_t)max_rows * share <= 16 ? 1 : 2;
-  const int64_t rows = 16 * p.tiles, chunks = (max_tokens + kAttendChunk - 1) / kAttendChunk;
-  const int64_t tiles = n_rows * share / rows + (seqs < n_rows ? seqs : n_rows);  // at most
-  const int64_t units = heads * tiles * chunks;
-  p.blocks = (int)(units < kMostBlocks ? units : kMostBlocks);
-  p.join = chunks > 1;
-  p.part = 0;
-  if (p.join) {
-    p.part_ml = align256((size_t)2 * p.blocks * rows * dim * sizeof(float));
-    p.bytes = p.part_ml + align256((size_t)2 * p.blocks * rows * sizeof(float2));
+  const int64_t chunks = (max_tokens + kAttendChunk - 1) / kAttendChunk;
+  const int64_t some = seqs < n_rows ? seqs : n_rows;  // sequences with rows, at most
+  const int64_t most = (int64_t)max_rows * share;
+  const bool both = most > kFew;
+  p.few = both ? kFew : 0x7FFFFFFF;
+  p.stream.tile = most <= 16 ? 16 : 32;
+  const auto items = [&](int tile) { return heads * (n_rows * share / tile + some); };  // at most
+  const int64_t units = items(p.stream.tile) * chunks;
+  p.stream.blocks = (int)(units < kStreamBlocks ? units : kStreamBlocks);
+  p.stream.join = chunks > 1;
+  part_room(p.stream, dim, p.bytes);
+  if (both) {
+    p.tiles.tile = dim == 256 ? TileShape<256>::kRows : TileShape<128>::kRows;
+    const int64_t n = items(p.tiles.tile);
+    p.tiles.direct = n >= kDirectItems || chunks == 1;
+    p.tiles.join = !p.tiles.direct;
+    p.tiles.blocks = p.tiles.direct ? (int)n : kTileBlocks;
+    part_room(p.tiles, dim, p.bytes);
   }
   return p;
 }
 
-hipError_t launch_attend(const KvView& v, const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
-  auto* const f = v.dim == 64 ? attend_stream_64 : v.dim == 128 ? attend_stream_128 : attend_stream_256;
-  const hipError_t e = f(v, a, p.tiles, stream);
-  if (e != hipSuccess || !p.join) return e;
-  auto* const g = v.dim == 64 ? attend_join_64 : v.dim == 128 ? attend_join_128 : attend_join_256;
-  return g(v, a, 16 * p.tiles, stream);
+hipError_t launch_attend(const KvView& v, AttendArgs a, const AttendPlan& p, void* workspace, hipStream_t stream) {
+  const auto take = [&](const AttendPart& s) {
+    char* const w = (char*)workspace;
+    a.blocks = s.blocks;
+    a.direct = s.direct;
+    a.part = s.join ? (float*)(w + s.part) : nullptr;
+    a.part_ml = s.join ? (float2*)(w + s.part_ml) : nullptr;
+    a.split = s.join ? (AttendSplit*)(w + s.split) : nullptr;
+  };
+  auto* const streaming = v.dim == 64 ? attend_stream_64 : v.dim == 128 ? attend_stream_128 : attend_stream_256;
+  auto* const tiles = v.dim == 64 ? attend_tiles_64 : v.dim == 128 ? attend_tiles_128 : attend_tiles_256;
+  auto* const join = v.dim == 64 ? attend_join_64 : v.dim == 128 ? attend_join_128 : attend_join_256;
+  hipError_t e = hipSuccess;
+  if (p.tiles.tile) {
+    take(p.tiles);
+    e = tiles(v, a, AttendList{p.tiles.tile, p.few, 0x7FFFFFFF}, stream);
+    if (e == hipSuccess && p.tiles.join) e = join(a, p.tiles.tile, stream);
+    if (e != hipSuccess) return e;
+  }
+  take(p.stream);
+  e = streaming(v, a, AttendList{p.stream.tile, 0, p.few}, stream);
+  if (e == hipSuccess && p.stream.join) e = join(a, p.stream.tile, stream);
+  return e;
 }
 
 }  // namespace awq

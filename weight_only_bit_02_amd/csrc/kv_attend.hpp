@@ -25,32 +25,66 @@ constexpr int kAttendStep = 64;                          // tokens of a wave's s
 constexpr int kAttendChunk = kAttendStep * kAttendWaves;  // tokens of the work list's unit
 constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score passes it by 2^8
 
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;  // of a join block, at most
+
 typedef _Float16 half4a __attribute__((ext_vector_type(4)));
 
-// A sequence's share of the work list.
+// The work list of a kernel: units of kAttendChunk tokens of (sequence, tile of rows, head of
+// keys), of the sequences with more than `over` and at most `upto` rows x share.
+struct AttendList {
+  int tile;  // rows of a tile
+  int over, upto;
+};
+
 struct AttendSeq {
   KvSeq q;
   int flat;   // rows x share
-  int tiles;  // of `tile` rows
+  int tiles;  // 0: not of this list
   int first;  // first token looked at, a multiple of 64
-  int chunks;
-  int units;  // heads x tiles x chunks
+  int units;
 };
 
-__device__ __forceinline__ AttendSeq attend_seq(const KvView& v, const AttendArgs& a, int s, int tile) {
+// Chunks of tile j of a sequence: as far as its last row sees, one for rows without a token.
+__device__ __forceinline__ int attend_chunks(const AttendArgs& a, const AttendList& g, const AttendSeq& w, int j) {
+  const int end = (j + 1) * g.tile < w.flat ? (j + 1) * g.tile : w.flat;
+  const int p = w.q.length - w.q.rows + (end - 1) / a.share + 1;  // tokens up to the last row's own
+  const int n = (a.causal && p < w.q.tokens ? p : w.q.tokens) - w.first;
+  return n <= 0 ? 1 : (n + kAttendChunk - 1) / kAttendChunk;
+}
+
+__device__ __forceinline__ AttendSeq attend_seq(const KvView& v, const AttendArgs& a, const AttendList& g, int s) {
   AttendSeq w;
   w.q = kv_sequence(v, s);
   w.flat = w.q.rows * a.share;
-  w.tiles = (w.flat + tile - 1) / tile;
+  w.tiles = w.flat > g.over && w.flat <= g.upto ? (w.flat + g.tile - 1) / g.tile : 0;
   w.first = 0;
   if (a.window > 0) {
     const int64_t lo = (int64_t)w.q.length - w.q.rows - a.window + 1;
     w.first = lo <= 0 ? 0 : (int)(lo < w.q.tokens ? lo : w.q.tokens) & ~(kAttendStep - 1);
   }
-  const int n = w.q.tokens - w.first;
-  w.chunks = n <= 0 ? 1 : (n + kAttendChunk - 1) / kAttendChunk;  // a row without tokens is written, too
-  w.units = v.heads * w.tiles * w.chunks;
+  w.units = 0;
+  for (int j = 0; j < w.tiles; ++j) w.units += attend_chunks(a, g, w, j);
+  w.units *= v.heads;
   return w;
+}
+
+// A unit's place: tile, head and chunk of the item's chunks.
+struct AttendItem {
+  int tile, head, chunk, chunks;
+};
+__device__ __forceinline__ AttendItem attend_item(const KvView& v, const AttendArgs& a, const AttendList& g,
+                                                  const AttendSeq& w, int at) {
+  AttendItem x{0, 0, 0, 1};
+  for (; x.tile < w.tiles; ++x.tile) {
+    x.chunks = attend_chunks(a, g, w, x.tile);
+    const int n = x.chunks * v.heads;
+    if (at < n) break;
+    at -= n;
+  }
+  x.head = at / x.chunks;
+  x.chunk = at - x.head * x.chunks;
+  return x;
 }
 
 // First unit of block b of n, of `total` units (n at most total: no block between two others is
@@ -61,12 +95,12 @@ __device__ __forceinline__ int block_of(int x, int n, int total) {
 }
 
 // Units of all sequences, and of those before sequence s (uniform over the wave).
-__device__ __forceinline__ int attend_units(const KvView& v, const AttendArgs& a, int tile, int s, int lane,
+__device__ __forceinline__ int attend_units(const KvView& v, const AttendArgs& a, const AttendList& g, int s, int lane,
                                             int& before) {
   int total = 0;
   before = 0;
   for (int i = 0; i < v.seqs; i += kWave) {
-    const int n = i + lane < v.seqs ? attend_seq(v, a, i + lane, tile).units : 0;
+    const int n = i + lane < v.seqs ? attend_seq(v, a, g, i + lane).units : 0;
     total += __builtin_amdgcn_readlane(wave_scan(n), kWave - 1);
     before += __builtin_amdgcn_readlane(wave_scan(i + lane < s ? n : 0), kWave - 1);
   }
@@ -74,11 +108,11 @@ __device__ __forceinline__ int attend_units(const KvView& v, const AttendArgs& a
 }
 
 // The sequence that holds unit x of the list, and the units before it (uniform over the wave).
-__device__ __forceinline__ int attend_find(const KvView& v, const AttendArgs& a, int tile, int x, int lane,
+__device__ __forceinline__ int attend_find(const KvView& v, const AttendArgs& a, const AttendList& g, int x, int lane,
                                            int& before) {
   before = 0;
   for (int i = 0; i < v.seqs; i += kWave) {
-    const int n = i + lane < v.seqs ? attend_seq(v, a, i + lane, tile).units : 0;
+    const int n = i + lane < v.seqs ? attend_seq(v, a, g, i + lane).units : 0;
     const int sum = wave_scan(n);
     const uint64_t m = __ballot(before + sum > x);
     if (m) {
@@ -90,6 +124,36 @@ __device__ __forceinline__ int attend_find(const KvView& v, const AttendArgs& a,
   }
   return v.seqs;
 }
+
+// The sequence with tile x of all tiles, the units before it, and which of its tiles it is.
+__device__ __forceinline__ int attend_find_tile(const KvView& v, const AttendArgs& a, const AttendList& g, int x,
+                                                int lane, int& before, int& tile) {
+  int tiles = 0;
+  before = 0;
+  for (int i = 0; i < v.seqs; i += kWave) {
+    AttendSeq w{};
+    if (i + lane < v.seqs) w = attend_seq(v, a, g, i + lane);
+    const int sum = wave_scan(w.tiles), units = wave_scan(w.units);
+    const uint64_t m = __ballot(tiles + sum > x);
+    if (m) {
+      const int at = __ffsll((unsigned long long)m) - 1;
+      before += __builtin_amdgcn_readlane(units, at) - __builtin_amdgcn_readlane(w.units, at);
+      tile = x - tiles - __builtin_amdgcn_readlane(sum, at) + __builtin_amdgcn_readlane(w.tiles, at);
+      return i + at;
+    }
+    tiles += __builtin_amdgcn_readlane(sum, kWave - 1);
+    before += __builtin_amdgcn_readlane(units, kWave - 1);
+  }
+  return v.seqs;
+}
+
+// What block b leaves for k_attend_join (thread 0): the item that the next block goes on with.
+__device__ __forceinline__ void attend_split(const AttendArgs& a, const AttendSplit& d) {
+  if (a.split && threadIdx.x == 0) a.split[blockIdx.x] = d;
+}
+
+// log of a row's sum of exponentials from its maximum (of log2) and sum; -inf without a token.
+__device__ __forceinline__ float attend_lse(float m, float l) { return m * 0.69314718055994531f + __logf(l); }
 
 // (code - zero) scale of the four nibbles of each half of w, pairs by nibble: zz = -(1024 + z),
 // zz64 = -(64 + z), s2 = scale, of the low and of the high half.
@@ -114,7 +178,7 @@ __device__ __forceinline__ Params2 params2(uint32_t p) {
 
 // D channels, G groups of them, R tiles of 16 rows.
 template <int D, int G, int R>
-__global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v, AttendArgs a) {
+__global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
   constexpr int kSlices = D / 32, kTiles = D / 16, kPerGroup = kSlices / G;  // slices of a group
   constexpr int kPad = 68;
   __shared__ float sums[kAttendWaves][16][kPad];
@@ -123,24 +187,28 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int before;
-  const int total = attend_units(v, a, 16 * R, 0, lane, before);
+  const int total = attend_units(v, a, list, 0, lane, before);
   const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
-  if ((int)blockIdx.x >= blocks) return;
+  AttendSplit split{};
+  if ((int)blockIdx.x >= blocks) {
+    attend_split(a, split);
+    return;
+  }
   const int from = block_start(blockIdx.x, blocks, total), to = block_start(blockIdx.x + 1, blocks, total);
-  int s = attend_find(v, a, 16 * R, from, lane, before);
+  int s = attend_find(v, a, list, from, lane, before);
   int unit = from;
   while (unit < to && s < v.seqs) {
-    const AttendSeq w = attend_seq(v, a, s, 16 * R);
+    const AttendSeq w = attend_seq(v, a, list, s);
     const int at = unit - before;
-    if (at < 0) return;  // sums that wrapped (wrong rows)
+    if (at < 0) break;  // sums that wrapped (wrong rows)
     if (at >= w.units) {
       before += w.units;
       ++s;
       continue;
     }
-    const int item = at / w.chunks, u0 = at - item * w.chunks;
-    const int u1 = w.chunks - u0 < to - unit ? w.chunks : u0 + (to - unit);
-    const int tile = item / v.heads, head = item - tile * v.heads;
+    const AttendItem x = attend_item(v, a, list, w, at);
+    const int tile = x.tile, head = x.head, u0 = x.chunk;
+    const int u1 = x.chunks - u0 < to - unit ? x.chunks : u0 + (to - unit);
 
     // the tile's rows: their positions, queries as the second operand
     const int r0 = tile * 16 * R, r1 = (r0 + 16 * R < w.flat ? r0 + 16 * R : w.flat) - 1;
@@ -225,11 +293,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
         }
       }
       // scores
-      f32x4w x[R][4];
+      f32x4w sc[R][4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) x[r][u] = f32x4w{0, 0, 0, 0};
+        for (int r = 0; r < R; ++r) sc[r][u] = f32x4w{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const Params2 p = params2(kp[u][g] | kp[u][g] << 16);
@@ -240,7 +308,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
             const half8w key{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              x[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[r][t], x[r][u], 0, 0, 0);
+              sc[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[r][t], sc[r][u], 0, 0, 0);
           }
         }
       }
@@ -254,7 +322,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
             const int t = tb + 16 * u + 4 * h + i;
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              if (!(t >= lo[r] && t <= hi[r] && page[u] >= 0)) x[r][u][i] = -__builtin_inff();
+              if (!(t >= lo[r] && t <= hi[r] && page[u] >= 0)) sc[r][u][i] = -__builtin_inff();
             // what lies behind the sequence's last token may be anything, an infinite scale too
             if (t > last) {
 #pragma unroll
@@ -271,11 +339,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
       half8w ph[R][2], pl[R][2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float top = x[r][0][0];
+        float top = sc[r][0][0];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, x[r][u][i]);
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][u][i]);
         top *= a.scale_log2;
         if (__ballot(top > m[r] + kLazy)) {
           top = fmaxf(top, __shfl_xor(top, 16));
@@ -291,7 +359,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
         for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r][u][i], a.scale_log2, -base));
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][u][i], a.scale_log2, -base));
             l[r] += e;
             const _Float16 hi16 = (_Float16)e;
             ph[r][u >> 1][4 * (u & 1) + i] = hi16;
@@ -329,8 +397,12 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
     }
 
     // the waves' sums together
-    const bool alone = u0 == 0 && u1 == w.chunks;
+    const bool alone = u0 == 0 && u1 == x.chunks;
     const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
+    if (u1 < x.chunks) {
+      const int b0 = block_of(unit - u0, blocks, total), b1 = block_of(unit - u0 + x.chunks - 1, blocks, total);
+      split = AttendSplit{w.q.row0, r0, r1, head, b1 - b0 + 1, (int)blockIdx.x - b0};
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor(l[r], 16);
@@ -373,78 +445,91 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
 #pragma unroll
           for (int i = 0; i < 4; ++i) b[i] = (_Float16)(y[i] * d);
           *reinterpret_cast<half4a*>(a.out + q_row * a.out_ld + (int64_t)q_head * D + 64 * part + col) = b;
-        } else if (!alone) {
+        } else if (live) {
           *reinterpret_cast<f32x4w*>(a.part + ((int64_t)slot * (16 * R) + 16 * r + row) * D + 64 * part + col) = y;
         }
       }
       if (col == 0) {
         if (alone) {
           if (live && a.lse)
-            a.lse[q_row * a.q_heads + q_head] = rtop * 0.69314718055994531f + __logf(sum);
-        } else {
+            a.lse[q_row * a.q_heads + q_head] = attend_lse(rtop, sum);
+        } else if (live) {
           a.part_ml[(int64_t)slot * (16 * R) + 16 * r + row] = make_float2(rtop, sum);
         }
       }
     }
     unit += u1 - u0;
   }
+  attend_split(a, split);
 }
 
-// Rows whose tokens several blocks took: one block of four waves per (row, query head).
+// Items that several blocks took. The join block (b, y) belongs to the item that block b leaves
+// unfinished: the blocks of an item share its rows, so that an item cut into many pieces has many
+// blocks to add them. D / 4 lanes take 16 bytes each of a piece of a row; the 1024 / D such groups of
+// a block are dealt out to its one, two or four rows.
 template <int D>
-__global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_join(KvView v, AttendArgs a, int tile) {
-  constexpr int kEach = D / kWave;
-  __shared__ float part[kAttendWaves][D];
-  __shared__ float2 ml[kAttendWaves];
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int t = blockIdx.x / a.q_heads, q_head = blockIdx.x - t * a.q_heads;
-  const int s = kv_find(v, t, lane);
-  if (s >= v.seqs) return;
-  int before;
-  const int total = attend_units(v, a, tile, s, lane, before);
-  const AttendSeq w = attend_seq(v, a, s, tile);
-  if ((unsigned)(t - w.q.row0) >= (unsigned)w.q.rows) return;  // wrong rows
-  const int head = q_head / a.share, flat = (t - w.q.row0) * a.share + q_head - head * a.share;
-  const int x = before + ((flat / tile) * v.heads + head) * w.chunks;
-  const int blocks = a.blocks < total ? a.blocks : total;
-  if (blocks <= 0) return;
-  const int b0 = block_of(x, blocks, total), b1 = block_of(x + w.chunks - 1, blocks, total);
-  if (b0 == b1 || b0 < 0 || b1 >= blocks) return;  // written by its block; or sums that wrapped (wrong rows)
-  const int row = flat % tile;
-  float m = -__builtin_inff(), l = 0.0f, y[kEach] = {};
-  for (int b = b0 + wave; b <= b1; b += kAttendWaves) {
-    const int64_t slot = ((int64_t)2 * b + (b == b0 ? 1 : 0)) * tile + row;
-    const float2 p = a.part_ml[slot];
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, int tile) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ f32x4w part[kGroups][kLanes];
+  __shared__ float2 ml[kGroups];
+  const AttendSplit d = a.split[blockIdx.x];
+  const int joins = (d.blocks - 1) * gridDim.y, id = d.index * gridDim.y + blockIdx.y;
+  const int b0 = (int)blockIdx.x - d.index;
+  if (d.blocks < 2 || b0 < 0 || d.blocks > (int)gridDim.x - b0 || d.r0 + id > d.r1) return;
+  const int per = (tile + joins - 1) / joins, rows = per > 2 ? 4 : per;  // (at most four)
+  const int ways = kGroups / rows, group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int row = id + group / ways * joins, flat = d.r0 + row;
+  float m = -__builtin_inff(), l = 0.0f;
+  f32x4w y{0, 0, 0, 0};
+  if (row < tile && flat <= d.r1) {
+    constexpr int kDeep = 4;
+    for (int k = group % ways; k < d.blocks; k += kDeep * ways) {
+      float2 p[kDeep];
+      f32x4w z[kDeep];
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int kk = k + i * ways;
+        const int64_t slot = ((int64_t)2 * (b0 + kk) + (kk == 0 ? 1 : 0)) * tile + row;
+        p[i] = kk < d.blocks ? a.part_ml[slot] : make_float2(-__builtin_inff(), 0.0f);
+        z[i] = kk < d.blocks ? *reinterpret_cast<const f32x4w*>(a.part + slot * D + 4 * lane) : f32x4w{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const float top = fmaxf(m, p[i].x), base = top == -__builtin_inff() ? 0.0f : top;
+        const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(p[i].x - base);
+        l = l * f + p[i].y * g;
+        y = y * f + z[i] * g;
+        m = top;
+      }
+    }
+  }
+  part[group][lane] = y;
+  if (lane == 0) ml[group] = make_float2(m, l);
+  __syncthreads();
+  if (group % ways != 0 || row >= tile || flat > d.r1) return;
+  for (int i = 1; i < ways; ++i) {
+    const float2 p = ml[group + i];
     const float top = fmaxf(m, p.x), base = top == -__builtin_inff() ? 0.0f : top;
     const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(p.x - base);
     l = l * f + p.y * g;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) y[i] = y[i] * f + a.part[slot * D + kEach * lane + i] * g;
+    y = y * f + part[group + i][lane] * g;
     m = top;
   }
-  if (lane == 0) ml[wave] = make_float2(m, l);
+  const int token = flat / a.share;
+  const int64_t q_row = d.row0 + token;
+  const int q_head = d.head * a.share + flat - token * a.share;
+  const float r = l == 0.0f ? 0.0f : 1.0f / l;  // no token: zeros
+  half4a b;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) part[wave][kEach * lane + i] = y[i];
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = ml[0].x, sum = 0.0f, o = 0.0f;
-#pragma unroll
-  for (int i = 1; i < kAttendWaves; ++i) top = fmaxf(top, ml[i].x);
-  const float base = top == -__builtin_inff() ? 0.0f : top;
-#pragma unroll
-  for (int i = 0; i < kAttendWaves; ++i) {
-    const float f = __builtin_amdgcn_exp2f(ml[i].x - base);
-    sum += ml[i].y * f;
-    o += part[i][threadIdx.x] * f;
-  }
-  a.out[t * a.out_ld + (int64_t)q_head * D + threadIdx.x] = f2h_bits(sum == 0.0f ? 0.0f : o / sum);
-  if (a.lse && threadIdx.x == 0) a.lse[(int64_t)t * a.q_heads + q_head] = top * 0.69314718055994531f + __logf(sum);
+  for (int e = 0; e < 4; ++e) b[e] = (_Float16)(y[e] * r);
+  *reinterpret_cast<half4a*>(a.out + q_row * a.out_ld + (int64_t)q_head * D + 4 * lane) = b;
+  if (a.lse && lane == 0) a.lse[q_row * a.q_heads + q_head] = attend_lse(m, l);
 }
 
 template <int D, int G>
-hipError_t attend_stream(const KvView& v, const AttendArgs& a, int tiles, hipStream_t stream) {
-  auto* const f = tiles == 1 ? k_attend_stream<D, G, 1> : k_attend_stream<D, G, 2>;
-  hipLaunchKernelGGL(f, dim3(a.blocks), dim3(kAttendWaves * kWave), 0, stream, v, a);
+hipError_t attend_stream(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream) {
+  auto* const f = list.tile == 16 ? k_attend_stream<D, G, 1> : k_attend_stream<D, G, 2>;
+  hipLaunchKernelGGL(f, dim3(a.blocks), dim3(kAttendWaves * kWave), 0, stream, v, a, list);
   return hipGetLastError();
 }
 

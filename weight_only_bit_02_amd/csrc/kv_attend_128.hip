@@ -1,20 +1,28 @@
-// Attention over the 4-bit cache, heads of 128 channels (kv_attend.hpp).
-#include "kv_attend.hpp"
+// Attention over the 4-bit cache, heads of 128 channels (kv_attend.hpp, kv_attend_tiles.hpp).
+#include "kv_attend_tiles.hpp"
 
 namespace awq {
 
-hipError_t attend_stream_128(const KvView& v, const AttendArgs& a, int tiles, hipStream_t stream) {
+hipError_t attend_stream_128(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream) {
   switch (v.group) {
-    case 128: return attend_stream<128, 1>(v, a, tiles, stream);
-    case 64: return attend_stream<128, 2>(v, a, tiles, stream);
-    case 32: return attend_stream<128, 4>(v, a, tiles, stream);
+    case 128: return attend_stream<128, 1>(v, a, list, stream);
+    case 64: return attend_stream<128, 2>(v, a, list, stream);
+    case 32: return attend_stream<128, 4>(v, a, list, stream);
   }
   return hipErrorInvalidValue;
 }
 
-hipError_t attend_join_128(const KvView& v, const AttendArgs& a, int tile, hipStream_t stream) {
-  hipLaunchKernelGGL(k_attend_join<128>, dim3((unsigned)(v.n_rows * a.q_heads)), dim3(kAttendWaves * kWave), 0,
-                     stream, v, a, tile);
+hipError_t attend_tiles_128(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream) {
+  switch (v.group) {
+    case 128: return attend_tiles<128, 1>(v, a, list, stream);
+    case 64: return attend_tiles<128, 2>(v, a, list, stream);
+    case 32: return attend_tiles<128, 4>(v, a, list, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t attend_join_128(const AttendArgs& a, int tile, hipStream_t stream) {
+  hipLaunchKernelGGL(k_attend_join<128>, dim3(a.blocks, tile / kJoinRows), dim3(kJoinThreads), 0, stream, a, tile);
   return hipGetLastError();
 }
 

@@ -1,0 +1,330 @@
+// Attention over the 4-bit cache, tile form: many query rows per sequence and head of keys
+// (prompts and pieces of them).
+//
+// A block takes 32 rows a wave of one head of keys, so that the codes are widened once for all
+// of them: keys as fp16 [token][channel], values transposed, [channel][token], in LDS, while the
+// matrix cores work on the tokens before (two buffers, codes two steps ahead in registers, one
+// barrier a step). v_mfma_f32_32x32x16_f16: S^T = K Q^T leaves lane (h, c) = (lane / 32, lane % 32)
+// row c's scores of tokens 8 i + 4 h + 0..3, which are the second operand of O^T = V^T P^T for
+// values whose tokens lie in that order: LDS holds them so. Probabilities go to the second
+// product rounded to fp16 (an error of the output's own size; hi + lo would be half as much matrix
+// work again).
+//
+// 16-byte pieces of an LDS row are exchanged by the row's number, so that the 16 rows that a
+// read touches at a time lie in different banks.
+#pragma once
+
+#include "kv_attend.hpp"
+
+namespace awq {
+
+template <int D>
+struct TileShape {
+  static constexpr int kWaves = D == 256 ? 4 : 8;  // D = 256: a wave's sums take the registers of two
+  static constexpr int kRows = 32 * kWaves;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kTokens = 8192 / D;         // of a step: 4 KB of codes of each kind
+  static constexpr int kWords = 1024 / kThreads;   // of codes of each kind per thread and step
+  static constexpr int kUnitThreads = 16 * kThreads / kTokens;  // threads of 16 tokens
+};
+
+// 16-byte slot of piece `c` of row r, rows of N pieces: 16 rows at the same c lie in different
+// banks (16 slots of them).
+template <int N>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  constexpr int kMix = N < 16 ? N : 16;
+  return r * N + (c ^ (r / (16 / kMix) % kMix));
+}
+
+// A thread's codes and parameters of one step.
+template <int D, int G>
+struct TileCodes {
+  static constexpr int kWords = TileShape<D>::kWords, kPerGroup = D / 32 / G;
+  static constexpr int kGroups = kWords > kPerGroup ? kWords / kPerGroup : 1;  // that the thread's words have
+  uint32_t k[kWords], v[kWords];
+  uint32_t kp[kGroups];
+  uint2 vp[kGroups];
+  int page;
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView v, AttendArgs a, AttendList list) {
+  using T = TileShape<D>;
+  using Codes = TileCodes<D, G>;
+  constexpr int kTokens = T::kTokens, kWords = T::kWords, kSlices = D / 16, kParts = kTokens / 32;
+  __shared__ uint4 keys0[kTokens * D / 8], keys1[kTokens * D / 8];    // [token][D / 8]
+  __shared__ int there0[kTokens / 16], there1[kTokens / 16];          // whether 16 tokens have a page
+  __shared__ uint4 vals0[kTokens * D / 8], vals1[kTokens * D / 8];    // [channel][kTokens / 8]
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), h = lane >> 5, c = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  int before;
+  const int total = attend_units(v, a, list, 0, lane, before);
+  const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
+  int unit, to, s;
+  AttendSplit split{};
+  if (a.direct) {  // one item a block, the heads of a tile together, a sequence's last tiles first
+    const int tile = blockIdx.x / v.heads;
+    int j;
+    s = attend_find_tile(v, a, list, tile, lane, before, j);
+    if (s >= v.seqs) return;
+    const AttendSeq w = attend_seq(v, a, list, s);
+    j = w.tiles - 1 - j;
+    unit = before;
+    for (int i = 0; i < j; ++i) unit += attend_chunks(a, list, w, i) * v.heads;
+    const int n = attend_chunks(a, list, w, j);
+    unit += (int)(blockIdx.x - tile * v.heads) * n;
+    to = unit + n;
+  } else {
+    if ((int)blockIdx.x >= blocks) {
+      attend_split(a, split);
+      return;
+    }
+    unit = block_start(blockIdx.x, blocks, total);
+    to = block_start(blockIdx.x + 1, blocks, total);
+    s = attend_find(v, a, list, unit, lane, before);
+  }
+
+  // the thread's part of a step's codes: 16 tokens' keys, then values
+  const int sub = tid / T::kUnitThreads, in = tid % T::kUnitThreads;
+  constexpr int kPerToken = D / 8 / kWords;                       // threads of a token's keys
+  const int k_token = in / kPerToken, k_word = in % kPerToken * kWords;  // words h (D / 32) + s
+  const int k_h = k_word / (D / 32), k_s = k_word % (D / 32);
+  constexpr int kPerCell = D / 32 / kWords;                       // threads of a lane's values (h, c)
+  const int v_h = in / kPerCell / 16, v_c = in / kPerCell % 16, v_w = in % kPerCell * (kWords / 2);
+
+  while (unit < to && s < v.seqs) {
+    const AttendSeq w = attend_seq(v, a, list, s);
+    const int at = unit - before;
+    if (at < 0) break;  // sums that wrapped (wrong rows)
+    if (at >= w.units) {
+      before += w.units;
+      ++s;
+      continue;
+    }
+    const AttendItem x = attend_item(v, a, list, w, at);
+    const int u0 = x.chunk, u1 = x.chunks - u0 < to - unit ? x.chunks : u0 + (to - unit);
+
+    const int r0 = x.tile * T::kRows, r1 = (r0 + T::kRows < w.flat ? r0 + T::kRows : w.flat) - 1;
+    const int p0 = w.q.length - w.q.rows, last = w.q.tokens - 1;
+    // the wave's rows
+    const int wr0 = r0 + 32 * wave, wr1 = wr0 + 31 < r1 ? wr0 + 31 : r1;
+    const int row = wr0 + c, rin = row <= r1 ? row : r1;
+    const int token = rin / a.share, q_head = x.head * a.share + rin - token * a.share;
+    const int p = p0 + token;
+    const int hi = a.causal && p < last ? p : last, lo = a.window > 0 ? p - a.window + 1 : 0;
+    half8w q[kSlices];
+    {
+      const uint16_t* qr = a.q + (w.q.row0 + token) * a.q_ld + (int64_t)q_head * D;
+#pragma unroll
+      for (int t = 0; t < kSlices; ++t) {
+        const uint4 b = row <= r1 ? *reinterpret_cast<const uint4*>(qr + 16 * t + 8 * h) : make_uint4(0, 0, 0, 0);
+        q[t] = __builtin_bit_cast(half8w, b);
+      }
+    }
+    // tokens that all of the wave's rows see, that any does, and that any of the block's does
+    const int pa = p0 + wr0 / a.share, pb = p0 + wr1 / a.share, pe = p0 + r1 / a.share;
+    const int all_hi = a.causal && pa < last ? pa : last, any_hi = a.causal && pb < last ? pb : last;
+    const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
+    const int end = (a.causal && pe < last ? pe : last) + 1;
+    const int t0 = w.first + u0 * kAttendChunk;
+    const int t1 = w.first + u1 * kAttendChunk < end ? w.first + u1 * kAttendChunk : end;
+    const bool rows = wr0 <= r1;
+
+    f32x16w o[D / 32];
+    float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n) o[n] = f32x16w{};
+
+    const auto page_at = [&](int tb) {  // of the thread's 16 tokens
+      const int t = tb + 16 * sub;
+      return t < t1 ? v.page_of(s, t) : -1;
+    };
+    const auto load = [&](Codes& d, int page, int tb) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) d.k[i] = d.v[i] = 0;
+#pragma unroll
+      for (int i = 0; i < Codes::kGroups; ++i) d.kp[i] = 0, d.vp[i] = make_uint2(0, 0);
+      d.page = page;
+      if (page < 0) return;
+      const int place = (tb + 16 * sub) & ((1 << v.page_shift) - 1);
+      const int64_t part = (int64_t)page * v.heads + x.head;
+      const uint8_t* kb = v.k_codes + part * v.code_bytes() + (int64_t)(place + k_token) * (D / 2) + 4 * k_word;
+      const uint8_t* vb = v.v_codes + part * v.code_bytes() + (int64_t)place * (D / 2) + 4 * kWords * in;
+      if constexpr (kWords == 2) {
+        const uint2 y = *reinterpret_cast<const uint2*>(kb), z = *reinterpret_cast<const uint2*>(vb);
+        d.k[0] = y.x, d.k[1] = y.y, d.v[0] = z.x, d.v[1] = z.y;
+      } else {
+        const uint4 y = *reinterpret_cast<const uint4*>(kb), z = *reinterpret_cast<const uint4*>(vb);
+        d.k[0] = y.x, d.k[1] = y.y, d.k[2] = y.z, d.k[3] = y.w;
+        d.v[0] = z.x, d.v[1] = z.y, d.v[2] = z.z, d.v[3] = z.w;
+      }
+      const uint16_t* kq = v.k_params + part * v.param_words() + place + k_token;
+      const uint16_t* vq = v.v_params + part * v.param_words() + place + 4 * v_h;
+#pragma unroll
+      for (int i = 0; i < Codes::kGroups; ++i) {
+        d.kp[i] = kq[(int64_t)(k_s / Codes::kPerGroup + i) << v.page_shift];
+        d.vp[i] = *reinterpret_cast<const uint2*>(vq + ((int64_t)(2 * v_w / Codes::kPerGroup + i) << v.page_shift));
+      }
+    };
+    const auto widen = [&](const Codes& d, int tb, uint4* keys, uint4* vals, int* there) {
+      const uint32_t magic = 0x64006400u;
+      if (in == 0) there[sub] = d.page >= 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t kp = d.kp[i / Codes::kPerGroup];
+        const Params2 y = params2(kp | kp << 16);
+        const half8w b = widen_word(d.k[i], y.zz, y.zz64, y.s2, magic);
+        keys[swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
+      }
+      // what lies behind the sequence's last token may be anything, an infinite scale too
+      const int behind = tb + 16 * sub + 4 * v_h - last;  // token i of the four: behind + i > 0
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {  // channels v_c + 16 (4 (v_w + i) + j)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {         // j = 2 g, 2 g + 1: one group
+          uint2 vp = d.vp[(2 * i + g) / Codes::kPerGroup];
+          if (behind > -4) {
+            vp.x &= (behind > 0 ? 0 : 0xFFFFu) | (behind + 1 > 0 ? 0 : 0xFFFF0000u);
+            vp.y &= (behind + 2 > 0 ? 0 : 0xFFFFu) | (behind + 3 > 0 ? 0 : 0xFFFF0000u);
+          }
+          const Params2 y = params2(vp.x), z = params2(vp.y);
+          half2w e[4], f[4];
+          widen4(d.v[2 * i], y.zz, y.zz64, y.s2, e);
+          widen4(d.v[2 * i + 1], z.zz, z.zz64, z.s2, f);
+#pragma unroll
+          for (int j = 2 * g; j < 2 * g + 2; ++j) {
+            const int ch = v_c + 16 * (4 * (v_w + i) + j);
+            uint2* slot = reinterpret_cast<uint2*>(vals + swizzled<kTokens / 8>(ch, 2 * sub + (v_h & 1)));
+            slot[v_h >> 1] = make_uint2(__builtin_bit_cast(uint32_t, e[j]), __builtin_bit_cast(uint32_t, f[j]));
+          }
+        }
+      }
+    };
+    const auto multiply = [&](int tb, const uint4* keys, const uint4* vals, const int* there) {
+      if (!rows || tb > any_hi || tb + kTokens <= any_lo) return;
+      f32x16w sc[kParts];
+#pragma unroll
+      for (int t = 0; t < kParts; ++t) {
+        sc[t] = f32x16w{};
+#pragma unroll
+        for (int i = 0; i < kSlices; ++i) {
+          const half8w b = __builtin_bit_cast(half8w, keys[swizzled<D / 8>(32 * t + c, 2 * i + h)]);
+          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, q[i], sc[t], 0, 0, 0);
+        }
+      }
+      // 16 tokens without a page, by bits
+      const uint64_t gone = __ballot(there[lane % (kTokens / 16)] == 0);
+      if (gone || tb + kTokens > all_hi + 1 || tb < all_lo) {
+#pragma unroll
+        for (int t = 0; t < kParts; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int tok = tb + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
+            if (!(tok >= lo && tok <= hi) || (gone >> (2 * t + (i >> 3)) & 1)) sc[t][i] = -__builtin_inff();
+          }
+      }
+      float top = sc[0][0];
+#pragma unroll
+      for (int t = 0; t < kParts; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
+      top *= a.scale_log2;
+      if (__ballot(top > m + kLazy)) {
+        top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m);
+        const float f = top > m ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) o[n] *= f;
+      }
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+      half8w pr[kParts][2];
+#pragma unroll
+      for (int t = 0; t < kParts; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.scale_log2, -base));
+          l += e;
+          pr[t][i >> 3][i & 7] = (_Float16)e;
+        }
+#pragma unroll
+      for (int t = 0; t < kParts; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < D / 32; ++n) {
+            const half8w b =
+                __builtin_bit_cast(half8w, vals[swizzled<kTokens / 8>(32 * n + c, 2 * (2 * t + k) + h)]);
+            o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, pr[t][k], o[n], 0, 0, 0);
+          }
+    };
+
+    Codes next;
+    int page = page_at(t0);
+    load(next, page, t0);
+    page = page_at(t0 + kTokens);
+    __syncthreads();  // the item before is done with the buffers
+    widen(next, t0, keys0, vals0, there0);
+    load(next, page, t0 + kTokens);
+    page = page_at(t0 + 2 * kTokens);
+    __syncthreads();
+    for (int tb = t0; tb < t1; tb += 2 * kTokens) {
+      widen(next, tb + kTokens, keys1, vals1, there1);
+      load(next, page, tb + 2 * kTokens);
+      page = page_at(tb + 3 * kTokens);
+      multiply(tb, keys0, vals0, there0);
+      __syncthreads();
+      if (tb + kTokens >= t1) break;
+      widen(next, tb + 2 * kTokens, keys0, vals0, there0);
+      load(next, page, tb + 3 * kTokens);
+      page = page_at(tb + 4 * kTokens);
+      multiply(tb + kTokens, keys1, vals1, there1);
+      __syncthreads();
+    }
+
+    const bool alone = u0 == 0 && u1 == x.chunks;
+    if (u1 < x.chunks) {
+      const int b0 = block_of(unit - u0, blocks, total), b1 = block_of(unit - u0 + x.chunks - 1, blocks, total);
+      split = AttendSplit{w.q.row0, r0, r1, x.head, b1 - b0 + 1, (int)blockIdx.x - b0};
+    }
+    l += __shfl_xor(l, 32);
+    if (rows && row <= r1) {
+      if (alone) {
+        const float d = l == 0.0f ? 0.0f : 1.0f / l;  // no token: zeros
+        uint16_t* y = a.out + (w.q.row0 + token) * a.out_ld + (int64_t)q_head * D;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            half4a b;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = (_Float16)(o[n][i + k] * d);
+            *reinterpret_cast<half4a*>(y + 32 * n + 2 * i + 4 * h) = b;
+          }
+        if (a.lse && h == 0)
+          a.lse[(int64_t)(w.q.row0 + token) * a.q_heads + q_head] = attend_lse(m, l);
+      } else {
+        const int64_t slot = ((int64_t)2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * T::kRows + (row - r0);
+        float* y = a.part + slot * D;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4w*>(y + 32 * n + 2 * i + 4 * h) =
+                f32x4w{o[n][i], o[n][i + 1], o[n][i + 2], o[n][i + 3]};
+        if (h == 0) a.part_ml[slot] = make_float2(m, l);
+      }
+    }
+    unit += u1 - u0;
+  }
+  attend_split(a, split);
+}
+
+template <int D, int G>
+hipError_t attend_tiles(const KvView& v, const AttendArgs& a, const AttendList& list, hipStream_t stream) {
+  hipLaunchKernelGGL((k_attend_tiles<D, G>), dim3(a.blocks), dim3(TileShape<D>::kThreads), 0, stream, v, a, list);
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -82,6 +82,15 @@ __device__ __forceinline__ int kv_find(const KvView& v, int t, int lane) {
   return lo;
 }
 
+// An item (rows of one sequence and head of keys) that several blocks took, one after the other.
+struct AttendSplit {
+  int row0;    // the sequence's first row
+  int r0, r1;  // the item's rows x heads of the sequence
+  int head;    // of keys
+  int blocks;  // 0: none
+  int index;   // which of them this is
+};
+
 // Queries of one attention call, beside the batch.
 struct AttendArgs {
   const uint16_t* q;  // rows of q_heads heads, q_ld apart
@@ -89,11 +98,14 @@ struct AttendArgs {
   float* lse;         // [n_rows][q_heads] or NULL
   int64_t q_ld, out_ld;
   int q_heads, share;  // share = q_heads / heads of keys
-  float scale, scale_log2;
+  float scale_log2;    // scale / ln 2
   int causal, window;  // window 0: none
-  int blocks;          // of the streaming kernel
-  float* part;         // their partial sums [2 blocks][rows of a tile][dim] ...
-  float2* part_ml;     // ... and (maximum, sum) [2 blocks][rows of a tile]
+  // of one kernel: its blocks; their sums, unnormalised [2 blocks][rows of a tile][dim], with (maximum
+  // of log2, sum) [2 blocks][rows]: item that went on from the block before, item that goes on
+  int blocks, direct;
+  float* part;
+  float2* part_ml;
+  AttendSplit* split;  // [blocks], NULL: nothing is split
 };
 
 hipError_t launch_kv_append(const KvView& c, const uint16_t* q, int64_t q_ld, int q_heads, uint16_t* out,
@@ -102,15 +114,19 @@ hipError_t launch_kv_append(const KvView& c, const uint16_t* q, int64_t q_ld, in
                             hipStream_t stream);
 hipError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, hipStream_t stream);
 
-// Attention (kv_attend.hip): plan() fills in what depends on the sizes alone.
+// Attention (kv_attend.hip). The plan goes by what the host knows: sizes, not lengths.
+struct AttendPart {  // one kernel's share
+  int tile;          // rows of a tile; 0: the kernel does not run
+  int blocks;
+  bool direct, join; // one item a block; items may be split over blocks
+  size_t part, part_ml, split;  // offsets in the workspace
+};
 struct AttendPlan {
-  int tiles;            // 16-row tiles of a block of the streaming kernel
-  int blocks;           // its blocks
-  bool join;            // items may be split over blocks
-  size_t part, part_ml; // offsets in the workspace
-  size_t bytes;         // of the workspace
+  AttendPart stream, tiles;
+  int few;       // rows x share up to which a sequence is streamed
+  size_t bytes;  // of the workspace
 };
 AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim);
-hipError_t launch_attend(const KvView& c, const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
+hipError_t launch_attend(const KvView& c, AttendArgs a, const AttendPlan& p, void* workspace, hipStream_t stream);
 
 }  // namespace awq
