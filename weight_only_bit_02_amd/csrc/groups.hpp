@@ -117,4 +117,12 @@ __device__ __forceinline__ void dma16_own(u32x4 b, uint32_t to, uint32_t lane_at
 #endif
 }
 
+// dma16_own with 4 bytes per lane.
+__device__ __forceinline__ void dma4_own(u32x4 b, uint32_t to, uint32_t lane_at, uint32_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(lane_at), "s"(b), "s"(at), "{m0}"(to)
+               : "memory");
+#endif
+}
+
 }  // namespace awq

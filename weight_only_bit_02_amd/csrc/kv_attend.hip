@@ -15,7 +15,10 @@ AWQ_DECLARE(256)
 namespace {
 
 constexpr int kFew = 64;
-constexpr int kStreamBlocks = 1024;  // four blocks a CU
+#ifndef KBLK
+#define KBLK 1024
+#endif
+constexpr int kStreamBlocks = KBLK;
 constexpr int kTileBlocks = 256;     // one block a CU
 constexpr int64_t kDirectItems = 512;
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }

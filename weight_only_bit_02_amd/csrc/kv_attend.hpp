@@ -20,9 +20,18 @@
 
 namespace awq {
 
+#define AWQ_INLINE __attribute__((always_inline))
 constexpr int kAttendWaves = 4;
-constexpr int kAttendStep = 64;                          // tokens of a wave's step
-constexpr int kAttendChunk = kAttendStep * kAttendWaves;  // tokens of the work list's unit
+constexpr int kAttendChunk = 256;  // tokens of the work list's unit, a multiple of every kernel's step
+#ifndef KUNITS
+#define KUNITS 2
+#endif
+#ifndef KST
+#define KST 2
+#endif
+#ifndef KWPE
+#define KWPE 4
+#endif
 constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score passes it by 2^8
 
 constexpr int kJoinThreads = 256;
@@ -61,7 +70,7 @@ __device__ __forceinline__ AttendSeq attend_seq(const KvView& v, const AttendArg
   w.first = 0;
   if (a.window > 0) {
     const int64_t lo = (int64_t)w.q.length - w.q.rows - a.window + 1;
-    w.first = lo <= 0 ? 0 : (int)(lo < w.q.tokens ? lo : w.q.tokens) & ~(kAttendStep - 1);
+    w.first = lo <= 0 ? 0 : (int)(lo < w.q.tokens ? lo : w.q.tokens) & ~63;
   }
   w.units = 0;
   for (int j = 0; j < w.tiles; ++j) w.units += attend_chunks(a, g, w, j);
@@ -87,65 +96,75 @@ __device__ __forceinline__ AttendItem attend_item(const KvView& v, const AttendA
   return x;
 }
 
-// First unit of block b of n, of `total` units (n at most total: no block between two others is
-// without a unit); and the block that unit x belongs to.
-__device__ __forceinline__ int block_start(int b, int n, int total) { return (int)((int64_t)b * total / n); }
-__device__ __forceinline__ int block_of(int x, int n, int total) {
-  return (int)((((int64_t)x + 1) * n - 1) / total);
-}
-
-// Units of all sequences, and of those before sequence s (uniform over the wave).
-__device__ __forceinline__ int attend_units(const KvView& v, const AttendArgs& a, const AttendList& g, int s, int lane,
-                                            int& before) {
-  int total = 0;
-  before = 0;
-  for (int i = 0; i < v.seqs; i += kWave) {
-    const int n = i + lane < v.seqs ? attend_seq(v, a, g, i + lane).units : 0;
-    total += __builtin_amdgcn_readlane(wave_scan(n), kWave - 1);
-    before += __builtin_amdgcn_readlane(wave_scan(i + lane < s ? n : 0), kWave - 1);
+// The list's `total` units in one piece for each of n blocks (n at most total, so that every block
+// has some): the first `more` have one unit more than the rest.
+struct AttendCut {
+  int each, more;
+  __device__ __forceinline__ AttendCut(int total, int n) {
+    each = (int)((unsigned)total / (unsigned)n);
+    more = total - each * n;
   }
-  return total;
-}
+  __device__ __forceinline__ int start(int b) const { return b * each + (b < more ? b : more); }
+  __device__ __forceinline__ int block(int x) const {  // of unit x
+    const unsigned wide = (unsigned)more * (each + 1);
+    return (unsigned)x < wide ? (unsigned)x / (unsigned)(each + 1) : more + ((unsigned)x - wide) / (unsigned)each;
+  }
+};
 
-// The sequence that holds unit x of the list, and the units before it (uniform over the wave).
-__device__ __forceinline__ int attend_find(const KvView& v, const AttendArgs& a, const AttendList& g, int x, int lane,
-                                           int& before) {
-  before = 0;
-  for (int i = 0; i < v.seqs; i += kWave) {
-    const int n = i + lane < v.seqs ? attend_seq(v, a, g, i + lane).units : 0;
-    const int sum = wave_scan(n);
-    const uint64_t m = __ballot(before + sum > x);
-    if (m) {
-      const int at = __ffsll((unsigned long long)m) - 1;
-      before += __builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(n, at);
-      return i + at;
+// The batch's sequences, 64 at a time, one to a lane: what a wave has once read it finds there.
+struct AttendSeqs {
+  const KvView& v;
+  const AttendArgs& a;
+  const AttendList& g;
+  int lane, base;
+  AttendSeq mine;
+
+  __device__ __forceinline__ AttendSeqs(const KvView& v, const AttendArgs& a, const AttendList& g, int lane)
+      : v(v), a(a), g(g), lane(lane), base(-1) {}
+  __device__ __forceinline__ void fetch(int i) {
+    if (i == base) return;
+    base = i;
+    mine = AttendSeq{};
+    if (i + lane < v.seqs) mine = attend_seq(v, a, g, i + lane);
+  }
+  // Sequence s (uniform), of those fetched last.
+  __device__ __forceinline__ AttendSeq get(int s) const {
+    const int at = s & (kWave - 1);
+    const auto of = [&](int x) AWQ_INLINE { return __builtin_amdgcn_readlane(x, at); };
+    AttendSeq w;
+    w.q = KvSeq{of(mine.q.row0), of(mine.q.rows), of(mine.q.length), of(mine.q.tokens)};
+    w.flat = of(mine.flat), w.tiles = of(mine.tiles), w.first = of(mine.first), w.units = of(mine.units);
+    return w;
+  }
+  // Units of all sequences.
+  __device__ __forceinline__ int units() {
+    int total = 0;
+    for (int i = 0; i < v.seqs; i += kWave) {
+      fetch(i);
+      total += __builtin_amdgcn_readlane(wave_scan(mine.units), kWave - 1);
     }
-    before += __builtin_amdgcn_readlane(sum, kWave - 1);
+    return total;
   }
-  return v.seqs;
-}
-
-// The sequence with tile x of all tiles, the units before it, and which of its tiles it is.
-__device__ __forceinline__ int attend_find_tile(const KvView& v, const AttendArgs& a, const AttendList& g, int x,
-                                                int lane, int& before, int& tile) {
-  int tiles = 0;
-  before = 0;
-  for (int i = 0; i < v.seqs; i += kWave) {
-    AttendSeq w{};
-    if (i + lane < v.seqs) w = attend_seq(v, a, g, i + lane);
-    const int sum = wave_scan(w.tiles), units = wave_scan(w.units);
-    const uint64_t m = __ballot(tiles + sum > x);
-    if (m) {
-      const int at = __ffsll((unsigned long long)m) - 1;
-      before += __builtin_amdgcn_readlane(units, at) - __builtin_amdgcn_readlane(w.units, at);
-      tile = x - tiles - __builtin_amdgcn_readlane(sum, at) + __builtin_amdgcn_readlane(w.tiles, at);
-      return i + at;
+  // The sequence that holds unit x (or, tiles = true, tile x of all tiles); the units and tiles
+  // before it.
+  __device__ __forceinline__ int find(int x, bool tiles, int& units_before, int& tiles_before) {
+    units_before = tiles_before = 0;
+    for (int i = 0; i < v.seqs; i += kWave) {
+      fetch(i);
+      const int u = wave_scan(mine.units), t = wave_scan(mine.tiles);
+      const uint64_t m = __ballot((tiles ? tiles_before + t : units_before + u) > x);
+      if (m) {
+        const int at = __ffsll((unsigned long long)m) - 1;
+        units_before += __builtin_amdgcn_readlane(u, at) - __builtin_amdgcn_readlane(mine.units, at);
+        tiles_before += __builtin_amdgcn_readlane(t, at) - __builtin_amdgcn_readlane(mine.tiles, at);
+        return i + at;
+      }
+      units_before += __builtin_amdgcn_readlane(u, kWave - 1);
+      tiles_before += __builtin_amdgcn_readlane(t, kWave - 1);
     }
-    tiles += __builtin_amdgcn_readlane(sum, kWave - 1);
-    before += __builtin_amdgcn_readlane(units, kWave - 1);
+    return v.seqs;
   }
-  return v.seqs;
-}
+};
 
 // What block b leaves for k_attend_join (thread 0): the item that the next block goes on with.
 __device__ __forceinline__ void attend_split(const AttendArgs& a, const AttendSplit& d) {
@@ -155,12 +174,28 @@ __device__ __forceinline__ void attend_split(const AttendArgs& a, const AttendSp
 // log of a row's sum of exponentials from its maximum (of log2) and sum; -inf without a token.
 __device__ __forceinline__ float attend_lse(float m, float l) { return m * 0.69314718055994531f + __logf(l); }
 
+// (a & mask) | magic in one instruction (with two constants the compiler takes two): the mask in a
+// scalar register, the magic in a vector register.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "s"(mask), "v"(magic));
+  return r;
+}
+struct Magic {  // the exponents under which a nibble at bits 0..3, and at 4..7, counts ones
+  uint32_t m64, m54;
+};
+__device__ __forceinline__ Magic magics() {
+  Magic m;
+  asm volatile("v_mov_b32 %0, 0x64006400\n\tv_mov_b32 %1, 0x54005400" : "=v"(m.m64), "=v"(m.m54));
+  return m;
+}
+
 // (code - zero) scale of the four nibbles of each half of w, pairs by nibble: zz = -(1024 + z),
 // zz64 = -(64 + z), s2 = scale, of the low and of the high half.
-__device__ __forceinline__ void widen4(uint32_t w, half2w zz, half2w zz64, half2w s2, half2w (&d)[4]) {
+__device__ __forceinline__ void widen4(uint32_t w, half2w zz, half2w zz64, half2w s2, Magic m, half2w (&d)[4]) {
   const uint32_t w8 = w >> 8;
-  const uint32_t u0 = (w & 0x000F000Fu) | 0x64006400u, u1 = (w & 0x00F000F0u) | 0x54005400u;
-  const uint32_t u2 = (w8 & 0x000F000Fu) | 0x64006400u, u3 = (w8 & 0x00F000F0u) | 0x54005400u;
+  const uint32_t u0 = and_or(w, 0x000F000Fu, m.m64), u1 = and_or(w, 0x00F000F0u, m.m54);
+  const uint32_t u2 = and_or(w8, 0x000F000Fu, m.m64), u3 = and_or(w8, 0x00F000F0u, m.m54);
   d[0] = (__builtin_bit_cast(half2w, u0) + zz) * s2;
   d[1] = (__builtin_bit_cast(half2w, u1) + zz64) * s2;
   d[2] = (__builtin_bit_cast(half2w, u2) + zz) * s2;
@@ -176,34 +211,83 @@ __device__ __forceinline__ Params2 params2(uint32_t p) {
                  __builtin_bit_cast(half2w, p & 0xFFF0FFF0u)};
 }
 
+// A wave's buffers of the streaming kernel: one step's codes and parameters each.
+template <int D, int G>
+struct StreamShape {
+  static constexpr int kUnits = KUNITS;   // of 16 tokens, of a step
+  static constexpr int kStages = KST;
+  static constexpr int kCodes = 8 * D;    // bytes of a unit's keys, or values
+  static constexpr int kParams = 32 * G;  // of their parameters, [group][token]
+  static constexpr int kStage = 2 * kUnits * (kCodes + kParams);
+  static constexpr int kSends = kUnits * (2 * (D == 256 ? 2 : 1) + 2);  // DMA instructions of a step
+  static constexpr int k_codes(int u) { return u * kCodes; }
+  static constexpr int v_codes(int u) { return (kUnits + u) * kCodes; }
+  static constexpr int k_params(int u) { return 2 * kUnits * kCodes + u * kParams; }
+  static constexpr int v_params(int u) { return k_params(kUnits + u); }
+
+  // A lane's words of a unit: D / 32 slices of token c's keys, or of four tokens' values. They lie in
+  // the lanes' order, 16 bytes each at a time (D = 64: as in the cache).
+  static __device__ __forceinline__ void key_words(const char* p, int lane, uint32_t (&w)[D / 32]) {
+    if constexpr (D == 64) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p + (lane & 15) * 32 + (lane >> 4) * 8);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      value_words(p, lane, w);
+    }
+  }
+  static __device__ __forceinline__ void value_words(const char* p, int lane, uint32_t (&w)[D / 32]) {
+    if constexpr (D == 64) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p + lane * 8);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + 1024 * i + 16 * lane);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+    }
+  }
+};
+
 // D channels, G groups of them, R tiles of 16 rows.
 template <int D, int G, int R>
-__global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
+__global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_waves_per_eu(R == 2 ? (D == 256 ? 1 : 2) : D == 256 ? 2 : KWPE))) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
   constexpr int kSlices = D / 32, kTiles = D / 16, kPerGroup = kSlices / G;  // slices of a group
+  using S = StreamShape<D, G>;
+  constexpr int kUnits = S::kUnits, kStep = 16 * kUnits, kStages = S::kStages;
   constexpr int kPad = 68;
-  __shared__ float sums[kAttendWaves][16][kPad];
+  using Sums = float[kAttendWaves][16][kPad];
+  constexpr int kRing = kAttendWaves * kStages * S::kStage;
+  __shared__ __attribute__((aligned(16))) char smem[kRing > (int)sizeof(Sums) ? kRing : (int)sizeof(Sums)];
+  Sums& sums = *reinterpret_cast<Sums*>(smem);  // after an item's last step
   __shared__ float2 ml[kAttendWaves][16];
 
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  int before;
-  const int total = attend_units(v, a, list, 0, lane, before);
+  const uint32_t ring = lds_address(reinterpret_cast<uint4*>(smem + wave * kStages * S::kStage));
+  const Magic magic = magics();
+  AttendSeqs seqs(v, a, list, lane);
+  const int total = seqs.units();
   const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
   AttendSplit split{};
   if ((int)blockIdx.x >= blocks) {
     attend_split(a, split);
     return;
   }
-  const int from = block_start(blockIdx.x, blocks, total), to = block_start(blockIdx.x + 1, blocks, total);
-  int s = attend_find(v, a, list, from, lane, before);
+  const AttendCut cut(total, blocks);
+  const int from = cut.start(blockIdx.x), to = cut.start(blockIdx.x + 1);
+  int before, tiles_before;
+  int s = seqs.find(from, false, before, tiles_before);
+  if (s >= v.seqs) return;  // (wrong rows)
+  AttendSeq w = seqs.get(s);
   int unit = from;
-  while (unit < to && s < v.seqs) {
-    const AttendSeq w = attend_seq(v, a, list, s);
+  while (unit < to) {
     const int at = unit - before;
     if (at < 0) break;  // sums that wrapped (wrong rows)
     if (at >= w.units) {
       before += w.units;
-      ++s;
+      if (++s >= v.seqs) break;
+      w = attend_seq(v, a, list, s);
       continue;
     }
     const AttendItem x = attend_item(v, a, list, w, at);
@@ -246,106 +330,108 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
       for (int n = 0; n < kTiles; ++n) o[r][n] = f32x4w{0, 0, 0, 0};
     }
 
-    const int64_t code_head = v.code_bytes(), par_head = v.param_words();
-    int pages = -1;  // lane 4 k + u: the page of unit u of the wave's step k of 16
-    for (int tb = t0 + wave * kAttendStep, k = 0; tb < t1; tb += kAttendChunk, ++k) {
-      if ((k & 15) == 0) pages = v.page_of(s, (int64_t)tb + (lane >> 2) * kAttendChunk + (lane & 3) * 16);
-      // codes and parameters of 64 tokens: units of 16
-      uint32_t kc[4][kSlices], vc[4][kSlices];
-      uint32_t kp[4][G];
-      uint2 vp[4][G];
-      int page[4];
+    // Codes and parameters of a step go to one of the wave's own buffers by DMA, kStages - 1 steps
+    // ahead: nobody else waits for them. A unit without a page (or behind t1) takes page 0's.
+    const uint32_t code_page = v.heads * (uint32_t)v.code_bytes(), par_page = v.heads * (uint32_t)v.param_words();
+    const uint8_t* const kb0 = v.k_codes + head * v.code_bytes();
+    const uint8_t* const vb0 = v.v_codes + head * v.code_bytes();
+    const uint16_t* const kq0 = v.k_params + head * v.param_words();
+    const uint16_t* const vq0 = v.v_params + head * v.param_words();
+    int pages = -1;      // lane kUnits k + u: the page of unit u of the wave's step k of 64 / kUnits
+    uint64_t gone = 0;   // units without a page of the steps sent, the last one's in the lowest bits
+    const auto send = [&](int k) AWQ_INLINE {
+      constexpr int kMany = kWave / kUnits;
+      const int tb = t0 + (wave + k * kAttendWaves) * kStep;
+      if (k % kMany == 0)
+        pages = v.page_of(s, (int64_t)tb + lane / kUnits * (kAttendWaves * kStep) + lane % kUnits * 16);
+      const uint32_t to = ring + (uint32_t)(k % kStages) * S::kStage;
+      u32x4 kb, vb, kq, vq;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer's last reads
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        page[u] = __builtin_amdgcn_readlane(pages, 4 * (k & 15) + u);
-        if (tb + 16 * u >= t1) page[u] = -1;
-        if (page[u] >= 0) {
-          const int place = (tb + 16 * u) & ((1 << v.page_shift) - 1);
-          const int64_t at = (int64_t)page[u] * v.heads + head;
-          const uint8_t* kb = v.k_codes + at * code_head + (int64_t)place * (D / 2);
-          const uint8_t* vb = v.v_codes + at * code_head + (int64_t)place * (D / 2);
-          // D / 8 bytes a lane
-          if constexpr (kSlices == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(kb + c * (D / 2) + h * (D / 8));
-            const uint2 y = *reinterpret_cast<const uint2*>(vb + lane * (D / 8));
-            kc[u][0] = x.x, kc[u][1] = x.y, vc[u][0] = y.x, vc[u][1] = y.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < kSlices; i += 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(kb + c * (D / 2) + h * (D / 8) + 4 * i);
-              const uint4 y = *reinterpret_cast<const uint4*>(vb + lane * (D / 8) + 4 * i);
-              kc[u][i] = x.x, kc[u][i + 1] = x.y, kc[u][i + 2] = x.z, kc[u][i + 3] = x.w;
-              vc[u][i] = y.x, vc[u][i + 1] = y.y, vc[u][i + 2] = y.z, vc[u][i + 3] = y.w;
-            }
-          }
-          const uint16_t* kpar = v.k_params + at * par_head + place;
-          const uint16_t* vpar = v.v_params + at * par_head + place;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            kp[u][g] = kpar[((int64_t)g << v.page_shift) + c];
-            vp[u][g] = *reinterpret_cast<const uint2*>(vpar + ((int64_t)g << v.page_shift) + 4 * h);
+      for (int u = 0; u < kUnits; ++u) {
+        int page = __builtin_amdgcn_readlane(pages, kUnits * (k % kMany) + u);
+        if (tb + 16 * u >= t1) page = -1;
+        gone = gone << 1 | (page < 0 ? 1 : 0);
+        if (u == 0 || v.page_shift == 4) {  // a step's tokens lie in one page of 32 or more
+          const uint32_t in = page < 0 ? 0 : page;
+          const uint32_t place = (uint32_t)(tb + 16 * u) & ((1u << v.page_shift) - 1);
+          const uint64_t code = (uint64_t)in * code_page + place * (D / 2), par = (uint64_t)in * par_page + place;
+          kb = buffer_words(kb0 + code), vb = buffer_words(vb0 + code);
+          kq = buffer_words(kq0 + par), vq = buffer_words(vq0 + par);
+        }
+        const uint32_t on = u == 0 || v.page_shift == 4 ? 0 : u;  // units behind the address
+        if constexpr (D == 64) {
+          if (lane < 32) {
+            dma16_own(kb, to + S::k_codes(u), lane * 16, on * S::kCodes);
+            dma16_own(vb, to + S::v_codes(u), lane * 16, on * S::kCodes);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kSlices; ++i) kc[u][i] = vc[u][i] = 0;
-#pragma unroll
-          for (int g = 0; g < G; ++g) kp[u][g] = 0, vp[u][g] = make_uint2(0, 0);
+          for (int i = 0; i < D / 128; ++i) {
+            dma16_own(kb, to + S::k_codes(u) + 1024 * i, c * (D / 2) + h * (D / 8) + 16 * i, on * S::kCodes);
+            dma16_own(vb, to + S::v_codes(u) + 1024 * i, lane * (D / 8) + 16 * i, on * S::kCodes);
+          }
+        }
+        if (G == 8 || lane < 8 * G) {  // group lane / 8, tokens 2 (lane % 8) and the next
+          const uint32_t at = (lane / 8) << (v.page_shift + 1) | 4 * (lane % 8);
+          dma4_own(kq, to + S::k_params(u), at, on * 32);
+          dma4_own(vq, to + S::v_params(u), at, on * 32);
         }
       }
+    };
+    const auto step = [&](int k, int ahead) AWQ_INLINE {
+      const int tb = t0 + (wave + k * kAttendWaves) * kStep;
+      const char* from = smem + (wave * kStages + k % kStages) * S::kStage;
+      const uint32_t none = (uint32_t)(gone >> (kUnits * ahead)) & ((1u << kUnits) - 1);  // unit 0 in the highest bit
       // scores
-      f32x4w sc[R][4];
+      f32x4w sc[R][kUnits];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kUnits; ++u) {
+        uint32_t kw[kSlices];
+        S::key_words(from + S::k_codes(u), lane, kw);
 #pragma unroll
         for (int r = 0; r < R; ++r) sc[r][u] = f32x4w{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const Params2 p = params2(kp[u][g] | kp[u][g] << 16);
+          const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(u))[16 * g + c];
+          const Params2 p = params2(kp | kp << 16);
 #pragma unroll
           for (int t = g * kPerGroup; t < (g + 1) * kPerGroup; ++t) {
-            half2w d[4];
-            widen4(kc[u][t], p.zz, p.zz64, p.s2, d);
-            const half8w key{d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
+            half2w e[4];
+            widen4(kw[t], p.zz, p.zz64, p.s2, magic, e);
+            const half8w key{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
 #pragma unroll
             for (int r = 0; r < R; ++r)
               sc[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[r][t], sc[r][u], 0, 0, 0);
           }
         }
       }
-      const bool whole = tb + kAttendStep <= all_hi + 1 && tb >= all_lo && tb + kAttendStep <= t1 &&
-                         (page[0] | page[1] | page[2] | page[3]) >= 0;
-      if (!whole) {
+      const bool part = tb + kStep > all_hi + 1 || tb < all_lo || tb + kStep > t1 || none != 0;
+      if (part) {
+        asm volatile("");  // nothing of this ahead of the branch
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kUnits; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = tb + 16 * u + 4 * h + i;
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              if (!(t >= lo[r] && t <= hi[r] && page[u] >= 0)) sc[r][u][i] = -__builtin_inff();
-            // what lies behind the sequence's last token may be anything, an infinite scale too
-            if (t > last) {
-#pragma unroll
-              for (int g = 0; g < G; ++g) {
-                uint32_t& p = i < 2 ? vp[u][g].x : vp[u][g].y;
-                p &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-              }
-            }
+              if (!(t >= lo[r] && t <= hi[r]) || (none >> (kUnits - 1 - u) & 1)) sc[r][u][i] = -__builtin_inff();
           }
-        }
       }
       // probabilities, as fp16 hi + lo: rounded to fp16 alone they would add as much to the output's
       // error as its own rounding does
-      half8w ph[R][2], pl[R][2];
+      half8w ph[R][kUnits / 2], pl[R][kUnits / 2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float top = sc[r][0][0];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kUnits; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][u][i]);
         top *= a.scale_log2;
         if (__ballot(top > m[r] + kLazy)) {
+          asm volatile("");
           top = fmaxf(top, __shfl_xor(top, 16));
           top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[r]);
           const float f = top > m[r] ? __builtin_amdgcn_exp2f(m[r] - top) : 1.0f;
@@ -356,35 +442,49 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
         }
         const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kUnits; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][u][i], a.scale_log2, -base));
             l[r] += e;
             const _Float16 hi16 = (_Float16)e;
             ph[r][u >> 1][4 * (u & 1) + i] = hi16;
-            pl[r][u >> 1][4 * (u & 1) + i] = (_Float16)(e - (float)hi16);
+            pl[r][u >> 1][4 * (u & 1) + i] = (_Float16)__builtin_fmaf(-(float)hi16, 1.0f, e);
           }
       }
       // O^T += V^T P^T, 32 tokens at a time
 #pragma unroll
-      for (int u = 0; u < 4; u += 2) {
+      for (int u = 0; u < kUnits; u += 2) {
+        uint32_t vw[2][kSlices];
+        S::value_words(from + S::v_codes(u), lane, vw[0]);
+        S::value_words(from + S::v_codes(u + 1), lane, vw[1]);
+        uint2 vp[2][G];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
+            if (part) {  // what no token wrote may be anything, an infinite scale too
+              const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
+              vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
+              vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
+            }
+          }
 #pragma unroll
         for (int t = 0; t < kSlices / 2; ++t) {  // tiles 4 t .. 4 t + 3, 64 channels
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // tiles 4 t + 2 half and the next: one group of 32 channels
             const int g = (2 * t + half) / kPerGroup;
-            half2w d[4][4];
+            half2w e[4][4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {  // token pairs
-              const uint2 two = vp[u + (b >> 1)][g];
-              const Params2 p = params2(b & 1 ? two.y : two.x);
-              widen4(vc[u + (b >> 1)][2 * t + (b & 1)], p.zz, p.zz64, p.s2, d[b]);
+              const Params2 p = params2(b & 1 ? vp[b >> 1][g].y : vp[b >> 1][g].x);
+              widen4(vw[b >> 1][2 * t + (b & 1)], p.zz, p.zz64, p.s2, magic, e[b]);
             }
 #pragma unroll
             for (int j = 2 * half; j < 2 * half + 2; ++j) {
-              const half8w val{d[0][j][0], d[0][j][1], d[1][j][0], d[1][j][1],
-                               d[2][j][0], d[2][j][1], d[3][j][0], d[3][j][1]};
+              const half8w val{e[0][j][0], e[0][j][1], e[1][j][0], e[1][j][1],
+                               e[2][j][0], e[2][j][1], e[3][j][0], e[3][j][1]};
 #pragma unroll
               for (int r = 0; r < R; ++r) {
                 o[r][4 * t + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(val, ph[r][u >> 1], o[r][4 * t + j], 0, 0, 0);
@@ -394,13 +494,29 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) k_attend_stream(KvView v,
           }
         }
       }
+    };
+    __syncthreads();  // the item before is done with the buffers
+    const int left = t1 - t0 - wave * kStep;
+    const int steps = left <= 0 ? 0 : (left + kAttendWaves * kStep - 1) / (kAttendWaves * kStep);
+    for (int k = 0; k < kStages - 1 && k < steps; ++k) send(k);
+    for (int k = 0; k < steps; ++k) {
+      const int ahead = steps - 1 - k < kStages - 1 ? steps - 1 - k : kStages - 1;
+      if (ahead == kStages - 1) {
+        send(k + kStages - 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * S::kSends) : "memory");
+      } else if (kStages > 2 && ahead > 0) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kSends) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      step(k, ahead);
     }
 
     // the waves' sums together
     const bool alone = u0 == 0 && u1 == x.chunks;
     const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
     if (u1 < x.chunks) {
-      const int b0 = block_of(unit - u0, blocks, total), b1 = block_of(unit - u0 + x.chunks - 1, blocks, total);
+      const int b0 = cut.block(unit - u0), b1 = cut.block(unit - u0 + x.chunks - 1);
       split = AttendSplit{w.q.row0, r0, r1, head, b1 - b0 + 1, (int)blockIdx.x - b0};
     }
 #pragma unroll

@@ -58,31 +58,36 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  int before;
-  const int total = attend_units(v, a, list, 0, lane, before);
-  const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
-  int unit, to, s;
+  const Magic magic = magics();
+  AttendSeqs seqs(v, a, list, lane);
+  int unit, to, s, before, tiles_before;
+  AttendSeq w;
   AttendSplit split{};
+  AttendCut cut(1, 1);
   if (a.direct) {  // one item a block, the heads of a tile together, a sequence's last tiles first
     const int tile = blockIdx.x / v.heads;
-    int j;
-    s = attend_find_tile(v, a, list, tile, lane, before, j);
+    s = seqs.find(tile, true, before, tiles_before);
     if (s >= v.seqs) return;
-    const AttendSeq w = attend_seq(v, a, list, s);
-    j = w.tiles - 1 - j;
+    w = seqs.get(s);
+    const int j = w.tiles - 1 - (tile - tiles_before);
     unit = before;
     for (int i = 0; i < j; ++i) unit += attend_chunks(a, list, w, i) * v.heads;
     const int n = attend_chunks(a, list, w, j);
     unit += (int)(blockIdx.x - tile * v.heads) * n;
     to = unit + n;
   } else {
+    const int total = seqs.units();
+    const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
     if ((int)blockIdx.x >= blocks) {
       attend_split(a, split);
       return;
     }
-    unit = block_start(blockIdx.x, blocks, total);
-    to = block_start(blockIdx.x + 1, blocks, total);
-    s = attend_find(v, a, list, unit, lane, before);
+    cut = AttendCut(total, blocks);
+    unit = cut.start(blockIdx.x);
+    to = cut.start(blockIdx.x + 1);
+    s = seqs.find(unit, false, before, tiles_before);
+    if (s >= v.seqs) return;  // (wrong rows)
+    w = seqs.get(s);
   }
 
   // the thread's part of a step's codes: 16 tokens' keys, then values
@@ -93,13 +98,13 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
   constexpr int kPerCell = D / 32 / kWords;                       // threads of a lane's values (h, c)
   const int v_h = in / kPerCell / 16, v_c = in / kPerCell % 16, v_w = in % kPerCell * (kWords / 2);
 
-  while (unit < to && s < v.seqs) {
-    const AttendSeq w = attend_seq(v, a, list, s);
+  while (unit < to) {
     const int at = unit - before;
     if (at < 0) break;  // sums that wrapped (wrong rows)
     if (at >= w.units) {
       before += w.units;
-      ++s;
+      if (++s >= v.seqs) break;
+      w = attend_seq(v, a, list, s);
       continue;
     }
     const AttendItem x = attend_item(v, a, list, w, at);
@@ -168,13 +173,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
       }
     };
     const auto widen = [&](const Codes& d, int tb, uint4* keys, uint4* vals, int* there) {
-      const uint32_t magic = 0x64006400u;
       if (in == 0) there[sub] = d.page >= 0;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const uint32_t kp = d.kp[i / Codes::kPerGroup];
         const Params2 y = params2(kp | kp << 16);
-        const half8w b = widen_word(d.k[i], y.zz, y.zz64, y.s2, magic);
+        half2w e[4];
+        widen4(d.k[i], y.zz, y.zz64, y.s2, magic, e);
+        const half8w b{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
         keys[swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
       }
       // what lies behind the sequence's last token may be anything, an infinite scale too
@@ -190,8 +196,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
           }
           const Params2 y = params2(vp.x), z = params2(vp.y);
           half2w e[4], f[4];
-          widen4(d.v[2 * i], y.zz, y.zz64, y.s2, e);
-          widen4(d.v[2 * i + 1], z.zz, z.zz64, z.s2, f);
+          widen4(d.v[2 * i], y.zz, y.zz64, y.s2, magic, e);
+          widen4(d.v[2 * i + 1], z.zz, z.zz64, z.s2, magic, f);
 #pragma unroll
           for (int j = 2 * g; j < 2 * g + 2; ++j) {
             const int ch = v_c + 16 * (4 * (v_w + i) + j);
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
       // 16 tokens without a page, by bits
       const uint64_t gone = __ballot(there[lane % (kTokens / 16)] == 0);
       if (gone || tb + kTokens > all_hi + 1 || tb < all_lo) {
+        asm volatile("");  // nothing of this ahead of the branch
 #pragma unroll
         for (int t = 0; t < kParts; ++t)
 #pragma unroll
@@ -231,6 +238,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
       top *= a.scale_log2;
       if (__ballot(top > m + kLazy)) {
+        asm volatile("");
         top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m);
         const float f = top > m ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
         m = top;
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 
     const bool alone = u0 == 0 && u1 == x.chunks;
     if (u1 < x.chunks) {
-      const int b0 = block_of(unit - u0, blocks, total), b1 = block_of(unit - u0 + x.chunks - 1, blocks, total);
+      const int b0 = cut.block(unit - u0), b1 = cut.block(unit - u0 + x.chunks - 1);
       split = AttendSplit{w.q.row0, r0, r1, x.head, b1 - b0 + 1, (int)blockIdx.x - b0};
     }
     l += __shfl_xor(l, 32);
