@@ -15,10 +15,11 @@ AWQ_DECLARE(256)
 namespace {
 
 constexpr int kFew = 64;
-#ifndef KBLK
-#define KBLK 1024
-#endif
-constexpr int kStreamBlocks = KBLK;
+// Blocks of the streaming kernel that the chip holds at once, by registers and LDS.
+int stream_blocks(int dim, int tile) {
+  const int each = dim == 256 ? (tile == 16 ? 2 : 1) : tile == 16 ? 4 : dim == 64 ? 3 : 2;
+  return 256 * each;
+}
 constexpr int kTileBlocks = 256;     // one block a CU
 constexpr int64_t kDirectItems = 512;
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -47,7 +48,8 @@ AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_token
   p.stream.tile = most <= 16 ? 16 : 32;
   const auto items = [&](int tile) { return heads * (n_rows * share / tile + some); };  // at most
   const int64_t units = items(p.stream.tile) * chunks;
-  p.stream.blocks = (int)(units < kStreamBlocks ? units : kStreamBlocks);
+  const int fill = stream_blocks(dim, p.stream.tile);
+  p.stream.blocks = (int)(units < fill ? units : fill);
   p.stream.join = chunks > 1;
   part_room(p.stream, dim, p.bytes);
   if (both) {

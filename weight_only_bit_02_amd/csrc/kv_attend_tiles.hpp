@@ -2,13 +2,17 @@
 // (prompts and pieces of them).
 //
 // A block takes 32 rows a wave of one head of keys, so that the codes are widened once for all
-// of them: keys as fp16 [token][channel], values transposed, [channel][token], in LDS, while the
-// matrix cores work on the tokens before (two buffers, codes two steps ahead in registers, one
-// barrier a step). v_mfma_f32_32x32x16_f16: S^T = K Q^T leaves lane (h, c) = (lane / 32, lane % 32)
-// row c's scores of tokens 8 i + 4 h + 0..3, which are the second operand of O^T = V^T P^T for
-// values whose tokens lie in that order: LDS holds them so. Probabilities go to the second
-// product rounded to fp16 (an error of the output's own size; hi + lo would be half as much matrix
-// work again).
+// of them: keys as fp16 [token][channel], values transposed, [channel][token], in LDS.
+// v_mfma_f32_32x32x16_f16: S^T = K Q^T leaves lane (h, c) = (lane / 32, lane % 32) row c's scores of
+// tokens 8 i + 4 h + 0..3, which are the second operand of O^T = V^T P^T for values whose tokens lie
+// in that order: LDS holds them so. Probabilities go to the second product rounded to fp16 (an
+// error of the output's own size; hi + lo would be half as much matrix work again).
+//
+// A step is two halves: scores and softmax, then widening of a later step's codes and the second
+// product. The block's second four waves, which share the SIMDs with the first four, run half a
+// step behind: one wave's products then meet the other's vector work. (All waves in step: the
+// products and the vector work add up.) A step's codes are widened two steps ahead into one of
+// three buffers, by each wave its share, from registers loaded a step before that.
 //
 // 16-byte pieces of an LDS row are exchanged by the row's number, so that the 16 rows that a
 // read touches at a time lie in different banks.
@@ -47,14 +51,37 @@ struct TileCodes {
   int page;
 };
 
+// N products with an operand from LDS each, four at a time with the next four's reads under way
+// (left to itself the compiler reads and waits just before each product). read(i) gives operand
+// i, multiply(i, operand) takes it.
+template <int N, class Read, class Multiply>
+__device__ __forceinline__ void products(const Read& read, const Multiply& multiply) {
+  static_assert(N % 4 == 0, "");
+  half8w b[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[0][i] = read(i);
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    __builtin_amdgcn_sched_barrier(0);
+    if (k + 4 < N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[k / 4 + 1 & 1][i] = read(k + 4 + i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) multiply(k + i, b[k / 4 & 1][i]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView v, AttendArgs a, AttendList list) {
   using T = TileShape<D>;
   using Codes = TileCodes<D, G>;
   constexpr int kTokens = T::kTokens, kWords = T::kWords, kSlices = D / 16, kParts = kTokens / 32;
-  __shared__ uint4 keys0[kTokens * D / 8], keys1[kTokens * D / 8];    // [token][D / 8]
-  __shared__ int there0[kTokens / 16], there1[kTokens / 16];          // whether 16 tokens have a page
-  __shared__ uint4 vals0[kTokens * D / 8], vals1[kTokens * D / 8];    // [channel][kTokens / 8]
+  __shared__ uint4 keys[3][kTokens * D / 8];    // [token][D / 8]
+  __shared__ uint4 vals[3][kTokens * D / 8];    // [channel][kTokens / 8]
+  __shared__ int there[3][kTokens / 16];        // whether 16 tokens have a page
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), h = lane >> 5, c = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -141,11 +168,12 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
     for (int n = 0; n < D / 32; ++n) o[n] = f32x16w{};
 
-    const auto page_at = [&](int tb) {  // of the thread's 16 tokens
+    const auto page_at = [&](int tb) AWQ_INLINE {  // of the thread's 16 tokens; looked at when it is used
       const int t = tb + 16 * sub;
-      return t < t1 ? v.page_of(s, t) : -1;
+      return t < t1 ? v.entry(s, t) : -1;
     };
-    const auto load = [&](Codes& d, int page, int tb) {
+    const auto load = [&](Codes& d, int entry, int tb) AWQ_INLINE {
+      const int page = v.page(entry);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) d.k[i] = d.v[i] = 0;
 #pragma unroll
@@ -172,8 +200,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         d.vp[i] = *reinterpret_cast<const uint2*>(vq + ((int64_t)(2 * v_w / Codes::kPerGroup + i) << v.page_shift));
       }
     };
-    const auto widen = [&](const Codes& d, int tb, uint4* keys, uint4* vals, int* there) {
-      if (in == 0) there[sub] = d.page >= 0;
+    const auto widen = [&](const Codes& d, int tb, int buf) AWQ_INLINE {
+      if (in == 0) there[buf][sub] = d.page >= 0;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const uint32_t kp = d.kp[i / Codes::kPerGroup];
@@ -181,7 +209,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         half2w e[4];
         widen4(d.k[i], y.zz, y.zz64, y.s2, magic, e);
         const half8w b{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
-        keys[swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
+        keys[buf][swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
       }
       // what lies behind the sequence's last token may be anything, an infinite scale too
       const int behind = tb + 16 * sub + 4 * v_h - last;  // token i of the four: behind + i > 0
@@ -201,26 +229,30 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
           for (int j = 2 * g; j < 2 * g + 2; ++j) {
             const int ch = v_c + 16 * (4 * (v_w + i) + j);
-            uint2* slot = reinterpret_cast<uint2*>(vals + swizzled<kTokens / 8>(ch, 2 * sub + (v_h & 1)));
+            uint2* slot = reinterpret_cast<uint2*>(vals[buf] + swizzled<kTokens / 8>(ch, 2 * sub + (v_h & 1)));
             slot[v_h >> 1] = make_uint2(__builtin_bit_cast(uint32_t, e[j]), __builtin_bit_cast(uint32_t, f[j]));
           }
         }
       }
     };
-    const auto multiply = [&](int tb, const uint4* keys, const uint4* vals, const int* there) {
-      if (!rows || tb > any_hi || tb + kTokens <= any_lo) return;
+    half8w pr[kParts][2];
+    const auto seen = [&](int tb) { return rows && tb <= any_hi && tb + kTokens > any_lo; };
+    // scores and probabilities of a step
+    const auto score = [&](int tb, int buf) AWQ_INLINE {
+      if (!seen(tb)) return;
       f32x16w sc[kParts];
 #pragma unroll
-      for (int t = 0; t < kParts; ++t) {
-        sc[t] = f32x16w{};
-#pragma unroll
-        for (int i = 0; i < kSlices; ++i) {
-          const half8w b = __builtin_bit_cast(half8w, keys[swizzled<D / 8>(32 * t + c, 2 * i + h)]);
-          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, q[i], sc[t], 0, 0, 0);
-        }
-      }
+      for (int t = 0; t < kParts; ++t) sc[t] = f32x16w{};
+      products<kParts * kSlices>(
+          [&](int i) AWQ_INLINE {
+            const int t = i % kParts, k = i / kParts;
+            return __builtin_bit_cast(half8w, keys[buf][swizzled<D / 8>(32 * t + c, 2 * k + h)]);
+          },
+          [&](int i, half8w b) AWQ_INLINE {
+            sc[i % kParts] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, q[i / kParts], sc[i % kParts], 0, 0, 0);
+          });
       // 16 tokens without a page, by bits
-      const uint64_t gone = __ballot(there[lane % (kTokens / 16)] == 0);
+      const uint64_t gone = __ballot(there[buf][lane % (kTokens / 16)] == 0);
       if (gone || tb + kTokens > all_hi + 1 || tb < all_lo) {
         asm volatile("");  // nothing of this ahead of the branch
 #pragma unroll
@@ -247,7 +279,6 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         for (int n = 0; n < D / 32; ++n) o[n] *= f;
       }
       const float base = m == -__builtin_inff() ? 0.0f : m;
-      half8w pr[kParts][2];
 #pragma unroll
       for (int t = 0; t < kParts; ++t)
 #pragma unroll
@@ -256,40 +287,48 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
           l += e;
           pr[t][i >> 3][i & 7] = (_Float16)e;
         }
-#pragma unroll
-      for (int t = 0; t < kParts; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int n = 0; n < D / 32; ++n) {
-            const half8w b =
-                __builtin_bit_cast(half8w, vals[swizzled<kTokens / 8>(32 * n + c, 2 * (2 * t + k) + h)]);
-            o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, pr[t][k], o[n], 0, 0, 0);
-          }
     };
+    const auto add = [&](int tb, int buf) AWQ_INLINE {
+      if (!seen(tb)) return;
+      products<2 * kParts * (D / 32)>(
+          [&](int i) AWQ_INLINE {
+            const int n = i % (D / 32), k = i / (D / 32);
+            return __builtin_bit_cast(half8w, vals[buf][swizzled<kTokens / 8>(32 * n + c, 2 * k + h)]);
+          },
+          [&](int i, half8w b) AWQ_INLINE {
+            const int n = i % (D / 32), k = i / (D / 32);
+            o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, pr[k >> 1][k & 1], o[n], 0, 0, 0);
+          });
+    };
+    // LDS alone is waited for: loads stay in flight
+    const auto meet = [&]() AWQ_INLINE { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     Codes next;
-    int page = page_at(t0);
-    load(next, page, t0);
-    page = page_at(t0 + kTokens);
-    __syncthreads();  // the item before is done with the buffers
-    widen(next, t0, keys0, vals0, there0);
+    load(next, page_at(t0), t0);
+    int page = page_at(t0 + kTokens);
+    meet();  // the item before is done with the buffers
+    widen(next, t0, 0);
     load(next, page, t0 + kTokens);
     page = page_at(t0 + 2 * kTokens);
-    __syncthreads();
-    for (int tb = t0; tb < t1; tb += 2 * kTokens) {
-      widen(next, tb + kTokens, keys1, vals1, there1);
-      load(next, page, tb + 2 * kTokens);
-      page = page_at(tb + 3 * kTokens);
-      multiply(tb, keys0, vals0, there0);
-      __syncthreads();
-      if (tb + kTokens >= t1) break;
-      widen(next, tb + 2 * kTokens, keys0, vals0, there0);
+    widen(next, t0 + kTokens, 1);
+    load(next, page, t0 + 2 * kTokens);
+    page = page_at(t0 + 3 * kTokens);
+    meet();
+    const bool behind = wave >= T::kWaves / 2;
+    if (behind) meet();
+    int buf = 0;
+    for (int tb = t0; tb < t1; tb += kTokens) {
+      score(tb, buf);
+      meet();
+      const int after = buf == 0 ? 2 : buf - 1;  // (buf + 2) % 3
+      widen(next, tb + 2 * kTokens, after);
       load(next, page, tb + 3 * kTokens);
       page = page_at(tb + 4 * kTokens);
-      multiply(tb + kTokens, keys1, vals1, there1);
-      __syncthreads();
+      add(tb, buf);
+      meet();
+      buf = buf == 2 ? 0 : buf + 1;
     }
+    if (!behind) meet();
 
     const bool alone = u0 == 0 && u1 == x.chunks;
     if (u1 < x.chunks) {

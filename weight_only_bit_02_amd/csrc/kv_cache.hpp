@@ -37,13 +37,13 @@ struct KvView {
   __device__ __forceinline__ int64_t code_bytes() const { return ((int64_t)dim / 2) << page_shift; }
   __device__ __forceinline__ int64_t param_words() const { return ((int64_t)(dim / group)) << page_shift; }
 
-  // The page with token `pos` of sequence s, -1 if there is none.
-  __device__ __forceinline__ int page_of(int s, int64_t pos) const {
+  // The page table's entry for token `pos` of sequence s (-1 beyond it); the page, -1 if there is none.
+  __device__ __forceinline__ int entry(int s, int64_t pos) const {
     const int64_t at = pos >> page_shift;
-    if (pos < 0 || at >= max_pages) return -1;
-    const int p = table[(int64_t)s * max_pages + at];
-    return p >= 0 && p < pages ? p : -1;
+    return pos < 0 || at >= max_pages ? -1 : table[(int64_t)s * max_pages + at];
   }
+  __device__ __forceinline__ int page(int entry) const { return entry >= 0 && entry < pages ? entry : -1; }
+  __device__ __forceinline__ int page_of(int s, int64_t pos) const { return page(entry(s, pos)); }
 };
 
 // One sequence of the batch: its first row, its rows and its tokens in the cache.
