@@ -8,11 +8,12 @@
 // in that order: LDS holds them so. Probabilities go to the second product rounded to fp16 (an
 // error of the output's own size; hi + lo would be half as much matrix work again).
 //
-// A step is two halves: scores and softmax, then widening of a later step's codes and the second
-// product. The block's second four waves, which share the SIMDs with the first four, run half a
-// step behind: one wave's products then meet the other's vector work. (All waves in step: the
-// products and the vector work add up.) A step's codes are widened two steps ahead into one of
-// three buffers, by each wave its share, from registers loaded a step before that.
+// A step: scores and softmax, widening of a later step's codes, the second product. The block's
+// second four waves, which share the SIMDs with the first four, run half a step behind, so that one
+// wave's products meet the other's vector work (in step, the two add up); there is one barrier a
+// step, after the first waves' second product and the second waves' softmax. A step's codes are
+// widened by each wave its share, one step ahead into one of three buffers, from registers loaded
+// a step before that.
 //
 // 16-byte pieces of an LDS row are exchanged by the row's number, so that the 16 rows that a
 // read touches at a time lie in different banks.
@@ -46,20 +47,20 @@ struct TileCodes {
   static constexpr int kWords = TileShape<D>::kWords, kPerGroup = D / 32 / G;
   static constexpr int kGroups = kWords > kPerGroup ? kWords / kPerGroup : 1;  // that the thread's words have
   uint32_t k[kWords], v[kWords];
-  uint32_t kp[kGroups];
+  uint32_t kp[kGroups];  // of the token and its neighbour (a 16-bit load would be waited for to be widened)
   uint2 vp[kGroups];
   int page;
 };
 
 // N products with an operand from LDS each, four at a time with the next four's reads under way
 // (left to itself the compiler reads and waits just before each product). read(i) gives operand
-// i, multiply(i, operand) takes it.
+// i, multiply(i, operand) takes it; the first four have been read.
 template <int N, class Read, class Multiply>
-__device__ __forceinline__ void products(const Read& read, const Multiply& multiply) {
+__device__ __forceinline__ void products(half8w (&first)[4], const Read& read, const Multiply& multiply) {
   static_assert(N % 4 == 0, "");
   half8w b[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[0][i] = read(i);
+  for (int i = 0; i < 4; ++i) b[0][i] = first[i];
 #pragma unroll
   for (int k = 0; k < N; k += 4) {
     __builtin_amdgcn_sched_barrier(0);
@@ -117,13 +118,16 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     w = seqs.get(s);
   }
 
-  // the thread's part of a step's codes: 16 tokens' keys, then values
+  // The thread's part of a step's codes: `kWords` words of 16 tokens' keys, and of their values. The
+  // order of the threads lets 16 lanes' 16-byte pieces of keys, and 32 lanes' 8-byte pieces of
+  // values, lie in different banks.
   const int sub = tid / T::kUnitThreads, in = tid % T::kUnitThreads;
-  constexpr int kPerToken = D / 8 / kWords;                       // threads of a token's keys
-  const int k_token = in / kPerToken, k_word = in % kPerToken * kWords;  // words h (D / 32) + s
-  const int k_h = k_word / (D / 32), k_s = k_word % (D / 32);
-  constexpr int kPerCell = D / 32 / kWords;                       // threads of a lane's values (h, c)
-  const int v_h = in / kPerCell / 16, v_c = in / kPerCell % 16, v_w = in % kPerCell * (kWords / 2);
+  const int k_h = in & 3;
+  const int k_token = D == 64 ? (in >> 2 & 1) | (in >> 3 & 1) << 3 | (in >> 4) << 1 : (in >> 2 & 3) << 2 | in >> 5;
+  const int k_s = D == 64 ? 0 : (in >> 4 & 1) * kWords;            // words (k_h, k_s), (k_h, k_s + 1) ...
+  const int v_c = in & 15, v_h = (in >> 4 & 1) << 1 | (in >> 5 & 1);
+  const int v_w = D == 64 ? 0 : (in >> 6) * (kWords / 2);          // cells (v_h, v_c, v_w), ...
+  const uint32_t code_page = v.heads * (uint32_t)v.code_bytes(), par_page = v.heads * (uint32_t)v.param_words();
 
   while (unit < to) {
     const int at = unit - before;
@@ -168,36 +172,37 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
     for (int n = 0; n < D / 32; ++n) o[n] = f32x16w{};
 
-    const auto page_at = [&](int tb) AWQ_INLINE {  // of the thread's 16 tokens; looked at when it is used
-      const int t = tb + 16 * sub;
-      return t < t1 ? v.entry(s, t) : -1;
+    // The page table's entry of the thread's 16 tokens of a step; looked at when it is used.
+    const int32_t* const table = v.table + (int64_t)s * v.max_pages;
+    const auto entry_of = [&](int tb) AWQ_INLINE {
+      const int at = (tb + 16 * sub) >> v.page_shift;
+      return table[at < v.max_pages ? at : v.max_pages - 1];
     };
+    const uint8_t* const kb0 =
+        v.k_codes + x.head * v.code_bytes() + k_token * (D / 2) + 4 * (k_h * (D / 32) + k_s);
+    const uint8_t* const vb0 =
+        v.v_codes + x.head * v.code_bytes() + 4 * ((v_h * 16 + v_c) * (D / 32) + 2 * v_w);
+    const uint16_t* const kq0 =
+        v.k_params + x.head * v.param_words() + (k_token & ~1) + ((k_s / Codes::kPerGroup) << v.page_shift);
+    const uint16_t* const vq0 =
+        v.v_params + x.head * v.param_words() + 4 * v_h + ((2 * v_w / Codes::kPerGroup) << v.page_shift);
     const auto load = [&](Codes& d, int entry, int tb) AWQ_INLINE {
-      const int page = v.page(entry);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) d.k[i] = d.v[i] = 0;
-#pragma unroll
-      for (int i = 0; i < Codes::kGroups; ++i) d.kp[i] = 0, d.vp[i] = make_uint2(0, 0);
-      d.page = page;
-      if (page < 0) return;
-      const int place = (tb + 16 * sub) & ((1 << v.page_shift) - 1);
-      const int64_t part = (int64_t)page * v.heads + x.head;
-      const uint8_t* kb = v.k_codes + part * v.code_bytes() + (int64_t)(place + k_token) * (D / 2) + 4 * k_word;
-      const uint8_t* vb = v.v_codes + part * v.code_bytes() + (int64_t)place * (D / 2) + 4 * kWords * in;
+      d.page = tb + 16 * sub < t1 ? v.page(entry) : -1;
+      const uint32_t page = d.page < 0 ? 0 : d.page;  // (page 0 for none: not looked at)
+      const uint32_t place = (uint32_t)(tb + 16 * sub) & ((1u << v.page_shift) - 1);
+      const uint64_t code = (uint64_t)page * code_page + place * (D / 2), par = (uint64_t)page * par_page + place;
       if constexpr (kWords == 2) {
-        const uint2 y = *reinterpret_cast<const uint2*>(kb), z = *reinterpret_cast<const uint2*>(vb);
+        const uint2 y = *reinterpret_cast<const uint2*>(kb0 + code), z = *reinterpret_cast<const uint2*>(vb0 + code);
         d.k[0] = y.x, d.k[1] = y.y, d.v[0] = z.x, d.v[1] = z.y;
       } else {
-        const uint4 y = *reinterpret_cast<const uint4*>(kb), z = *reinterpret_cast<const uint4*>(vb);
+        const uint4 y = *reinterpret_cast<const uint4*>(kb0 + code), z = *reinterpret_cast<const uint4*>(vb0 + code);
         d.k[0] = y.x, d.k[1] = y.y, d.k[2] = y.z, d.k[3] = y.w;
         d.v[0] = z.x, d.v[1] = z.y, d.v[2] = z.z, d.v[3] = z.w;
       }
-      const uint16_t* kq = v.k_params + part * v.param_words() + place + k_token;
-      const uint16_t* vq = v.v_params + part * v.param_words() + place + 4 * v_h;
 #pragma unroll
       for (int i = 0; i < Codes::kGroups; ++i) {
-        d.kp[i] = kq[(int64_t)(k_s / Codes::kPerGroup + i) << v.page_shift];
-        d.vp[i] = *reinterpret_cast<const uint2*>(vq + ((int64_t)(2 * v_w / Codes::kPerGroup + i) << v.page_shift));
+        d.kp[i] = *reinterpret_cast<const uint32_t*>(kq0 + par + (i << v.page_shift));
+        d.vp[i] = *reinterpret_cast<const uint2*>(vq0 + par + (i << v.page_shift));
       }
     };
     const auto widen = [&](const Codes& d, int tb, int buf) AWQ_INLINE {
@@ -205,24 +210,31 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const uint32_t kp = d.kp[i / Codes::kPerGroup];
-        const Params2 y = params2(kp | kp << 16);
+        const Params2 y = params2(__builtin_amdgcn_perm(kp, kp, k_token & 1 ? 0x03020302u : 0x01000100u));
         half2w e[4];
         widen4(d.k[i], y.zz, y.zz64, y.s2, magic, e);
         const half8w b{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
         keys[buf][swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
       }
-      // what lies behind the sequence's last token may be anything, an infinite scale too
-      const int behind = tb + 16 * sub + 4 * v_h - last;  // token i of the four: behind + i > 0
+      // what no token wrote may be anything, an infinite scale too
+      uint2 vp[Codes::kGroups];
+#pragma unroll
+      for (int i = 0; i < Codes::kGroups; ++i) vp[i] = d.vp[i];
+      if (tb + kTokens > t1 || __ballot(d.page < 0)) {
+        asm volatile("");  // nothing of this ahead of the branch
+        const int behind = d.page < 0 ? 4 : tb + 16 * sub + 4 * v_h - last;  // token i of the four: behind + i > 0
+#pragma unroll
+        for (int i = 0; i < Codes::kGroups; ++i) {
+          vp[i].x &= (behind > 0 ? 0 : 0xFFFFu) | (behind + 1 > 0 ? 0 : 0xFFFF0000u);
+          vp[i].y &= (behind + 2 > 0 ? 0 : 0xFFFFu) | (behind + 3 > 0 ? 0 : 0xFFFF0000u);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kWords / 2; ++i) {  // channels v_c + 16 (4 (v_w + i) + j)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {         // j = 2 g, 2 g + 1: one group
-          uint2 vp = d.vp[(2 * i + g) / Codes::kPerGroup];
-          if (behind > -4) {
-            vp.x &= (behind > 0 ? 0 : 0xFFFFu) | (behind + 1 > 0 ? 0 : 0xFFFF0000u);
-            vp.y &= (behind + 2 > 0 ? 0 : 0xFFFFu) | (behind + 3 > 0 ? 0 : 0xFFFF0000u);
-          }
-          const Params2 y = params2(vp.x), z = params2(vp.y);
+          const uint2 p = vp[(2 * i + g) / Codes::kPerGroup];
+          const Params2 y = params2(p.x), z = params2(p.y);
           half2w e[4], f[4];
           widen4(d.v[2 * i], y.zz, y.zz64, y.s2, magic, e);
           widen4(d.v[2 * i + 1], z.zz, z.zz64, z.s2, magic, f);
@@ -235,7 +247,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         }
       }
     };
-    half8w pr[kParts][2];
+    half8w pr[kParts][2], first[4];
+    const auto read_key = [&](int buf, int i) AWQ_INLINE {  // operand i of the scores
+      return __builtin_bit_cast(half8w, keys[buf][swizzled<D / 8>(32 * (i % kParts) + c, 2 * (i / kParts) + h)]);
+    };
+    const auto read_value = [&](int buf, int i) AWQ_INLINE {  // of the second product
+      constexpr int kN = D / 32;
+      return __builtin_bit_cast(half8w, vals[buf][swizzled<kTokens / 8>(32 * (i % kN) + c, 2 * (i / kN) + h)]);
+    };
     const auto seen = [&](int tb) { return rows && tb <= any_hi && tb + kTokens > any_lo; };
     // scores and probabilities of a step
     const auto score = [&](int tb, int buf) AWQ_INLINE {
@@ -244,10 +263,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
       for (int t = 0; t < kParts; ++t) sc[t] = f32x16w{};
       products<kParts * kSlices>(
-          [&](int i) AWQ_INLINE {
-            const int t = i % kParts, k = i / kParts;
-            return __builtin_bit_cast(half8w, keys[buf][swizzled<D / 8>(32 * t + c, 2 * k + h)]);
-          },
+          first, [&](int i) AWQ_INLINE { return read_key(buf, i); },
           [&](int i, half8w b) AWQ_INLINE {
             sc[i % kParts] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, q[i / kParts], sc[i % kParts], 0, 0, 0);
           });
@@ -291,10 +307,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     const auto add = [&](int tb, int buf) AWQ_INLINE {
       if (!seen(tb)) return;
       products<2 * kParts * (D / 32)>(
-          [&](int i) AWQ_INLINE {
-            const int n = i % (D / 32), k = i / (D / 32);
-            return __builtin_bit_cast(half8w, vals[buf][swizzled<kTokens / 8>(32 * n + c, 2 * k + h)]);
-          },
+          first, [&](int i) AWQ_INLINE { return read_value(buf, i); },
           [&](int i, half8w b) AWQ_INLINE {
             const int n = i % (D / 32), k = i / (D / 32);
             o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, pr[k >> 1][k & 1], o[n], 0, 0, 0);
@@ -303,32 +316,36 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     // LDS alone is waited for: loads stay in flight
     const auto meet = [&]() AWQ_INLINE { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-    Codes next;
-    load(next, page_at(t0), t0);
-    int page = page_at(t0 + kTokens);
-    meet();  // the item before is done with the buffers
-    widen(next, t0, 0);
-    load(next, page, t0 + kTokens);
-    page = page_at(t0 + 2 * kTokens);
-    widen(next, t0 + kTokens, 1);
-    load(next, page, t0 + 2 * kTokens);
-    page = page_at(t0 + 3 * kTokens);
-    meet();
     const bool behind = wave >= T::kWaves / 2;
-    if (behind) meet();
+    const auto advance = [&](Codes& d, int& entry, int tb, int buf) AWQ_INLINE {  // widens step tb, loads the next
+      widen(d, tb, buf);
+      load(d, entry, tb + kTokens);
+      entry = entry_of(tb + 2 * kTokens);
+    };
+    Codes next;
+    load(next, entry_of(t0), t0);
+    int entry = entry_of(t0 + kTokens);
+    meet();  // the item before is done with the buffers
+    advance(next, entry, t0, 0);
+    meet();
+    if (behind) advance(next, entry, t0 + kTokens, 1);
     int buf = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) first[i] = read_key(0, i);
     for (int tb = t0; tb < t1; tb += kTokens) {
+      const int after = buf == 2 ? 0 : buf + 1;
       score(tb, buf);
-      meet();
-      const int after = buf == 0 ? 2 : buf - 1;  // (buf + 2) % 3
-      widen(next, tb + 2 * kTokens, after);
-      load(next, page, tb + 3 * kTokens);
-      page = page_at(tb + 4 * kTokens);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) first[i] = read_value(buf, i);
+      if (behind) meet();
+      // (buf + 1 + behind) % 3
+      advance(next, entry, tb + (behind ? 2 : 1) * kTokens, behind ? (after == 2 ? 0 : after + 1) : after);
       add(tb, buf);
-      meet();
-      buf = buf == 2 ? 0 : buf + 1;
+      if (!behind) meet();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) first[i] = read_key(after, i);
+      buf = after;
     }
-    if (!behind) meet();
 
     const bool alone = u0 == 0 && u1 == x.chunks;
     if (u1 < x.chunks) {
