@@ -259,25 +259,45 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     // scores and probabilities of a step
     const auto score = [&](int tb, int buf) AWQ_INLINE {
       if (!seen(tb)) return;
+      const int paged = there[buf][lane % (kTokens / 16)];
       f32x16w sc[kParts];
 #pragma unroll
       for (int t = 0; t < kParts; ++t) sc[t] = f32x16w{};
+      __builtin_amdgcn_s_setprio(1);  // products first: 2% over equal waves
       products<kParts * kSlices>(
           first, [&](int i) AWQ_INLINE { return read_key(buf, i); },
           [&](int i, half8w b) AWQ_INLINE {
             sc[i % kParts] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, q[i / kParts], sc[i % kParts], 0, 0, 0);
           });
-      // 16 tokens without a page, by bits
-      const uint64_t gone = __ballot(there[buf][lane % (kTokens / 16)] == 0);
-      if (gone || tb + kTokens > all_hi + 1 || tb < all_lo) {
-        asm volatile("");  // nothing of this ahead of the branch
+      __builtin_amdgcn_s_setprio(0);
+      // (empty asm: nothing of a branch ahead of it)
+      const float none = -__builtin_inff();
+      if (tb + kTokens > all_hi + 1) {
+        asm volatile("");
+        const int most = hi - tb - 4 * h;
 #pragma unroll
         for (int t = 0; t < kParts; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int tok = tb + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
-            if (!(tok >= lo && tok <= hi) || (gone >> (2 * t + (i >> 3)) & 1)) sc[t][i] = -__builtin_inff();
-          }
+          for (int i = 0; i < 16; ++i)
+            if (32 * t + 8 * (i >> 2) + (i & 3) > most) sc[t][i] = none;
+      }
+      if (tb < all_lo) {
+        asm volatile("");
+        const int least = lo - tb - 4 * h;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (32 * t + 8 * (i >> 2) + (i & 3) < least) sc[t][i] = none;
+      }
+      const uint64_t gone = __ballot(paged == 0);  // 16 tokens without a page, by bits
+      if (gone) {
+        asm volatile("");
+#pragma unroll
+        for (int t = 0; t < kParts; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (gone >> (2 * t + (i >> 3)) & 1) sc[t][i] = none;
       }
       float top = sc[0][0];
 #pragma unroll
@@ -306,12 +326,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     };
     const auto add = [&](int tb, int buf) AWQ_INLINE {
       if (!seen(tb)) return;
+      __builtin_amdgcn_s_setprio(1);
       products<2 * kParts * (D / 32)>(
           first, [&](int i) AWQ_INLINE { return read_value(buf, i); },
           [&](int i, half8w b) AWQ_INLINE {
             const int n = i % (D / 32), k = i / (D / 32);
             o[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, pr[k >> 1][k & 1], o[n], 0, 0, 0);
           });
+      __builtin_amdgcn_s_setprio(0);
     };
     // LDS alone is waited for: loads stay in flight
     const auto meet = [&]() AWQ_INLINE { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
