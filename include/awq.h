@@ -553,7 +553,7 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, voi
  *   window > 0: t > p - window. A row without a token: zeros (lse -inf).
  *   q        fp16 [n_rows][q_ld], out fp16 [n_rows][out_ld]: q_heads x head_dim values a row,
  *            strides multiples of 8; q_heads a multiple of kv_heads
- *   scale    above 0 (1 / sqrt(head_dim) as a rule)
+ *   scale    above 0, below 1e20 (1 / sqrt(head_dim) as a rule)
  *   lse      fp32 [n_rows][q_heads] or NULL: log of the sum of exp(scale q . k_t)
  *   workspace device scratch of awq_attention_kv4_workspace_size bytes (max_tokens = max_pages
  *            page_size), 16-byte aligned; 0 where nothing is split. One for each of the

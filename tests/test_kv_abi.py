@@ -106,7 +106,7 @@ def test_attend(lib):
         return lib.awq_attention_kv4(q, q_ld, qh, c, b, scale, causal, window, out, out_ld, lse, ws, wsb, None)
     assert call(q=None) == NULL and call(out=None) == NULL
     assert call(causal=2) == UNSUPPORTED
-    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e31):
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e20):
         assert call(scale=scale) == UNSUPPORTED
     assert call(window=-1) == SHAPE
     for qh in (0, -2, 1, 3, 1026):

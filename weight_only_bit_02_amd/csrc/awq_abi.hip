@@ -757,7 +757,8 @@ static bool attend_sizes_ok(int64_t n_rows, int32_t seqs, int32_t max_rows, int6
 size_t awq_attention_kv4_workspace_size(int64_t n_rows, int32_t seqs, int32_t max_rows, int64_t max_tokens,
                                         int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   if (!attend_sizes_ok(n_rows, seqs, max_rows, max_tokens, q_heads, kv_heads, head_dim)) return 0;
-  return awq::attend_plan(n_rows, seqs, max_rows, max_tokens, q_heads / kv_heads, kv_heads, head_dim).bytes;
+  return awq::attend_plan(n_rows, seqs, max_rows, max_tokens, q_heads / kv_heads, kv_heads, head_dim, 32)
+      .bytes;
 }
 
 awq_status awq_attention_kv4(const void* q, int64_t q_ld, int32_t q_heads, const awq_kv_cache* cache,
@@ -767,13 +768,13 @@ awq_status awq_attention_kv4(const void* q, int64_t q_ld, int32_t q_heads, const
   if (!q || !out) return AWQ_ERR_NULL_POINTER;
   const awq_status s = kv_view(cache, batch, c);
   if (s != AWQ_OK) return s;
-  if ((causal != 0 && causal != 1) || !(scale > 0.0f && scale < 1e30f)) return AWQ_ERR_UNSUPPORTED;
+  if ((causal != 0 && causal != 1) || !(scale > 0.0f && scale < 1e20f)) return AWQ_ERR_UNSUPPORTED;
   const int64_t max_tokens = (int64_t)batch->max_pages * cache->page_size;
   if (!attend_sizes_ok(batch->n_rows, batch->seqs, batch->max_rows, max_tokens, q_heads, c.heads, c.dim) ||
       !good_ld(q_ld, q_heads, c.dim) || !good_ld(out_ld, q_heads, c.dim) || window < 0)
     return AWQ_ERR_BAD_SHAPE;
   const awq::AttendPlan p = awq::attend_plan(batch->n_rows, batch->seqs, batch->max_rows, max_tokens,
-                                             q_heads / c.heads, c.heads, c.dim);
+                                             q_heads / c.heads, c.heads, c.dim, c.group);
   if (!good_workspace(workspace, workspace_bytes, p.bytes)) return AWQ_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(out) || (lse && !aligned4(lse))) return AWQ_ERR_MISALIGNED;
   awq::AttendArgs a{};

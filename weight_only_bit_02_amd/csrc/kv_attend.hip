@@ -15,50 +15,50 @@ AWQ_DECLARE(256)
 namespace {
 
 constexpr int kFew = 64;
-// Blocks of the streaming kernel that the chip holds at once, by registers and LDS.
-int stream_blocks(int dim, int tile) {
-  const int each = dim == 256 ? (tile == 16 ? 2 : 1) : tile == 16 ? 4 : dim == 64 ? 3 : 2;
-  return 256 * each;
-}
-constexpr int kTileBlocks = 256;     // one block a CU
+constexpr int kCus = 256;
 constexpr int64_t kDirectItems = 512;
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Room for the sums of items that are split.
-void part_room(AttendPart& p, int dim, size_t& bytes) {
+// Room for the sums of items that are split, `blocks` or fewer of them.
+void part_room(AttendPart& p, int blocks, int dim, size_t& bytes) {
   if (!p.join) return;
-  const size_t rows = (size_t)2 * p.blocks * p.tile;
+  const size_t rows = (size_t)2 * blocks * p.tile;
   p.part = bytes;
   bytes += align256(rows * dim * sizeof(float));
   p.part_ml = bytes;
   bytes += align256(rows * sizeof(float2));
   p.split = bytes;
-  bytes += align256(p.blocks * sizeof(AttendSplit));
+  bytes += align256(blocks * sizeof(AttendSplit));
 }
 
 }  // namespace
 
-AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim) {
+AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim,
+                       int group) {
   AttendPlan p{};
   const int64_t chunks = (max_tokens + kAttendChunk - 1) / kAttendChunk;
-  const int64_t some = seqs < n_rows ? seqs : n_rows;  // sequences with rows, at most
-  const int64_t most = (int64_t)max_rows * share;
-  const bool both = most > kFew;
+  const int64_t flat = n_rows * share;
+  const bool both = (int64_t)max_rows * share > kFew;
   p.few = both ? kFew : 0x7FFFFFFF;
-  p.stream.tile = most <= 16 ? 16 : 32;
-  const auto items = [&](int tile) { return heads * (n_rows * share / tile + some); };  // at most
-  const int64_t units = items(p.stream.tile) * chunks;
-  const int fill = stream_blocks(dim, p.stream.tile);
-  p.stream.blocks = (int)(units < fill ? units : fill);
+  // items at most: whole tiles, and the last one of each sequence with rows
+  p.stream.tile = (int64_t)max_rows * share <= 16 ? 16 : 32;
+  const int64_t some = seqs < n_rows ? seqs : n_rows;
+  const int64_t units = heads * (flat / p.stream.tile + some) * chunks;
+  const auto blocks = [&](int g) {  // one wave's place on every SIMD takes a block per CU
+    const int fill = kCus * stream_waves(dim, g, p.stream.tile);
+    return (int)(units < fill ? units : fill);
+  };
+  p.stream.blocks = blocks(group);
   p.stream.join = chunks > 1;
-  part_room(p.stream, dim, p.bytes);
+  part_room(p.stream, blocks(32), dim, p.bytes);  // the most of any group: the workspace does not go by it
   if (both) {
     p.tiles.tile = dim == 256 ? TileShape<256>::kRows : TileShape<128>::kRows;
-    const int64_t n = items(p.tiles.tile);
+    const int64_t long_ones = flat / (kFew + 1) < some ? flat / (kFew + 1) : some;
+    const int64_t n = heads * (flat / p.tiles.tile + long_ones);
     p.tiles.direct = n >= kDirectItems || chunks == 1;
     p.tiles.join = !p.tiles.direct;
-    p.tiles.blocks = p.tiles.direct ? (int)n : kTileBlocks;
-    part_room(p.tiles, dim, p.bytes);
+    p.tiles.blocks = p.tiles.direct ? (int)n : kCus;
+    part_room(p.tiles, kCus, dim, p.bytes);
   }
   return p;
 }

@@ -23,15 +23,6 @@ namespace awq {
 #define AWQ_INLINE __attribute__((always_inline))
 constexpr int kAttendWaves = 4;
 constexpr int kAttendChunk = 256;  // tokens of the work list's unit, a multiple of every kernel's step
-#ifndef KUNITS
-#define KUNITS 2
-#endif
-#ifndef KST
-#define KST 2
-#endif
-#ifndef KWPE
-#define KWPE 4
-#endif
 constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score passes it by 2^8
 
 constexpr int kJoinThreads = 256;
@@ -202,6 +193,12 @@ __device__ __forceinline__ void widen4(uint32_t w, half2w zz, half2w zz64, half2
   d[3] = (__builtin_bit_cast(half2w, u3) + zz64) * s2;
 }
 
+// The bare codes of the four nibbles of each half of w, as fp16 subnormals: code 2^-24.
+__device__ __forceinline__ void raw4(uint32_t w, half2w (&d)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __builtin_bit_cast(half2w, (w >> (4 * i)) & 0x000F000Fu);
+}
+
 struct Params2 {  // of two tokens, or of one twice
   half2w zz, zz64, s2;
 };
@@ -211,11 +208,18 @@ __device__ __forceinline__ Params2 params2(uint32_t p) {
                  __builtin_bit_cast(half2w, p & 0xFFF0FFF0u)};
 }
 
+// Waves of the streaming kernel per SIMD, so blocks per CU: what registers and LDS allow, and where
+// that is more than pays. 24 sequences of 300-4000 tokens, 32 heads, groups of 128: four a SIMD 64.7
+// us, three 60.2, two 74.5; 64 sequences, shared heads, groups of 32: four 95, three 101.
+constexpr int stream_waves(int dim, int group, int tile) {
+  return tile == 32 ? (dim == 256 ? 1 : 2) : dim == 256 ? 2 : dim / group <= 2 ? 3 : 4;
+}
+
 // A wave's buffers of the streaming kernel: one step's codes and parameters each.
 template <int D, int G>
 struct StreamShape {
-  static constexpr int kUnits = KUNITS;   // of 16 tokens, of a step
-  static constexpr int kStages = KST;
+  static constexpr int kUnits = 2;   // of 16 tokens, of a step (4: two buffers take half the chip's waves)
+  static constexpr int kStages = 2;
   static constexpr int kCodes = 8 * D;    // bytes of a unit's keys, or values
   static constexpr int kParams = 32 * G;  // of their parameters, [group][token]
   static constexpr int kStage = 2 * kUnits * (kCodes + kParams);
@@ -251,7 +255,7 @@ struct StreamShape {
 
 // D channels, G groups of them, R tiles of 16 rows.
 template <int D, int G, int R>
-__global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_waves_per_eu(R == 2 ? (D == 256 ? 1 : 2) : D == 256 ? 2 : KWPE))) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
+__global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_waves_per_eu(stream_waves(D, D / G, 16 * R)))) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
   constexpr int kSlices = D / 32, kTiles = D / 16, kPerGroup = kSlices / G;  // slices of a group
   using S = StreamShape<D, G>;
   constexpr int kUnits = S::kUnits, kStep = 16 * kUnits, kStages = S::kStages;
@@ -260,12 +264,18 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
   constexpr int kRing = kAttendWaves * kStages * S::kStage;
   __shared__ __attribute__((aligned(16))) char smem[kRing > (int)sizeof(Sums) ? kRing : (int)sizeof(Sums)];
   Sums& sums = *reinterpret_cast<Sums*>(smem);  // after an item's last step
+  // Up to two groups a head, scale and zero are applied outside the products: operands are the bare
+  // codes (fp16 subnormals, code 2^-24), and a token's scale and zero multiply its scores and
+  // probabilities in fp32: 208 vector instructions a step instead of 317 at one group.
+  constexpr bool kFold = G <= 2;
+  __shared__ __attribute__((aligned(16))) float folds[kFold ? kAttendWaves : 1][128 * G];
   __shared__ float2 ml[kAttendWaves][16];
 
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t ring = lds_address(reinterpret_cast<uint4*>(smem + wave * kStages * S::kStage));
   const Magic magic = magics();
+  float* const mine = folds[kFold ? wave : 0];
   AttendSeqs seqs(v, a, list, lane);
   const int total = seqs.units();
   const int blocks = (int)gridDim.x < total ? (int)gridDim.x : total;
@@ -322,10 +332,25 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
 
     f32x4w o[R][kTiles];
     float m[R], l[R];
+    // folded: sums of a row's queries by group, and of probabilities times zeros; the values' ref
+    float q_sum[R][G], z_sum[R][G], ref = 0.0f, norm = 0.0f;  // norm = 2^7 / ref
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = -__builtin_inff();
       l[r] = 0.0f;
+      if constexpr (kFold) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float x = 0.0f;
+#pragma unroll
+          for (int t = g * kPerGroup; t < (g + 1) * kPerGroup; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += (float)q[r][t][i];
+          x += __shfl_xor(x, 16);
+          q_sum[r][g] = x + __shfl_xor(x, 32);
+          z_sum[r][g] = 0.0f;
+        }
+      }
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) o[r][n] = f32x4w{0, 0, 0, 0};
     }
@@ -379,11 +404,52 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         }
       }
     };
+    // Folded: a lane turns one token's (and group's) parameters into what its scores and probabilities
+    // take, for all lanes that have that token: of keys scale 2^24 c and -zero scale c (c = scale of the
+    // scores, in log2), of values scale 2^7 / ref and zero, ref a power of two that no scale passes.
+    const auto fold = [&](const char* from, int tb, uint32_t none, bool part) AWQ_INLINE {
+      const int u = lane >> 4 & 1, at = 16 * (G == 2 ? lane >> 5 : 0) + (lane & 15);
+      uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
+      uint32_t vp = reinterpret_cast<const uint16_t*>(from + S::v_params(0) + u * S::kParams)[at];
+      if (part) {  // what no token wrote may be anything, an infinite scale too
+        asm volatile("");
+        if (tb + (lane & 31) > last || (none >> (kUnits - 1 - u) & 1)) kp = vp = 0;
+      }
+      const float ks = h2f(kp & 0xFFF0), vs = h2f(vp & 0xFFF0);
+      if (__ballot(vs > ref)) {
+        asm volatile("");
+        float most = vs;
+#pragma unroll
+        for (int i = 1; i < kWave; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
+        const float next = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, most) + 0x7FFFFFu) & 0xFF800000u);
+        const float f = ref / next;  // (exact)
+        ref = next;
+        norm = 128.0f / next;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) z_sum[r][g] *= f;
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
+        }
+      }
+      const float a1 = ks * a.scale_log2;
+      float* const to = mine + lane;  // (G = 1: lanes from 32 on repeat the others' values)
+      to[G == 1 ? -(lane & 32) : 0] = a1 * 0x1p24f;
+      to[32 * G + (G == 1 ? -(lane & 32) : 0)] = -(float)(kp & 15) * a1;
+      to[64 * G + (G == 1 ? -(lane & 32) : 0)] = vs * norm;
+      to[96 * G + (G == 1 ? -(lane & 32) : 0)] = (float)(vp & 15);
+    };
+    const auto folded = [&](int what, int g, int u) AWQ_INLINE {
+      return *reinterpret_cast<const f32x4w*>(mine + 32 * G * what + 32 * g + 16 * u + 4 * h);
+    };
     const auto step = [&](int k, int ahead) AWQ_INLINE {
       const int tb = t0 + (wave + k * kAttendWaves) * kStep;
       const char* from = smem + (wave * kStages + k % kStages) * S::kStage;
       const uint32_t none = (uint32_t)(gone >> (kUnits * ahead)) & ((1u << kUnits) - 1);  // unit 0 in the highest bit
-      // scores
+      const bool part = tb + kStep > all_hi + 1 || tb < all_lo || tb + kStep > t1 || none != 0;
+      if constexpr (kFold) fold(from, tb, none, part);
+      // scores (folded ones in units of log2)
       f32x4w sc[R][kUnits];
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
@@ -393,35 +459,55 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         for (int r = 0; r < R; ++r) sc[r][u] = f32x4w{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(u))[16 * g + c];
-          const Params2 p = params2(kp | kp << 16);
+          f32x4w part_sum[R];
+          Params2 p;
+          if constexpr (kFold) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) part_sum[r] = f32x4w{0, 0, 0, 0};
+          } else {
+            const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(u))[16 * g + c];
+            p = params2(kp | kp << 16);
+          }
 #pragma unroll
           for (int t = g * kPerGroup; t < (g + 1) * kPerGroup; ++t) {
             half2w e[4];
-            widen4(kw[t], p.zz, p.zz64, p.s2, magic, e);
+            if constexpr (kFold) raw4(kw[t], e);
+            else widen4(kw[t], p.zz, p.zz64, p.s2, magic, e);
             const half8w key{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
 #pragma unroll
+            for (int r = 0; r < R; ++r) {
+              f32x4w& x = kFold ? part_sum[r] : sc[r][u];
+              x = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[r][t], x, 0, 0, 0);
+            }
+          }
+          if constexpr (kFold) {
+            const f32x4w a1 = folded(0, g, u), a2 = folded(1, g, u);
+#pragma unroll
             for (int r = 0; r < R; ++r)
-              sc[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[r][t], sc[r][u], 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sc[r][u][i] = __builtin_fmaf(part_sum[r][i], a1[i], __builtin_fmaf(q_sum[r][g], a2[i], sc[r][u][i]));
           }
         }
       }
-      const bool part = tb + kStep > all_hi + 1 || tb < all_lo || tb + kStep > t1 || none != 0;
       if (part) {
         asm volatile("");  // nothing of this ahead of the branch
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
+        for (int r = 0; r < R; ++r) {
+          const int most = hi[r] - tb - 4 * h, least = lo[r] - tb - 4 * h;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = tb + 16 * u + 4 * h + i;
+          for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-              if (!(t >= lo[r] && t <= hi[r]) || (none >> (kUnits - 1 - u) & 1)) sc[r][u][i] = -__builtin_inff();
-          }
+            for (int i = 0; i < 4; ++i)
+              if (16 * u + i > most || 16 * u + i < least || (none >> (kUnits - 1 - u) & 1))
+                sc[r][u][i] = -__builtin_inff();
+        }
+        asm volatile("");
       }
       // probabilities, as fp16 hi + lo: rounded to fp16 alone they would add as much to the output's
       // error as its own rounding does
-      half8w ph[R][kUnits / 2], pl[R][kUnits / 2];
+      constexpr int kP = kFold ? G : 1;
+      half8w ph[kP][R][kUnits / 2], pl[kP][R][kUnits / 2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float top = sc[r][0][0];
@@ -429,7 +515,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         for (int u = 0; u < kUnits; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][u][i]);
-        top *= a.scale_log2;
+        if constexpr (!kFold) top *= a.scale_log2;
         if (__ballot(top > m[r] + kLazy)) {
           asm volatile("");
           top = fmaxf(top, __shfl_xor(top, 16));
@@ -437,20 +523,41 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
           const float f = top > m[r] ? __builtin_amdgcn_exp2f(m[r] - top) : 1.0f;
           m[r] = top;
           l[r] *= f;
+          if constexpr (kFold) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) z_sum[r][g] *= f;
+          }
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
         }
         const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
+        for (int u = 0; u < kUnits; ++u) {
+          f32x4w e;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][u][i], a.scale_log2, -base));
-            l[r] += e;
-            const _Float16 hi16 = (_Float16)e;
-            ph[r][u >> 1][4 * (u & 1) + i] = hi16;
-            pl[r][u >> 1][4 * (u & 1) + i] = (_Float16)__builtin_fmaf(-(float)hi16, 1.0f, e);
+            e[i] = __builtin_amdgcn_exp2f(kFold ? sc[r][u][i] - base : __builtin_fmaf(sc[r][u][i], a.scale_log2, -base));
+            l[r] += e[i];
           }
+#pragma unroll
+          for (int g = 0; g < kP; ++g) {
+            f32x4w y = e;
+            if constexpr (kFold) {
+              const f32x4w b1 = folded(2, g, u), z = folded(3, g, u);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                y[i] = e[i] * b1[i];
+                z_sum[r][g] = __builtin_fmaf(y[i], z[i], z_sum[r][g]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const _Float16 hi16 = (_Float16)y[i];
+              ph[g][r][u >> 1][4 * (u & 1) + i] = hi16;
+              pl[g][r][u >> 1][4 * (u & 1) + i] = (_Float16)__builtin_fmaf(-(float)hi16, 1.0f, y[i]);
+            }
+          }
+        }
       }
       // O^T += V^T P^T, 32 tokens at a time
 #pragma unroll
@@ -459,17 +566,19 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         S::value_words(from + S::v_codes(u), lane, vw[0]);
         S::value_words(from + S::v_codes(u + 1), lane, vw[1]);
         uint2 vp[2][G];
+        if constexpr (!kFold) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
-            if (part) {  // what no token wrote may be anything, an infinite scale too
-              const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
-              vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
-              vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
+            for (int g = 0; g < G; ++g) {
+              vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
+              if (part) {  // what no token wrote may be anything, an infinite scale too
+                const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
+                vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
+                vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
+              }
             }
-          }
+        }
 #pragma unroll
         for (int t = 0; t < kSlices / 2; ++t) {  // tiles 4 t .. 4 t + 3, 64 channels
 #pragma unroll
@@ -478,8 +587,13 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
             half2w e[4][4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {  // token pairs
-              const Params2 p = params2(b & 1 ? vp[b >> 1][g].y : vp[b >> 1][g].x);
-              widen4(vw[b >> 1][2 * t + (b & 1)], p.zz, p.zz64, p.s2, magic, e[b]);
+              const uint32_t word = vw[b >> 1][2 * t + (b & 1)];
+              if constexpr (kFold) {
+                raw4(word, e[b]);
+              } else {
+                const Params2 p = params2(b & 1 ? vp[b >> 1][g].y : vp[b >> 1][g].x);
+                widen4(word, p.zz, p.zz64, p.s2, magic, e[b]);
+              }
             }
 #pragma unroll
             for (int j = 2 * half; j < 2 * half + 2; ++j) {
@@ -487,8 +601,9 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
                                e[2][j][0], e[2][j][1], e[3][j][0], e[3][j][1]};
 #pragma unroll
               for (int r = 0; r < R; ++r) {
-                o[r][4 * t + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(val, ph[r][u >> 1], o[r][4 * t + j], 0, 0, 0);
-                o[r][4 * t + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(val, pl[r][u >> 1], o[r][4 * t + j], 0, 0, 0);
+                f32x4w& x = o[r][4 * t + j];
+                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(val, ph[kFold ? g : 0][r][u >> 1], x, 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(val, pl[kFold ? g : 0][r][u >> 1], x, 0, 0, 0);
               }
             }
           }
@@ -509,6 +624,14 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
+      // Waves of one age share a SIMD's issue slots fairly, of several the oldest takes them: four
+      // blocks a CU would end one after the other, the last alone. The turn changes hands.
+      switch ((k / 2 + blockIdx.x / 256) % 4) {
+        case 0: __builtin_amdgcn_s_setprio(0); break;
+        case 1: __builtin_amdgcn_s_setprio(1); break;
+        case 2: __builtin_amdgcn_s_setprio(2); break;
+        default: __builtin_amdgcn_s_setprio(3);
+      }
       step(k, ahead);
     }
 
@@ -523,6 +646,18 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor(l[r], 16);
       l[r] += __shfl_xor(l[r], 32);
+      if constexpr (kFold) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          z_sum[r][g] += __shfl_xor(z_sum[r][g], 16);
+          z_sum[r][g] += __shfl_xor(z_sum[r][g], 32);
+        }
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[r][n][i] = __builtin_fmaf(o[r][n][i], 0x1p24f, -z_sum[r][n / 2 / kPerGroup]) * (ref * 0x1p-7f);
+      }
       __syncthreads();
       if (h == 0) ml[wave][c] = make_float2(m[r], l[r]);
       __syncthreads();
@@ -598,7 +733,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, int 
   float m = -__builtin_inff(), l = 0.0f;
   f32x4w y{0, 0, 0, 0};
   if (row < tile && flat <= d.r1) {
-    constexpr int kDeep = 4;
+    constexpr int kDeep = 8;
     for (int k = group % ways; k < d.blocks; k += kDeep * ways) {
       float2 p[kDeep];
       f32x4w z[kDeep];

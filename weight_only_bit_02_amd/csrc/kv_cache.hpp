@@ -126,7 +126,8 @@ struct AttendPlan {
   int few;       // rows x share up to which a sequence is streamed
   size_t bytes;  // of the workspace
 };
-AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim);
+AttendPlan attend_plan(int64_t n_rows, int seqs, int max_rows, int64_t max_tokens, int share, int heads, int dim,
+                       int group);
 hipError_t launch_attend(const KvView& c, AttendArgs a, const AttendPlan& p, void* workspace, hipStream_t stream);
 
 }  // namespace awq
