@@ -66,20 +66,22 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvView& v, int s) {
   return q;
 }
 
-// The sequence of row t (uniform over the wave): how many rows[s + 1] are at most t, by a search
-// with 64 probes a step; seqs: none.
+// The sequence of row t: how many rows[s + 1] are at most t; seqs: none. W adjacent lanes have one
+// t, and search for it with W probes a step.
+template <int W>
 __device__ __forceinline__ int kv_find(const KvView& v, int t, int lane) {
-  if (t < v.rows[0]) return v.seqs;
+  const int first = v.rows[0];
   int lo = 0, n = v.seqs;
   while (n > 0) {
-    const int step = (n + kWave - 1) / kWave;
-    const int at = (lane + 1) * step;
+    const int step = (n + W - 1) / W;
+    const int at = (lane % W + 1) * step;
     const bool before = at <= n && v.rows[lo + (at <= n ? at : 0)] <= t;
-    const int c = __popcll(__ballot(before));
+    const uint64_t found = __ballot(before) >> (lane / W * W);
+    const int c = __popcll(found & (~0ull >> (64 - W)));
     lo += c * step;
     n = n - c * step < step - 1 ? n - c * step : step - 1;
   }
-  return lo;
+  return t < first ? v.seqs : lo;
 }
 
 // An item (rows of one sequence and head of keys) that several blocks took, one after the other.
