@@ -123,6 +123,12 @@ def test_tiles_holes():
     attend(256, 64, 16, 1, 2, [60], [290], seed=8, holes=[(0, 1), (0, 17)])
 
 
+@pytest.mark.parametrize("n,length", [(3, 700), (1, 1), (0, 0), (150, 200)])
+def test_one_sequence_and_rows_behind_it(n, length):
+    """A single sequence with fewer rows than the tensors: what they have says little."""
+    attend(128, 64, 16, 1, 2, [n], [length], extra_rows=230, seed=10 + n)
+
+
 def test_tiles_rows_before_the_sequence():
     attend(128, 128, 16, 1, 4, [90, 80, 70], [30, 0, 1], seed=9)
 

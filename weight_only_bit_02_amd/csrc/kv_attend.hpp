@@ -288,7 +288,10 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
   const int from = cut.start(blockIdx.x), to = cut.start(blockIdx.x + 1);
   int before, tiles_before;
   int s = seqs.find(from, false, before, tiles_before);
-  if (s >= v.seqs) return;  // (wrong rows)
+  if (s >= v.seqs) {  // (wrong rows)
+    attend_split(a, split);
+    return;
+  }
   AttendSeq w = seqs.get(s);
   int unit = from;
   while (unit < to) {

@@ -114,7 +114,10 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     unit = cut.start(blockIdx.x);
     to = cut.start(blockIdx.x + 1);
     s = seqs.find(unit, false, before, tiles_before);
-    if (s >= v.seqs) return;  // (wrong rows)
+    if (s >= v.seqs) {  // (wrong rows)
+      attend_split(a, split);
+      return;
+    }
     w = seqs.get(s);
   }
 
