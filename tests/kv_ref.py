@@ -91,38 +91,37 @@ class Cache:
 
 
 def tokens(cache, table_row, length):
-    """Keys and values of a sequence [length][heads][D], the ranges 15 scale of their groups, and which
-    tokens have a page."""
-    k, v, k_range, v_range = (np.zeros((length, cache.heads, cache.D)) for _ in "kvKV")
+    """Keys and values of a sequence [length][heads][D], the ranges 15 scale of the values' groups, and
+    which tokens have a page."""
+    k, v, v_range = (np.zeros((length, cache.heads, cache.D)) for _ in "kvr")
     there = np.zeros(length, bool)
     for t in range(length):
         at = t // cache.size
         if at < len(table_row) and 0 <= table_row[at] < cache.pages:
             k[t], v[t] = cache.get("k", table_row[at], t % cache.size), cache.get("v", table_row[at], t % cache.size)
-            for name, out in (("k", k_range), ("v", v_range)):
-                p = getattr(cache, name + "_params")[table_row[at], :, :, t % cache.size]
-                sc = (p & 0xFFF0).astype(np.uint16).view(np.float16).astype(np.float64)
-                out[t] = 15 * sc.repeat(cache.group, 1)
+            p = cache.v_params[table_row[at], :, :, t % cache.size]
+            sc = (p & 0xFFF0).astype(np.uint16).view(np.float16).astype(np.float64)
+            v_range[t] = 15 * sc.repeat(cache.group, 1)
             there[t] = True
-    return k, v, k_range, v_range, there
+    return k, v, v_range, there
 
 
 def attention(q, kv, scale, causal, window, rounded):
     """Rows q [n][q_heads][D] at the end of a sequence (kv: what tokens() gives): (out, lse, bound of
     |out - exact|, of lse).
 
-    The bounds. A kernel may add q (code - zero) scale, or q code scale and q zero scale apart: terms
-    of at most |q| 15 scale, exact as products of short numbers, each multiplied by the scale in fp32.
-    D of them are added with an error of at most D 2^-24 of the sum of their sizes; scale, softmax
-    scale, the maximum and the exponential (two units of 2^-23) are a few roundings of the score more:
-    a probability is off by at most e = (D + 8) 2^-24 softmax_scale sum |q| 15 scale + 2^-21, relatively.
+    The bounds. Terms q (code - zero), or q times the value, are exact as products of short numbers; a
+    kernel may multiply their sums by the scale in fp32. D of them are added with an error of at most
+    D 2^-24 of the sum of their sizes; scales, softmax scale, the maximum and the exponential (two units
+    of 2^-23) are a few roundings of the score more: a probability is off by at most
+    e = (D + 8) 2^-24 softmax_scale sum |q| |k| + 2^-21, relatively.
     Numerator and denominator have that error each, and that of adding n numbers, n 2^-24.
-    In the second product a value's terms are as large as 15 scale. Probabilities (times scale) go to
-    it as fp16 hi + lo: 2^-22 relative, and 2^-25 absolute in units where the largest scale times a
-    probability of one is 2^7 or more. rounded = True: or as fp16 beside exact values, 2^-11 relative,
-    2^-24 absolute of the largest probability. The output is rounded to fp16: 2^-11 relative, 2^-25
-    absolute."""
-    k, v, k_range, v_range, there = kv
+    Probabilities (or probabilities times scale) go to the second product as fp16 hi + lo: 2^-22
+    relative, and 2^-25 absolute in units where the largest scale times a probability of one is 2^6 or
+    more, times code - zero: 2^-31 of 15 scale. rounded = True: or as fp16 beside exact values, 2^-11
+    relative, 2^-24 absolute of the largest probability. The output is rounded to fp16: 2^-11 relative,
+    2^-25 absolute."""
+    k, v, v_range, there = kv
     n, heads, D = q.shape
     share, length = heads // k.shape[1], k.shape[0]
     out, lse = np.zeros((n, heads, D)), np.full((n, heads), -np.inf)
@@ -139,15 +138,15 @@ def attention(q, kv, scale, causal, window, rounded):
             continue
         for h in range(heads):
             kk, vv = k[see, h // share], v[see, h // share]
-            kr, vr = k_range[see, h // share], v_range[see, h // share]
+            vr = v_range[see, h // share]
             s = scale * (kk @ q[i, h])
-            size = (scale * (kr @ np.abs(q[i, h]))).max()
+            size = (scale * (np.abs(kk) @ np.abs(q[i, h]))).max()
             top = s.max()
             w = np.exp(s - top)
             w_sum = w.sum()
             out[i, h], lse[i, h] = w @ vv / w_sum, top + math.log(w_sum)
             e = (D + 8) * 2.0 ** -24 * size + 2.0 ** -21 + see.sum() * 2.0 ** -24
-            off = (2 * e + 2.0 ** -22) * (w @ vr) / w_sum + see.sum() * 2.0 ** -32 * vr.max() / w_sum
+            off = (2 * e + 2.0 ** -22) * (w @ np.abs(vv)) / w_sum + see.sum() * 2.0 ** -31 * vr.max() / w_sum
             if rounded:
                 off = off + 2.0 ** -11 * (w @ np.abs(vv)) / w_sum + 2.0 ** -24 * np.abs(vv).sum(0) / w_sum
             bound[i, h] = off + 2.0 ** -11 * (np.abs(out[i, h]) + off) + 2.0 ** -25

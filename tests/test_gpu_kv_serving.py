@@ -305,12 +305,13 @@ def test_many_sequences_and_heads():
     s = (k * q.double()).sum(2) / math.sqrt(D)
     s = s.masked_fill(torch.arange(3, device=DEV)[None] >= b.lengths[:, None], -math.inf)
     want = (torch.softmax(s, 1)[:, :, None] * v).sum(1)
-    # kv_ref.attention's bound with scales below 1: values, and 15 scale, below 15
-    e = (D + 8) * 2.0 ** -24 * 15 * q.double().abs().sum(2) / math.sqrt(D) + 2.0 ** -21 + 3 * 2.0 ** -24
-    off = (2 * e + 2.0 ** -22) * 15 + 3 * 2.0 ** -32 * 15
+    # kv_ref.attention's bound; scales are below 1
+    size = (k.abs() * q.double().abs()).sum(2).amax(1, keepdim=True) / math.sqrt(D)
+    e = (D + 8) * 2.0 ** -24 * size + 2.0 ** -21 + 3 * 2.0 ** -24
+    off = (2 * e + 2.0 ** -22) * (torch.softmax(s, 1)[:, :, None] * v.abs()).sum(1) + 3 * 2.0 ** -31 * 15
     assert bool(((y[:, 0].double() - want).abs() <= off + 2.0 ** -11 * (want.abs() + off) + 2.0 ** -25).all())
     wl = torch.logsumexp(s, 1, keepdim=True)
-    assert bool(((lse.double() - wl).abs() <= e + 2.0 ** -22 * (2 * wl.abs() + 3)).all())
+    assert bool(((lse.double() - wl).abs() <= e + 2.0 ** -22 * (wl.abs() + s.amax(1, keepdim=True).abs() + 1)).all())
 
     b, pages, table, rows = batch_of(awq, [1, 2], [40, 3], 16, rng)
     c = filled(pages, 1, 16, D, D, table, [40, 3], rng)

@@ -193,10 +193,13 @@ __device__ __forceinline__ void widen4(uint32_t w, half2w zz, half2w zz64, half2
   d[3] = (__builtin_bit_cast(half2w, u3) + zz64) * s2;
 }
 
-// The bare codes of the four nibbles of each half of w, as fp16 subnormals: code 2^-24.
-__device__ __forceinline__ void raw4(uint32_t w, half2w (&d)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = __builtin_bit_cast(half2w, (w >> (4 * i)) & 0x000F000Fu);
+// code - zero of the four nibbles of each half of w.
+__device__ __forceinline__ void centre4(uint32_t w, half2w zz, half2w zz64, Magic m, half2w (&d)[4]) {
+  const uint32_t w8 = w >> 8;
+  d[0] = __builtin_bit_cast(half2w, and_or(w, 0x000F000Fu, m.m64)) + zz;
+  d[1] = __builtin_bit_cast(half2w, and_or(w, 0x00F000F0u, m.m54)) + zz64;
+  d[2] = __builtin_bit_cast(half2w, and_or(w8, 0x000F000Fu, m.m64)) + zz;
+  d[3] = __builtin_bit_cast(half2w, and_or(w8, 0x00F000F0u, m.m54)) + zz64;
 }
 
 struct Params2 {  // of two tokens, or of one twice
@@ -209,8 +212,9 @@ __device__ __forceinline__ Params2 params2(uint32_t p) {
 }
 
 // Waves of the streaming kernel per SIMD, so blocks per CU: what registers and LDS allow, and where
-// that is more than pays. 24 sequences of 300-4000 tokens, 32 heads, groups of 128: four a SIMD 64.7
-// us, three 60.2, two 74.5; 64 sequences, shared heads, groups of 32: four 95, three 101.
+// that is more than pays. One sequence of 131071 tokens, groups of 128: four a SIMD 46 us, three 43; 24
+// sequences of 300-4000 tokens, 32 heads: 62, 63 (two: 74); 64 sequences, shared heads, groups of 32:
+// four 97, three 101.
 constexpr int stream_waves(int dim, int group, int tile) {
   return tile == 32 ? (dim == 256 ? 1 : 2) : dim == 256 ? 2 : dim / group <= 2 ? 3 : 4;
 }
@@ -264,11 +268,13 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
   constexpr int kRing = kAttendWaves * kStages * S::kStage;
   __shared__ __attribute__((aligned(16))) char smem[kRing > (int)sizeof(Sums) ? kRing : (int)sizeof(Sums)];
   Sums& sums = *reinterpret_cast<Sums*>(smem);  // after an item's last step
-  // Up to two groups a head, scale and zero are applied outside the products: operands are the bare
-  // codes (fp16 subnormals, code 2^-24), and a token's scale and zero multiply its scores and
-  // probabilities in fp32: 208 vector instructions a step instead of 317 at one group.
+  // Up to two groups a head, the scale is applied outside the products: operands are code - zero, and a
+  // token's scale multiplies its scores and probabilities in fp32: some 230 vector instructions a step
+  // instead of 317 at one group. (The zero outside as well takes 208, but then sums of codes and of
+  // zeros, up to 15 scales a token, leave a small difference: 131071 tokens with values around zero
+  // came out 1e-3 off, relatively, not 2e-4.)
   constexpr bool kFold = G <= 2;
-  __shared__ __attribute__((aligned(16))) float folds[kFold ? kAttendWaves : 1][128 * G];
+  __shared__ __attribute__((aligned(16))) float folds[kFold ? kAttendWaves : 1][64 * G];
   __shared__ float2 ml[kAttendWaves][16];
 
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 4, c = lane & 15;
@@ -335,25 +341,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
 
     f32x4w o[R][kTiles];
     float m[R], l[R];
-    // folded: sums of a row's queries by group, and of probabilities times zeros; the values' ref
-    float q_sum[R][G], z_sum[R][G], ref = 0.0f, norm = 0.0f;  // norm = 2^7 / ref
+    float ref = 0.0f, norm = 0.0f;  // folded: a power of two that no value's scale passes; 2^7 / ref
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = -__builtin_inff();
       l[r] = 0.0f;
-      if constexpr (kFold) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float x = 0.0f;
-#pragma unroll
-          for (int t = g * kPerGroup; t < (g + 1) * kPerGroup; ++t)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x += (float)q[r][t][i];
-          x += __shfl_xor(x, 16);
-          q_sum[r][g] = x + __shfl_xor(x, 32);
-          z_sum[r][g] = 0.0f;
-        }
-      }
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) o[r][n] = f32x4w{0, 0, 0, 0};
     }
@@ -407,9 +399,9 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         }
       }
     };
-    // Folded: a lane turns one token's (and group's) parameters into what its scores and probabilities
-    // take, for all lanes that have that token: of keys scale 2^24 c and -zero scale c (c = scale of the
-    // scores, in log2), of values scale 2^7 / ref and zero, ref a power of two that no scale passes.
+    // Folded: a lane turns one token's (and group's) scales into what its scores and probabilities
+    // take, for all lanes that have that token: of keys scale c (c = scale of the scores, in log2), of
+    // values scale 2^7 / ref.
     const auto fold = [&](const char* from, int tb, uint32_t none, bool part) AWQ_INLINE {
       const int u = lane >> 4 & 1, at = 16 * (G == 2 ? lane >> 5 : 0) + (lane & 15);
       uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
@@ -431,17 +423,12 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
-          for (int g = 0; g < G; ++g) z_sum[r][g] *= f;
-#pragma unroll
           for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
         }
       }
-      const float a1 = ks * a.scale_log2;
       float* const to = mine + lane;  // (G = 1: lanes from 32 on repeat the others' values)
-      to[G == 1 ? -(lane & 32) : 0] = a1 * 0x1p24f;
-      to[32 * G + (G == 1 ? -(lane & 32) : 0)] = -(float)(kp & 15) * a1;
-      to[64 * G + (G == 1 ? -(lane & 32) : 0)] = vs * norm;
-      to[96 * G + (G == 1 ? -(lane & 32) : 0)] = (float)(vp & 15);
+      to[G == 1 ? -(lane & 32) : 0] = ks * a.scale_log2;
+      to[32 * G + (G == 1 ? -(lane & 32) : 0)] = vs * norm;
     };
     const auto folded = [&](int what, int g, int u) AWQ_INLINE {
       return *reinterpret_cast<const f32x4w*>(mine + 32 * G * what + 32 * g + 16 * u + 4 * h);
@@ -463,18 +450,16 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           f32x4w part_sum[R];
-          Params2 p;
+          const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(u))[16 * g + c];
+          const Params2 p = params2(kp | kp << 16);
           if constexpr (kFold) {
 #pragma unroll
             for (int r = 0; r < R; ++r) part_sum[r] = f32x4w{0, 0, 0, 0};
-          } else {
-            const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(u))[16 * g + c];
-            p = params2(kp | kp << 16);
           }
 #pragma unroll
           for (int t = g * kPerGroup; t < (g + 1) * kPerGroup; ++t) {
             half2w e[4];
-            if constexpr (kFold) raw4(kw[t], e);
+            if constexpr (kFold) centre4(kw[t], p.zz, p.zz64, magic, e);
             else widen4(kw[t], p.zz, p.zz64, p.s2, magic, e);
             const half8w key{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
 #pragma unroll
@@ -484,12 +469,12 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
             }
           }
           if constexpr (kFold) {
-            const f32x4w a1 = folded(0, g, u), a2 = folded(1, g, u);
+            const f32x4w by = folded(0, g, u);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                sc[r][u][i] = __builtin_fmaf(part_sum[r][i], a1[i], __builtin_fmaf(q_sum[r][g], a2[i], sc[r][u][i]));
+                sc[r][u][i] = __builtin_fmaf(part_sum[r][i], by[i], sc[r][u][i]);
           }
         }
       }
@@ -526,10 +511,6 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
           const float f = top > m[r] ? __builtin_amdgcn_exp2f(m[r] - top) : 1.0f;
           m[r] = top;
           l[r] *= f;
-          if constexpr (kFold) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) z_sum[r][g] *= f;
-          }
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
         }
@@ -546,12 +527,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
           for (int g = 0; g < kP; ++g) {
             f32x4w y = e;
             if constexpr (kFold) {
-              const f32x4w b1 = folded(2, g, u), z = folded(3, g, u);
+              y *= folded(1, g, u);
+              // rounded to fp32 before hi is taken of it: one instruction for product and hi would round
+              // once, now and then to another hi than the one that lo is the rest of
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                y[i] = e[i] * b1[i];
-                z_sum[r][g] = __builtin_fmaf(y[i], z[i], z_sum[r][g]);
-              }
+              for (int i = 0; i < 4; ++i) asm("" : "+v"(y[i]));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -569,19 +549,17 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
         S::value_words(from + S::v_codes(u), lane, vw[0]);
         S::value_words(from + S::v_codes(u + 1), lane, vw[1]);
         uint2 vp[2][G];
-        if constexpr (!kFold) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
-              if (part) {  // what no token wrote may be anything, an infinite scale too
-                const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
-                vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
-                vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
-              }
+          for (int g = 0; g < G; ++g) {
+            vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
+            if (!kFold && part) {  // what no token wrote may be anything, an infinite scale too
+              const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
+              vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
+              vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
             }
-        }
+          }
 #pragma unroll
         for (int t = 0; t < kSlices / 2; ++t) {  // tiles 4 t .. 4 t + 3, 64 channels
 #pragma unroll
@@ -591,12 +569,9 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
 #pragma unroll
             for (int b = 0; b < 4; ++b) {  // token pairs
               const uint32_t word = vw[b >> 1][2 * t + (b & 1)];
-              if constexpr (kFold) {
-                raw4(word, e[b]);
-              } else {
-                const Params2 p = params2(b & 1 ? vp[b >> 1][g].y : vp[b >> 1][g].x);
-                widen4(word, p.zz, p.zz64, p.s2, magic, e[b]);
-              }
+              const Params2 p = params2(b & 1 ? vp[b >> 1][g].y : vp[b >> 1][g].x);
+              if constexpr (kFold) centre4(word, p.zz, p.zz64, magic, e[b]);
+              else widen4(word, p.zz, p.zz64, p.s2, magic, e[b]);
             }
 #pragma unroll
             for (int j = 2 * half; j < 2 * half + 2; ++j) {
@@ -651,15 +626,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_wav
       l[r] += __shfl_xor(l[r], 32);
       if constexpr (kFold) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          z_sum[r][g] += __shfl_xor(z_sum[r][g], 16);
-          z_sum[r][g] += __shfl_xor(z_sum[r][g], 32);
-        }
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[r][n][i] = __builtin_fmaf(o[r][n][i], 0x1p24f, -z_sum[r][n / 2 / kPerGroup]) * (ref * 0x1p-7f);
+        for (int n = 0; n < kTiles; ++n) o[r][n] *= ref * 0x1p-7f;
       }
       __syncthreads();
       if (h == 0) ml[wave][c] = make_float2(m[r], l[r]);
