@@ -13,6 +13,18 @@
 // piece per block whatever the sequences' lengths, which only the device knows. A block that holds
 // the whole of a (sequence, tile, head) writes its output; pieces of one leave their unnormalised
 // sums, which k_attend_join adds in the order of the blocks.
+//
+// A wave takes every fourth 32 tokens of its block's piece. Their codes and parameters come by DMA
+// into one of the wave's own two LDS buffers while the other is worked on: no wave waits for another,
+// and no register holds what is under way. Waves take turns at priority (left alone, the oldest one
+// wins, and the blocks of a CU end one after the other).
+//
+// Measured. 24 sequences of 300-4000 tokens, 32 heads, D = 128, groups of 128 (241 MB): 62 us and 5 for
+// the join, 3.9 TB/s; one sequence of 131071 tokens, 8 heads of keys (138 MB): 38 and 7, 3.6 TB/s; 64
+// sequences, 8 heads of keys, groups of 32 (345 MB): 96 and 10, 3.6 TB/s. Bound by loads (alone 52 us
+// in the first case, 4.6 TB/s) and vector instructions (alone 56) that overlap in part only; matrix
+// cores are busy for 13% of the time. Short calls are chains of loads: the work list's, the
+// page's, the codes', 8 us for one sequence of 77 tokens.
 #pragma once
 
 #include "groups.hpp"
