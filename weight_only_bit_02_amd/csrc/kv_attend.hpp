@@ -21,7 +21,7 @@
 //
 // Measured. 24 sequences of 300-4000 tokens, 32 heads, D = 128, groups of 128 (241 MB): 62 us and 5 for
 // the join, 3.9 TB/s; one sequence of 131071 tokens, 8 heads of keys (138 MB): 38 and 7, 3.6 TB/s; 64
-// sequences, 8 heads of keys, groups of 32 (345 MB): 96 and 10, 3.6 TB/s. Bound by loads (alone 52 us
+// sequences, 8 heads of keys, groups of 32 (345 MB): 95 and 6, 3.7 TB/s. Bound by loads (alone 52 us
 // in the first case, 4.6 TB/s) and vector instructions (alone 56) that overlap in part only; matrix
 // cores are busy for 13% of the time. Short calls are chains of loads: the work list's, the
 // page's, the codes', 8 us for one sequence of 77 tokens.
@@ -273,7 +273,9 @@ struct StreamShape {
 
 // D channels, G groups of them, R tiles of 16 rows.
 template <int D, int G, int R>
-__global__ void __launch_bounds__(kAttendWaves* kWave) __attribute__((amdgpu_waves_per_eu(stream_waves(D, D / G, 16 * R)))) k_attend_stream(KvView v, AttendArgs a, AttendList list) {
+__global__ void __launch_bounds__(kAttendWaves* kWave)
+    __attribute__((amdgpu_waves_per_eu(stream_waves(D, D / G, 16 * R))))
+    k_attend_stream(KvView v, AttendArgs a, AttendList list) {
   constexpr int kSlices = D / 32, kTiles = D / 16, kPerGroup = kSlices / G;  // slices of a group
   using S = StreamShape<D, G>;
   constexpr int kUnits = S::kUnits, kStep = 16 * kUnits, kStages = S::kStages;

@@ -15,13 +15,13 @@
 // widened by each wave its share, one step ahead into one of three buffers, from registers loaded
 // a step before that.
 //
-// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 155 us, 889 TFLOP/s; pieces of
-// 257-1024 rows behind 2000-12345 tokens, 64 heads on 8 of keys, groups of 64: 885 us, 859 TFLOP/s (a
-// large product of the library: 1211). Matrix cores are busy for 38% of the cycles and vector
-// instructions for 50%, softmax 131 and widening some 100 a wave and step beside 2048 cycles of
-// products: the SIMD issues them in turn, and two waves of it overlap what they can. Operands
-// read eight products ahead, all waves in step, two running sums, or addresses in scalar registers: no
-// gain or a loss.
+// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 155-163 us by card, 846-889
+// TFLOP/s; pieces of 257-1024 rows behind 2000-12345 tokens, 64 heads on 8 of keys, groups of 64:
+// 885-925 us, 823-859 TFLOP/s (a large product of the library: 1211). Matrix cores are busy for 38% of
+// the cycles and vector instructions for 50%, softmax 131 and widening some 100 a wave and step beside
+// 2048 cycles of products: the SIMD issues them in turn, and its two waves overlap what they can.
+// Operands read eight products ahead, all waves in step, widening between the products, two running
+// sums, or addresses in scalar registers: no gain or a loss.
 //
 // 16-byte pieces of an LDS row are exchanged by the row's number, so that the 16 rows that a
 // read touches at a time lie in different banks.
