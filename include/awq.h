@@ -552,7 +552,8 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, voi
  *   over the tokens t < lengths[s] that have a page; causal = 1: t <= the row's position p;
  *   window > 0: t > p - window. A row without a token: zeros (lse -inf).
  *   q        fp16 [n_rows][q_ld], out fp16 [n_rows][out_ld]: q_heads x head_dim values a row,
- *            strides multiples of 8; q_heads a multiple of kv_heads
+ *            strides multiples of 8; q_heads a multiple of kv_heads; out may be q itself with the
+ *            same stride
  *   scale    above 0, below 1e20 (1 / sqrt(head_dim) as a rule)
  *   lse      fp32 [n_rows][q_heads] or NULL: log of the sum of exp(scale q . k_t)
  *   workspace device scratch of awq_attention_kv4_workspace_size bytes (max_tokens = max_pages

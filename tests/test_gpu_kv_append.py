@@ -230,6 +230,55 @@ def test_many_sequences():
         assert np.array_equal(host(o).astype(np.float64), (q - z.repeat(64, -1)) * sc.repeat(64, -1))
 
 
+@pytest.mark.parametrize("D,group,heads,q_heads,R,inter,T", [
+    (128, 64, 8, 12, 128, False, 2900),  # a wave takes heads of two kinds
+    (128, 128, 3, 7, 64, True, 9001),
+    (64, 32, 5, 5, 64, False, 20000),
+    (256, 128, 2, 6, 256, True, 3001),
+    (64, 64, 1, 1, 32, False, 200000),
+])
+def test_many_rows(D, group, heads, q_heads, R, inter, T):
+    """So many rows that a wave goes through several heads."""
+    rng = np.random.default_rng(10)
+    n = [T // 3, T - T // 3 - 1, 1]
+    lengths = [n[0] + 7, n[1], 900]
+    b, pages, table, rows = batch_of(awq, n, lengths, 64, rng)
+    dev = awq.alloc_kv_cache(pages, heads, D, DEV, group=group)
+    y = rows_of(T, q_heads + 2 * heads, D, rng)
+    q, k, v = to_dev(y).split([q_heads, heads, heads], dim=1)
+    tab = table_of(max(lengths), R, rng)
+    flags = flags_tensor()
+    out, check = guarded((T, q_heads, D), torch.float16)
+    awq.kv_append(dev, b, k, v, q, awq.Rotary(to_dev(tab), inter), out=out, flags=flags)
+    check()
+    assert host(flags)[0] == 0
+    at = positions_of(rows, lengths)
+    turned = kv_ref.rotate(y[:, :q_heads + heads], tab[at], inter)
+    assert np.array_equal(host(out).view(np.uint16), turned[:, :q_heads].view(np.uint16))
+    ko, vo = awq.kv_read(dev, b, T)
+    for x, o in ((turned[:, q_heads:], ko), (y[:, q_heads + heads:], vo)):
+        c, sc, z = kv_ref.quantize(x, group)
+        assert np.array_equal(host(o).astype(np.float64), (c - z.repeat(group, -1)) * sc.repeat(group, -1))
+
+
+@pytest.mark.parametrize("group", [32, 64])
+def test_halves(group):
+    """Values at and beside halves of the scale, of every size: quotients that are ties, or one fp16
+    step off."""
+    rng = np.random.default_rng(15)
+    T = 3000
+    x = rng.integers(-60, 61, (T, 1, 64)) / 4 * 2.0 ** rng.integers(-14, 8, (T, 1, 1))
+    x = x.astype(np.float16)
+    step = rng.integers(-1, 2, x.shape) * (rng.random(x.shape) < 0.3)
+    x = np.where(x == 0, x, (x.view(np.int16) + step).astype(np.int16).view(np.float16))
+    b, pages, _, _ = batch_of(awq, [T], [T], 64, rng)
+    dev = awq.alloc_kv_cache(pages, 1, 64, DEV, group=group)
+    awq.kv_append(dev, b, to_dev(x), to_dev(-x))
+    for y, o in zip((x, -x), awq.kv_read(dev, b, T)):
+        c, sc, z = kv_ref.quantize(y, group)
+        assert np.array_equal(host(o).astype(np.float64), (c - z.repeat(group, -1)) * sc.repeat(group, -1))
+
+
 def test_beyond_4_gib():
     """Pages whose codes lie past 2^32 bytes."""
     rng = np.random.default_rng(9)

@@ -218,10 +218,11 @@ def test_calls_at_once(n, max_rows):
     assert all(torch.equal(o, r) for part, r in zip(outs, ref) for o in part)
 
 
-@pytest.mark.parametrize("n,max_rows", [(1, 1), (40, None)])
-def test_strided_output(n, max_rows):
-    """Rows of outputs and queries with room between them, which stays as it was."""
-    b, pages, T = lists(3, n, 400, 32, 26, max_rows)
+@pytest.mark.parametrize("n,length,max_rows", [(1, 400, 1), (1, 9000, 1), (40, 400, None), (300, 2000, None)])
+def test_strided_output(n, length, max_rows):
+    """Rows of outputs and queries with room between them, which stays as it was; the output in the
+    queries' place."""
+    b, pages, T = lists(3, n, length, 32, 26, max_rows)
     cache = random_cache(pages, HEADS, 128, 32, 27)
     q = torch.randn(T, Q, 128, generator=torch.Generator(DEV).manual_seed(3), device=DEV).half()
     want = awq.attention_kv4(q, cache, b)
@@ -230,6 +231,8 @@ def test_strided_output(n, max_rows):
     assert awq.attention_kv4(strided(host(q), 16), cache, b, out=out) is out
     assert torch.equal(out, want)
     assert bool((buf[:, :8] == 7).all()) and bool((buf[:, 8 + Q * 128:] == 7).all())
+    assert awq.attention_kv4(q, cache, b, out=q) is q  # in place
+    assert torch.equal(q, want)
 
 
 def test_shared_pages():

@@ -175,7 +175,7 @@ def attention_kv4(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """awq_attention_kv4: attention of q fp16 [T][q_heads][head_dim] (rows may be strided), the
     batch's rows, over their sequences in the cache. scale: 1 / sqrt(head_dim) by default;
-    window: only the last so many tokens up to the row's own (0: all); lse fp32 [T][q_heads]
+    out: may be q; window: only the last so many tokens up to the row's own (0: all); lse fp32 [T][q_heads]
     (optional): log of the sums of exponentials. workspace: attention_kv4_workspace_size bytes,
     one for each of the calls that overlap."""
     dev = _first(q, (torch.float16,), 3, "q")
