@@ -35,7 +35,7 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave;
 
 template <int D>
 struct Lanes {
-  static constexpr int kRow = D / 8;                            // lanes of a row
+  static constexpr int kRow = D / 8;          // lanes of a row
   static constexpr int kRows = kWave / kRow;  // rows of a wave, and of its block
 };
 

@@ -31,7 +31,7 @@ constexpr int kFew = 64, kFewAlone = 128;
 // joins what is cut, some 40 us for the sums (128 KB of a piece). Pieces are taken where items are
 // few and their last round leaves CUs idle for longer than that: a tile's 36 tokens take a us at D =
 // 64 and 128, half as many at D = 256. 32 heads, D = 128, one item a block and pieces, in us:
-//   64 items of 512 tokens    30, 40       128 items of 1024     42, 55      256 of 2048    72, 120
+//   64 items of 512 tokens    30, 40        64 items of 1024     42, 55      256 of 2048    72, 120
 //   64 of 4000               118, 95       128 of 4096          120, 124     256 of 4096   135, 181
 //   64 of 16000              420, 191      128 of 8000          219, 180     384 of 9000   495, 458
 //   512 of 2048               94, 182     2048 of 2048          385, 471     512 of 9000   552, 585
