@@ -506,7 +506,8 @@ typedef struct awq_kv_cache {
  *                                 [0, pages): no page (not written, not attended to)
  *   n_rows      rows of the tensors, below 2^22; max_rows: no sequence has more (n_rows is
  *               always right; a smaller bound lets short rows take a shorter path)
- * A row before position 0 is no token: nothing is written for it, it attends to nothing.
+ * A row before position 0 is no token: its keys and values are not written, it attends to nothing
+ * (causal or not), reading gives zeros; its q is rotated by the table's first row.
  * A page that two sequences share is to be written by neither. */
 typedef struct awq_kv_batch {
   const int32_t *rows, *lengths, *page_table;

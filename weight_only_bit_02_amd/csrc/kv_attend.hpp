@@ -59,11 +59,17 @@ struct AttendSeq {
   int units;
 };
 
+// The last token that a row at position p may see, `last` the sequence's: none (-1 or less) for a row before
+// position 0, which is no token.
+__device__ __forceinline__ int attend_last(const AttendArgs& a, int p, int last) {
+  return p < last && (a.causal || p < 0) ? p : last;
+}
+
 // Chunks of tile j of a sequence: as far as its last row sees, one for rows without a token.
 __device__ __forceinline__ int attend_chunks(const AttendArgs& a, const AttendList& g, const AttendSeq& w, int j) {
   const int end = (j + 1) * g.tile < w.flat ? (j + 1) * g.tile : w.flat;
-  const int p = w.q.length - w.q.rows + (end - 1) / a.share + 1;  // tokens up to the last row's own
-  const int n = (a.causal && p < w.q.tokens ? p : w.q.tokens) - w.first;
+  const int p = w.q.length - w.q.rows + (end - 1) / a.share;  // the last row's position
+  const int n = attend_last(a, p, w.q.tokens - 1) + 1 - w.first;
   return n <= 0 ? 1 : (n + kAttendChunk - 1) / kAttendChunk;
 }
 
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     for (int r = 0; r < R; ++r) {
       const int row = r0 + 16 * r + c, in = row <= r1 ? row : r1;
       const int token = in / a.share, p = p0 + token;
-      hi[r] = a.causal && p < last ? p : last;
+      hi[r] = attend_last(a, p, last);
       lo[r] = a.window > 0 ? p - a.window + 1 : 0;
       const uint16_t* x = a.q + (w.q.row0 + token) * a.q_ld + (int64_t)(head * a.share + in - token * a.share) * D;
 #pragma unroll
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     }
     // tokens that every row of the tile sees, and that any does
     const int pa = p0 + r0 / a.share, pb = p0 + r1 / a.share;
-    const int all_hi = a.causal && pa < last ? pa : last, any_hi = a.causal && pb < last ? pb : last;
+    const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
     const int all_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int t0 = w.first + u0 * kAttendChunk;
     int t1 = w.first + u1 * kAttendChunk;

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     const int row = wr0 + c, rin = row <= r1 ? row : r1;
     const int token = rin / a.share, q_head = x.head * a.share + rin - token * a.share;
     const int p = p0 + token;
-    const int hi = a.causal && p < last ? p : last, lo = a.window > 0 ? p - a.window + 1 : 0;
+    const int hi = attend_last(a, p, last), lo = a.window > 0 ? p - a.window + 1 : 0;
     half8w q[kSlices];
     {
       const uint16_t* qr = a.q + (w.q.row0 + token) * a.q_ld + (int64_t)q_head * D;
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     }
     // tokens that all of the wave's rows see, that any does, and that any of the block's does
     const int pa = p0 + wr0 / a.share, pb = p0 + wr1 / a.share, pe = p0 + r1 / a.share;
-    const int all_hi = a.causal && pa < last ? pa : last, any_hi = a.causal && pb < last ? pb : last;
+    const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
     const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
-    const int end = (a.causal && pe < last ? pe : last) + 1;
+    const int end = attend_last(a, pe, last) + 1;
     const int t0 = w.first + u0 * kAttendChunk;
     const int t1 = w.first + u1 * kAttendChunk < end ? w.first + u1 * kAttendChunk : end;
     const bool rows = wr0 <= r1;
