@@ -552,6 +552,8 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, voi
  *     out[r][h] = sum_t softmax_t(scale q[r][h] . k_t) v_t,  k, v of head h / (q_heads / kv_heads)
  *   over the tokens t < lengths[s] that have a page; causal = 1: t <= the row's position p;
  *   window > 0: t > p - window. A row without a token: zeros (lse -inf).
+ *   Tokens that no row of a sequence sees (before the windows, behind its length) may hold
+ *   anything, infinite scales too: pages that were given up may stay in the table.
  *   q        fp16 [n_rows][q_ld], out fp16 [n_rows][out_ld]: q_heads x head_dim values a row,
  *            strides multiples of 8; q_heads a multiple of kv_heads; out may be q itself with the
  *            same stride

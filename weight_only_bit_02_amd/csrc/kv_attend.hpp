@@ -177,6 +177,15 @@ struct AttendSeqs {
   }
 };
 
+// Parameters of tokens t .. t + 3 with those outside [lo, hi] cleared: what nobody sees may be anything, an
+// infinite scale too.
+__device__ __forceinline__ uint2 attend_seen(uint2 p, int t, int lo, int hi) {
+  const auto keep = [&](int i, uint32_t bits) AWQ_INLINE { return t + i < lo || t + i > hi ? 0u : bits; };
+  p.x &= keep(0, 0xFFFFu) | keep(1, 0xFFFF0000u);
+  p.y &= keep(2, 0xFFFFu) | keep(3, 0xFFFF0000u);
+  return p;
+}
+
 // What block b leaves for k_attend_join (thread 0): the item that the next block goes on with.
 __device__ __forceinline__ void attend_split(const AttendArgs& a, const AttendSplit& d) {
   if (a.split && threadIdx.x == 0) a.split[blockIdx.x] = d;
@@ -356,7 +365,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     // tokens that every row of the tile sees, and that any does
     const int pa = p0 + r0 / a.share, pb = p0 + r1 / a.share;
     const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
-    const int all_lo = a.window > 0 ? pb - a.window + 1 : 0;
+    const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
     const int t0 = w.first + u0 * kAttendChunk;
     int t1 = w.first + u1 * kAttendChunk;
     t1 = t1 <= any_hi ? t1 : any_hi + 1;
@@ -428,9 +437,10 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
       const int u = lane >> 4 & 1, at = 16 * (G == 2 ? lane >> 5 : 0) + (lane & 15);
       uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
       uint32_t vp = reinterpret_cast<const uint16_t*>(from + S::v_params(0) + u * S::kParams)[at];
-      if (part) {  // what no token wrote may be anything, an infinite scale too
+      if (part) {  // (attend_seen)
         asm volatile("");
-        if (tb + (lane & 31) > last || (none >> (kUnits - 1 - u) & 1)) kp = vp = 0;
+        const int t = tb + (lane & 31);
+        if (t < any_lo || t > any_hi || (none >> (kUnits - 1 - u) & 1)) kp = vp = 0;
       }
       const float ks = h2f(kp & 0xFFF0), vs = h2f(vp & 0xFFF0);
       if (__ballot(vs > ref)) {
@@ -576,11 +586,9 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
-            if (!kFold && part) {  // what no token wrote may be anything, an infinite scale too
-              const int t = (none >> (kUnits - 1 - u - b) & 1) ? 4 : tb + 16 * (u + b) + 4 * h - last;
-              vp[b][g].x &= (t > 0 ? 0u : 0xFFFFu) | (t + 1 > 0 ? 0u : 0xFFFF0000u);
-              vp[b][g].y &= (t + 2 > 0 ? 0u : 0xFFFFu) | (t + 3 > 0 ? 0u : 0xFFFF0000u);
-            }
+            if (!kFold && part)
+              vp[b][g] = attend_seen(vp[b][g], tb + 16 * (u + b) + 4 * h, any_lo,
+                                     (none >> (kUnits - 1 - u - b) & 1) ? -1 : any_hi);
           }
 #pragma unroll
         for (int t = 0; t < kSlices / 2; ++t) {  // tiles 4 t .. 4 t + 3, 64 channels

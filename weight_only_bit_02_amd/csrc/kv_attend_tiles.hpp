@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     const int pa = p0 + wr0 / a.share, pb = p0 + wr1 / a.share, pe = p0 + r1 / a.share;
     const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
     const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
-    const int end = attend_last(a, pe, last) + 1;
+    const int end = attend_last(a, pe, last) + 1, begin = a.window > 0 ? p0 + r0 / a.share - a.window + 1 : 0;
     const int t0 = w.first + u0 * kAttendChunk;
     const int t1 = w.first + u1 * kAttendChunk < end ? w.first + u1 * kAttendChunk : end;
     const bool rows = wr0 <= r1;
@@ -227,18 +227,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         const half8w b{e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
         keys[buf][swizzled<D / 8>(16 * sub + k_token, 4 * (k_s + i) + k_h)] = __builtin_bit_cast(uint4, b);
       }
-      // what no token wrote may be anything, an infinite scale too
       uint2 vp[Codes::kGroups];
 #pragma unroll
       for (int i = 0; i < Codes::kGroups; ++i) vp[i] = d.vp[i];
-      if (tb + kTokens > t1 || __ballot(d.page < 0)) {
+      if (tb + kTokens > t1 || tb < begin || __ballot(d.page < 0)) {
         asm volatile("");  // nothing of this ahead of the branch
-        const int behind = d.page < 0 ? 4 : tb + 16 * sub + 4 * v_h - last;  // token i of the four: behind + i > 0
 #pragma unroll
-        for (int i = 0; i < Codes::kGroups; ++i) {
-          vp[i].x &= (behind > 0 ? 0 : 0xFFFFu) | (behind + 1 > 0 ? 0 : 0xFFFF0000u);
-          vp[i].y &= (behind + 2 > 0 ? 0 : 0xFFFFu) | (behind + 3 > 0 ? 0 : 0xFFFF0000u);
-        }
+        for (int i = 0; i < Codes::kGroups; ++i)
+          vp[i] = attend_seen(vp[i], tb + 16 * sub + 4 * v_h, begin, d.page < 0 ? -1 : end - 1);
       }
 #pragma unroll
       for (int i = 0; i < kWords / 2; ++i) {  // channels v_c + 16 (4 (v_w + i) + j)
