@@ -38,6 +38,10 @@ namespace awq {
 constexpr int kAttendWaves = 4;
 constexpr int kAttendChunk = 256;  // tokens of the work list's unit, a multiple of every kernel's step
 constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score passes it by 2^8
+// Probabilities go to the second product times 2^7: up to 2^15 (kLazy) they fit fp16, and its smallest
+// number, 2^-24, is 2^-31 of the largest probability, not 2^-24. A first token of value zero, 18 nats above 8000
+// others: off by 8e-3 (hi + lo) and 3e-2 (one fp16) without the 2^7, by 2e-4 with it, as the output's rounding alone.
+constexpr float kLift = 7.0f, kDrop = 0x1p-7f;
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;  // of a join block, at most
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
         }
-        const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+        const float base = m[r] == -__builtin_inff() ? 0.0f : m[r] - (kFold ? 0.0f : kLift);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
           f32x4w e;
@@ -657,6 +661,10 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
       if constexpr (kFold) {
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) o[r][n] *= ref * 0x1p-7f;
+      } else {
+        l[r] *= kDrop;
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) o[r][n] *= kDrop;
       }
       __syncthreads();
       if (h == 0) ml[wave][c] = make_float2(m[r], l[r]);

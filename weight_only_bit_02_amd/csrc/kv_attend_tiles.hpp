@@ -6,7 +6,8 @@
 // v_mfma_f32_32x32x16_f16: S^T = K Q^T leaves lane (h, c) = (lane / 32, lane % 32) row c's scores of
 // tokens 8 i + 4 h + 0..3, which are the second operand of O^T = V^T P^T for values whose tokens lie
 // in that order: LDS holds them so. Probabilities go to the second product rounded to fp16 (an
-// error of the output's own size; hi + lo would be half as much matrix work again).
+// error of the output's own size; hi + lo would be half as much matrix work again), below 2^-21 of the row's
+// largest in steps of 2^-31 of it (kLift).
 //
 // A step: scores and softmax, widening of a later step's codes, the second product. The block's
 // second four waves, which share the SIMDs with the first four, run half a step behind, so that one
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
         for (int n = 0; n < D / 32; ++n) o[n] *= f;
       }
-      const float base = m == -__builtin_inff() ? 0.0f : m;
+      const float base = m == -__builtin_inff() ? 0.0f : m - kLift;
 #pragma unroll
       for (int t = 0; t < kParts; ++t)
 #pragma unroll
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
             *reinterpret_cast<half4a*>(y + 32 * n + 2 * i + 4 * h) = b;
           }
         if (a.lse && h == 0)
-          a.lse[(int64_t)(w.q.row0 + token) * a.q_heads + q_head] = attend_lse(m, l);
+          a.lse[(int64_t)(w.q.row0 + token) * a.q_heads + q_head] = attend_lse(m, l * kDrop);
       } else {
         const int64_t slot = ((int64_t)2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * T::kRows + (row - r0);
         float* y = a.part + slot * D;
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<f32x4w*>(y + 32 * n + 2 * i + 4 * h) =
-                f32x4w{o[n][i], o[n][i + 1], o[n][i + 2], o[n][i + 3]};
-        if (h == 0) a.part_ml[slot] = make_float2(m, l);
+                f32x4w{o[n][i], o[n][i + 1], o[n][i + 2], o[n][i + 3]} * kDrop;
+        if (h == 0) a.part_ml[slot] = make_float2(m, l * kDrop);
       }
     }
     unit += u1 - u0;
