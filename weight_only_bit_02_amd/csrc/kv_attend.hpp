@@ -43,6 +43,11 @@ constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score pa
 // others: off by 8e-3 (hi + lo) and 3e-2 (one fp16) without the 2^7, by 2e-4 with it, as the output's rounding alone.
 constexpr float kLift = 7.0f, kDrop = 0x1p-7f;
 
+// A score times the softmax's scale minus the maximum is one instruction, but the maximum was rounded:
+// scores from 2^24 on differ from it by more than a unit of log2, from 2^27 on by so much that probabilities are
+// infinite in fp16 or all zero. Rows whose maximum passes this have it taken off first (attend_far).
+constexpr float kFar = 0x1p22f;
+
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;  // of a join block, at most
 
@@ -180,6 +185,17 @@ struct AttendSeqs {
     return v.seqs;
   }
 };
+
+// x as it is, rounded to fp32: no part of an instruction that rounds once for two operations.
+__device__ __forceinline__ float attend_rounded(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
+// The score that, times scale, is x scale - m with the product rounded, as m was.
+__device__ __forceinline__ float attend_far(float x, float m, float scale) {
+  return (attend_rounded(x * scale) - m) * __builtin_amdgcn_rcpf(scale);
+}
 
 // Parameters of tokens t .. t + 3 with those outside [lo, hi] cleared: what nobody sees may be anything, an
 // infinite scale too.
@@ -550,7 +566,17 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
         }
-        const float base = m[r] == -__builtin_inff() ? 0.0f : m[r] - (kFold ? 0.0f : kLift);
+        float base = m[r] == -__builtin_inff() ? 0.0f : m[r] - (kFold ? 0.0f : kLift);
+        if (!kFold && __ballot(__builtin_fabsf(base) > kFar)) {
+          asm volatile("");
+          if (__builtin_fabsf(base) > kFar) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[r][u][i] = attend_far(sc[r][u][i], m[r], a.scale_log2);
+            base = -kLift;
+          }
+        }
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
           f32x4w e;
@@ -564,10 +590,10 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
             f32x4w y = e;
             if constexpr (kFold) {
               y *= folded(1, g, u);
-              // rounded to fp32 before hi is taken of it: one instruction for product and hi would round
-              // once, now and then to another hi than the one that lo is the rest of
+              // before hi is taken of it: one instruction for product and hi would round once, now and then to
+              // another hi than the one that lo is the rest of
 #pragma unroll
-              for (int i = 0; i < 4; ++i) asm("" : "+v"(y[i]));
+              for (int i = 0; i < 4; ++i) y[i] = attend_rounded(y[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

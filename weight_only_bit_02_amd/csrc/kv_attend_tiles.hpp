@@ -322,7 +322,17 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 #pragma unroll
         for (int n = 0; n < D / 32; ++n) o[n] *= f;
       }
-      const float base = m == -__builtin_inff() ? 0.0f : m - kLift;
+      float base = m == -__builtin_inff() ? 0.0f : m - kLift;
+      if (__ballot(__builtin_fabsf(base) > kFar)) {
+        asm volatile("");
+        if (__builtin_fabsf(base) > kFar) {
+#pragma unroll
+          for (int t = 0; t < kParts; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[t][i] = attend_far(sc[t][i], m, a.scale_log2);
+          base = -kLift;
+        }
+      }
 #pragma unroll
       for (int t = 0; t < kParts; ++t)
 #pragma unroll
