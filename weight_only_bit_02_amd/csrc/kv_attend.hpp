@@ -42,7 +42,11 @@ constexpr float kLazy = 8.0f;  // the running maximum is renewed when a score pa
 // number, 2^-24, is 2^-31 of the largest probability, not 2^-24. A first token of value zero, 18 nats above 8000
 // others: off by 8e-3 (hi + lo) and 3e-2 (one fp16) without the 2^7, by 2e-4 with it, as the output's rounding alone.
 constexpr float kLift = 7.0f, kDrop = 0x1p-7f;
-
+// Folded (k_attend_stream), a probability takes the value's scale along, 2^-14 to 2^13, so that the maximum
+// that runs is that of their products, for each row and group: the largest one that the row met lies between 2^6
+// and 2^15. (One power of two for all rows of a wave, above every scale that it loaded: values 2^25 below others that
+// the row does not see were off by 2e-2.)
+constexpr float kRoom = 15.0f, kLeastScale = 0x1p-14f;
 // A score times the softmax's scale minus the maximum is one instruction, but the maximum was rounded:
 // scores from 2^24 on differ from it by more than a unit of log2, from 2^27 on by so much that probabilities are
 // infinite in fp16 or all zero. Rows whose maximum passes this have it taken off first (attend_far).
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
   // zeros, up to 15 scales a token, leave a small difference: 131071 tokens with values around zero
   // came out 1e-3 off, relatively, not 2e-4.)
   constexpr bool kFold = G <= 2;
-  __shared__ __attribute__((aligned(16))) float folds[kFold ? kAttendWaves : 1][64 * G];
+  __shared__ __attribute__((aligned(16))) float folds[kFold ? kAttendWaves : 1][96 * G];
   __shared__ float2 ml[kAttendWaves][16];
 
   const int lane = threadIdx.x & (kWave - 1), h = lane >> 4, c = lane & 15;
@@ -391,12 +395,15 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     t1 = t1 <= any_hi ? t1 : any_hi + 1;
 
     f32x4w o[R][kTiles];
-    float m[R], l[R];
-    float ref = 0.0f, norm = 0.0f;  // folded: a power of two that no value's scale passes; 2^7 / ref
+    constexpr int kP = kFold ? G : 1;
+    // a row's (group's) running maximum; folded: its sums are in units of 2^m[g], products up to limit[g] fit, and
+    // rest[g] = 2^(m[0] - m[g])
+    float m[R][kP], l[R], limit[R][kP], rest[R][kP];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      m[r] = -__builtin_inff();
       l[r] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kP; ++g) m[r][g] = limit[r][g] = -__builtin_inff(), rest[r][g] = 1.0f;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) o[r][n] = f32x4w{0, 0, 0, 0};
     }
@@ -450,9 +457,8 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
         }
       }
     };
-    // Folded: a lane turns one token's (and group's) scales into what its scores and probabilities
-    // take, for all lanes that have that token: of keys scale c (c = scale of the scores, in log2), of
-    // values scale 2^7 / ref.
+    // Folded: a lane brings one token's (and group's) scales into fp32 for all lanes that have that token: of keys
+    // times the softmax's (in log2), of values, and the latter's log2.
     const auto fold = [&](const char* from, int tb, uint32_t none, bool part) AWQ_INLINE {
       const int u = lane >> 4 & 1, at = 16 * (G == 2 ? lane >> 5 : 0) + (lane & 15);
       uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
@@ -463,24 +469,10 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
         if (t < any_lo || t >= t1 || (none >> (kUnits - 1 - u) & 1)) kp = vp = 0;
       }
       const float ks = h2f(kp & 0xFFF0), vs = h2f(vp & 0xFFF0);
-      if (__ballot(vs > ref)) {
-        asm volatile("");
-        float most = vs;
-#pragma unroll
-        for (int i = 1; i < kWave; i <<= 1) most = fmaxf(most, __shfl_xor(most, i));
-        const float next = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, most) + 0x7FFFFFu) & 0xFF800000u);
-        const float f = ref / next;  // (exact)
-        ref = next;
-        norm = 128.0f / next;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
-        }
-      }
       float* const to = mine + lane;  // (G = 1: lanes from 32 on repeat the others' values)
       to[G == 1 ? -(lane & 32) : 0] = ks * a.scale_log2;
-      to[32 * G + (G == 1 ? -(lane & 32) : 0)] = vs * norm;
+      to[32 * G + (G == 1 ? -(lane & 32) : 0)] = vs;
+      to[64 * G + (G == 1 ? -(lane & 32) : 0)] = __builtin_amdgcn_logf(fmaxf(vs, kLeastScale));
     };
     const auto folded = [&](int what, int g, int u) AWQ_INLINE {
       return *reinterpret_cast<const f32x4w*>(mine + 32 * G * what + 32 * g + 16 * u + 4 * h);
@@ -546,35 +538,71 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
       }
       // probabilities, as fp16 hi + lo: rounded to fp16 alone they would add as much to the output's
       // error as its own rounding does
-      constexpr int kP = kFold ? G : 1;
       half8w ph[kP][R][kUnits / 2], pl[kP][R][kUnits / 2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float top = sc[r][0][0];
+        const auto highest = [&](int g) AWQ_INLINE {  // of the scores; folded: g >= 0 with the values' scales
+          float x = -__builtin_inff();
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
+          for (int u = 0; u < kUnits; ++u) {
+            f32x4w y = sc[r][u];
+            if (kFold && g >= 0) y += folded(2, g, u);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][u][i]);
-        if constexpr (!kFold) top *= a.scale_log2;
-        if (__ballot(top > m[r] + kLazy)) {
-          asm volatile("");
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[r]);
-          const float f = top > m[r] ? __builtin_amdgcn_exp2f(m[r] - top) : 1.0f;
-          m[r] = top;
-          l[r] *= f;
+            for (int i = 0; i < 4; ++i) x = fmaxf(x, y[i]);
+          }
+          return x;
+        };
+        const auto of_row = [&](float x) AWQ_INLINE {
+          x = fmaxf(x, __shfl_xor(x, 16));
+          return fmaxf(x, __shfl_xor(x, 32));
+        };
+        float base;
+        if constexpr (kFold) {
+          float top[kP];
+          bool over = false;
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
-        }
-        float base = m[r] == -__builtin_inff() ? 0.0f : m[r] - (kFold ? 0.0f : kLift);
-        if (!kFold && __ballot(__builtin_fabsf(base) > kFar)) {
-          asm volatile("");
-          if (__builtin_fabsf(base) > kFar) {
+          for (int g = 0; g < kP; ++g) over |= (top[g] = highest(g)) > limit[r][g];
+          if (__ballot(over)) {
+            asm volatile("");
+            // scores beyond kFar lose the scales beside them: their maximum alone, looked at every step
+            const float plain = of_row(highest(-1));
+            const bool far = __builtin_fabsf(plain) > kFar;
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u)
+            for (int g = 0; g < kP; ++g) {
+              const float weighed = of_row(top[g]);
+              const float next = far ? plain : __builtin_ceilf(weighed) - kLift;
+              const bool renew = (far || weighed > limit[r][g]) && next > m[r][g];
+              const float f = renew ? __builtin_amdgcn_exp2f(m[r][g] - next) : 1.0f;
+              if (renew) limit[r][g] = far ? -__builtin_inff() : next + kRoom;
+              if (renew) m[r][g] = next;
+              if (g == 0) l[r] *= f;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sc[r][u][i] = attend_far(sc[r][u][i], m[r], a.scale_log2);
-            base = -kLift;
+              for (int n = g * kTiles / kP; n < (g + 1) * kTiles / kP; ++n) o[r][n] *= f;
+              rest[r][g] = g == 0 || m[r][g] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[r][0] - m[r][g]);
+            }
+          }
+          base = m[r][0] == -__builtin_inff() ? 0.0f : m[r][0];
+        } else {
+          float top = highest(-1) * a.scale_log2;
+          if (__ballot(top > m[r][0] + kLazy)) {
+            asm volatile("");
+            top = fmaxf(of_row(top), m[r][0]);
+            const float f = top > m[r][0] ? __builtin_amdgcn_exp2f(m[r][0] - top) : 1.0f;
+            m[r][0] = top;
+            l[r] *= f;
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) o[r][n] *= f;
+          }
+          base = m[r][0] == -__builtin_inff() ? 0.0f : m[r][0] - kLift;
+          if (__ballot(__builtin_fabsf(base) > kFar)) {
+            asm volatile("");
+            if (__builtin_fabsf(base) > kFar) {
+#pragma unroll
+              for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[r][u][i] = attend_far(sc[r][u][i], m[r][0], a.scale_log2);
+              base = -kLift;
+            }
           }
         }
 #pragma unroll
@@ -590,6 +618,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
             f32x4w y = e;
             if constexpr (kFold) {
               y *= folded(1, g, u);
+              if (g > 0) y *= rest[r][g];
               // before hi is taken of it: one instruction for product and hi would round once, now and then to
               // another hi than the one that lo is the rest of
 #pragma unroll
@@ -689,22 +718,21 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     for (int r = 0; r < R; ++r) {
       l[r] += __shfl_xor(l[r], 16);
       l[r] += __shfl_xor(l[r], 32);
-      if constexpr (kFold) {
+      if constexpr (!kFold) l[r] *= kDrop;
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) o[r][n] *= ref * 0x1p-7f;
-      } else {
-        l[r] *= kDrop;
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) o[r][n] *= kDrop;
+      for (int n = 0; n < kTiles; ++n) {
+        const int g = n * kP / kTiles;
+        if (!kFold) o[r][n] *= kDrop;
+        else if (g > 0) o[r][n] *= 1.0f / rest[r][g];
       }
       __syncthreads();
-      if (h == 0) ml[wave][c] = make_float2(m[r], l[r]);
+      if (h == 0) ml[wave][c] = make_float2(m[r][0], l[r]);
       __syncthreads();
       float top = ml[0][c].x;
 #pragma unroll
       for (int i = 1; i < kAttendWaves; ++i) top = fmaxf(top, ml[i][c].x);
       const float base = top == -__builtin_inff() ? 0.0f : top;
-      const float f = __builtin_amdgcn_exp2f(m[r] - base);
+      const float f = __builtin_amdgcn_exp2f(m[r][0] - base);
       const int row = threadIdx.x >> 4, col = 4 * (threadIdx.x & 15);  // the thread's part of 16 x 64 sums
       float rtop = ml[0][row].x, sum = 0.0f;
 #pragma unroll
