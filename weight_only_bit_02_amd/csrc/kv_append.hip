@@ -238,7 +238,8 @@ __device__ __forceinline__ void put_heads(const uint16_t* x, int lo, int hi, int
                        : rotated(v[i], v[i ^ 1], turn.cos[i / 2], i & 1 ? -turn.sin[i / 2] : turn.sin[i / 2]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = y[i];
-      met.over |= checks && !odd && nonfinite8(pack8(v));
+      // (of finite pairs: an Inf in the other half is no overflow)
+      met.over |= checks && !odd && !(two && nonfinite8(other)) && nonfinite8(pack8(v));
     }
     if constexpr (kKind == kQueries) {
       to(h, pack8(v), (uint16_t)0);
