@@ -276,7 +276,7 @@ constexpr int stream_waves(int dim, int group, int tile) {
 template <int D, int G>
 struct StreamShape {
   static constexpr int kUnits = 2;   // of 16 tokens, of a step (4: two buffers take half the chip's waves)
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 2;  // one is worked on (the waits count on it)
   static constexpr int kCodes = 8 * D;    // bytes of a unit's keys, or values
   static constexpr int kParams = 32 * G;  // of their parameters, [group][token]
   static constexpr int kStage = 2 * kUnits * (kCodes + kParams);
@@ -691,8 +691,6 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
       if (ahead == kStages - 1) {
         send(k + kStages - 1);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * S::kSends) : "memory");
-      } else if (kStages > 2 && ahead > 0) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kSends) : "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
