@@ -505,7 +505,8 @@ typedef struct awq_kv_cache {
  *   page_table  int32 [seqs][max_pages]  the page of each page_size tokens; outside
  *                                 [0, pages): no page (not written, not attended to)
  *   n_rows      rows of the tensors, below 2^22; max_rows: no sequence has more (n_rows is
- *               always right; a smaller bound lets short rows take a shorter path)
+ *               always right; a decoding batch should say 1: its attention is planned for one
+ *               long sequence otherwise and takes half as long again)
  * A row before position 0 is no token: its keys and values are not written, it attends to nothing
  * (causal or not), reading gives zeros; its q is rotated by the table's first row.
  * A page that two sequences share is to be written by neither. */
@@ -562,7 +563,9 @@ awq_status awq_kv_read(const awq_kv_cache* cache, const awq_kv_batch* batch, voi
  *   workspace device scratch of awq_attention_kv4_workspace_size bytes (max_tokens = max_pages
  *            page_size), 16-byte aligned; 0 where nothing is split. One for each of the
  *            calls that overlap
- *   Scores, softmax and sums in fp32. An Inf or NaN in q reaches its own row and head only.
+ *   Scores, softmax and sums in fp32; probabilities go to their product with the values as two
+ *   fp16 (22 bits) where rows are few, as one (11 bits) in prompts. An Inf or NaN in q reaches
+ *   its own row and head only.
  *   n_rows q_heads < 2^24, (n_rows q_heads / kv_heads / 16 + seqs) kv_heads (max_tokens / 256
  *   + 1) < 2^31 (else BAD_SHAPE).
  */

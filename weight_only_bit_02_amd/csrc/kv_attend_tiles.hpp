@@ -16,9 +16,9 @@
 // widened by each wave its share, one step ahead into one of three buffers, from registers loaded
 // a step before that.
 //
-// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 155-163 us by card, 846-889
+// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 157-161 us by card, 853-877
 // TFLOP/s; pieces of 257-1024 rows behind 2000-12345 tokens, 64 heads on 8 of keys, groups of 64:
-// 885-925 us, 823-859 TFLOP/s (a large product of the library: 1211). Matrix cores are busy for 38% of
+// 904-928 us, 819-841 TFLOP/s (a large product of the library: 1211). Matrix cores are busy for 37% of
 // the cycles and vector instructions for 50%, softmax 131 and widening some 100 a wave and step beside
 // 2048 cycles of products: the SIMD issues them in turn, and its two waves overlap what they can.
 // Operands read eight products ahead, all waves in step, widening between the products, two running

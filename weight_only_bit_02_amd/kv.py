@@ -2,7 +2,7 @@
 (argument marshalling only).
 
     cache = alloc_kv_cache(pages, kv_heads, head_dim, device)      # one per layer
-    batch = KVBatch(rows, lengths, page_table)                     # one per step, for all layers
+    batch = KVBatch(rows, lengths, page_table, max_rows)           # one per step, for all layers
     q, k, v = linear_w4a16(x, qkv).view(T, -1, head_dim).split([q_heads, kv_heads, kv_heads], dim=1)
     q = kv_append(cache, batch, k, v, q, Rotary(cos_sin))          # rotated; k and v are in the cache
     y = attention_kv4(q, cache, batch)                             # [T][q_heads][head_dim]
@@ -44,7 +44,8 @@ class KVBatch:
     rows: torch.Tensor        # int32 [S + 1]: sequence s has rows [rows[s], rows[s + 1])
     lengths: torch.Tensor     # int32 [S]: tokens in the cache, those of the rows among them
     page_table: torch.Tensor  # int32 [S][max_pages]; -1: no page
-    max_rows: int | None = None  # no sequence has more rows (None: as many as there are)
+    # no sequence has more rows; None: as many as there are, which takes a decoding batch (1) half as long again
+    max_rows: int | None = None
 
 
 @dataclass
