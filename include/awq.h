@@ -476,8 +476,8 @@ awq_status awq_linear_w4a16_lora(const void* X, int64_t M, const uint32_t* qweig
  * captured graph serves growing sequences.
  *
  * Format: per token, head and group of group_size channels one 16-bit parameter: the fp16
- * bits of a scale of 7 significant bits (the low four are zero) with the zero z in the low
- * four; value = (code - z) scale, exact in fp16. Codes, 4 bits:
+ * bits of a scale of 7 significant bits (the low four are zero), 2^-14 to 4352, with the zero z
+ * in the low four; value = (code - z) scale, exact in fp16. Codes, 4 bits:
  *   k_codes  [pages][kv_heads][page_size][D/2] bytes, D = head_dim. A token's row is D/8 words
  *            of 32 bits: word h (D/32) + s holds channels 32 s + 8 h + i, i = 0..7, with nibble
  *            order as in qweight (nibble j holds i = (0,2,4,6,1,3,5,7)[j])

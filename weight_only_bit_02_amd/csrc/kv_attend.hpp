@@ -201,13 +201,12 @@ __device__ __forceinline__ float attend_far(float x, float m, float scale) {
   return (attend_rounded(x * scale) - m) * __builtin_amdgcn_rcpf(scale);
 }
 
-// Parameters of tokens t .. t + 3 with those outside [lo, hi] cleared: what nobody sees may be anything, an
-// infinite scale too.
-__device__ __forceinline__ uint2 attend_seen(uint2 p, int t, int lo, int hi) {
-  const auto keep = [&](int i, uint32_t bits) AWQ_INLINE { return t + i < lo || t + i > hi ? 0u : bits; };
-  p.x &= keep(0, 0xFFFFu) | keep(1, 0xFFFF0000u);
-  p.y &= keep(2, 0xFFFFu) | keep(3, 0xFFFF0000u);
-  return p;
+// Parameters of two tokens' values, scales at most 4352 as appending writes them. What no row sees may be
+// anything, an infinite scale too, and its probability, zero, must meet a finite value. (Clearing what is seen by
+// none, by its position: 1% to 2% of every call with many groups or rows.)
+__device__ __forceinline__ uint32_t attend_finite(uint32_t p) {
+  typedef uint16_t half_words __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half_words, p), half_words{0x6C4F, 0x6C4F}));
 }
 
 // What block b leaves for k_attend_join (thread 0): the item that the next block goes on with.
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     // tokens that every row of the tile sees, and that any does
     const int pa = p0 + r0 / a.share, pb = p0 + r1 / a.share;
     const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
-    const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
+    const int all_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int t0 = w.first + u0 * kAttendChunk;
     int t1 = w.first + u1 * kAttendChunk;
     t1 = t1 <= any_hi ? t1 : any_hi + 1;
@@ -459,15 +458,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
     };
     // Folded: a lane brings one token's (and group's) scales into fp32 for all lanes that have that token: of keys
     // times the softmax's (in log2), of values, and the latter's log2.
-    const auto fold = [&](const char* from, int tb, uint32_t none, bool part) AWQ_INLINE {
+    const auto fold = [&](const char* from) AWQ_INLINE {
       const int u = lane >> 4 & 1, at = 16 * (G == 2 ? lane >> 5 : 0) + (lane & 15);
-      uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
+      const uint32_t kp = reinterpret_cast<const uint16_t*>(from + S::k_params(0) + u * S::kParams)[at];
       uint32_t vp = reinterpret_cast<const uint16_t*>(from + S::v_params(0) + u * S::kParams)[at];
-      if (part) {  // (attend_seen)
-        asm volatile("");
-        const int t = tb + (lane & 31);
-        if (t < any_lo || t >= t1 || (none >> (kUnits - 1 - u) & 1)) kp = vp = 0;
-      }
+      vp = attend_finite(vp);
       const float ks = h2f(kp & 0xFFF0), vs = h2f(vp & 0xFFF0);
       float* const to = mine + lane;  // (G = 1: lanes from 32 on repeat the others' values)
       to[G == 1 ? -(lane & 32) : 0] = ks * a.scale_log2;
@@ -482,7 +477,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
       const char* from = smem + (wave * kStages + k % kStages) * S::kStage;
       const uint32_t none = (uint32_t)(gone >> (kUnits * ahead)) & ((1u << kUnits) - 1);  // unit 0 in the highest bit
       const bool part = tb + kStep > all_hi + 1 || tb < all_lo || tb + kStep > t1 || none != 0;
-      if constexpr (kFold) fold(from, tb, none, part);
+      if constexpr (kFold) fold(from);
       // scores (folded ones in units of log2)
       f32x4w sc[R][kUnits];
 #pragma unroll
@@ -646,13 +641,11 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
           for (int g = 0; g < G; ++g)
             vp[b][g] = *reinterpret_cast<const uint2*>(from + S::v_params(u + b) + 32 * g + 8 * h);
         if (!kFold && part) {
-          asm volatile("");  // nothing of this ahead of the branch (1% of a decode batch)
+          asm volatile("");  // nothing of this ahead of the branch
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-              vp[b][g] = attend_seen(vp[b][g], tb + 16 * (u + b) + 4 * h, any_lo,
-                                     (none >> (kUnits - 1 - u - b) & 1) ? -1 : t1 - 1);
+            for (int g = 0; g < G; ++g) vp[b][g] = make_uint2(attend_finite(vp[b][g].x), attend_finite(vp[b][g].y));
         }
 #pragma unroll
         for (int t = 0; t < kSlices / 2; ++t) {  // tiles 4 t .. 4 t + 3, 64 channels

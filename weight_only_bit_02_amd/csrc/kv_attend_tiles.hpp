@@ -16,9 +16,9 @@
 // widened by each wave its share, one step ahead into one of three buffers, from registers loaded
 // a step before that.
 //
-// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 157-161 us by card, 853-877
+// Measured, D = 128, groups of 128: a prompt of 4096 tokens, 32 heads, 155-161 us by card, 853-888
 // TFLOP/s; pieces of 257-1024 rows behind 2000-12345 tokens, 64 heads on 8 of keys, groups of 64:
-// 904-928 us, 819-841 TFLOP/s (a large product of the library: 1211). Matrix cores are busy for 37% of
+// 893-925 us, 822-851 TFLOP/s (a large product of the library: 1211). Matrix cores are busy for 37% of
 // the cycles and vector instructions for 50%, softmax 131 and widening some 100 a wave and step beside
 // 2048 cycles of products: the SIMD issues them in turn, and its two waves overlap what they can.
 // Operands read eight products ahead, all waves in step, widening between the products, two running
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
     const int pa = p0 + wr0 / a.share, pb = p0 + wr1 / a.share, pe = p0 + r1 / a.share;
     const int all_hi = attend_last(a, pa, last), any_hi = attend_last(a, pb, last);
     const int all_lo = a.window > 0 ? pb - a.window + 1 : 0, any_lo = a.window > 0 ? pa - a.window + 1 : 0;
-    const int end = attend_last(a, pe, last) + 1, begin = a.window > 0 ? p0 + r0 / a.share - a.window + 1 : 0;
+    const int end = attend_last(a, pe, last) + 1;
     const int t0 = w.first + u0 * kAttendChunk;
     const int t1 = w.first + u1 * kAttendChunk < end ? w.first + u1 * kAttendChunk : end;
     const bool rows = wr0 <= r1;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
         d.vp[i] = *reinterpret_cast<const uint2*>(vq0 + par + (i << v.page_shift));
       }
     };
-    const auto widen = [&](const Codes& d, int tb, int buf) AWQ_INLINE {
+    const auto widen = [&](const Codes& d, int buf) AWQ_INLINE {
       if (in == 0) there[buf][sub] = d.page >= 0;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -230,13 +230,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
       }
       uint2 vp[Codes::kGroups];
 #pragma unroll
-      for (int i = 0; i < Codes::kGroups; ++i) vp[i] = d.vp[i];
-      if (tb + kTokens > t1 || tb < begin || __ballot(d.page < 0)) {
-        asm volatile("");  // nothing of this ahead of the branch
-#pragma unroll
-        for (int i = 0; i < Codes::kGroups; ++i)
-          vp[i] = attend_seen(vp[i], tb + 16 * sub + 4 * v_h, begin, d.page < 0 ? -1 : end - 1);
-      }
+      for (int i = 0; i < Codes::kGroups; ++i) vp[i] = make_uint2(attend_finite(d.vp[i].x), attend_finite(d.vp[i].y));
 #pragma unroll
       for (int i = 0; i < kWords / 2; ++i) {  // channels v_c + 16 (4 (v_w + i) + j)
 #pragma unroll
@@ -358,7 +352,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads) k_attend_tiles(KvView 
 
     const bool behind = wave >= T::kWaves / 2;
     const auto advance = [&](Codes& d, int& entry, int tb, int buf) AWQ_INLINE {  // widens step tb, loads the next
-      widen(d, tb, buf);
+      widen(d, buf);
       load(d, entry, tb + kTokens);
       entry = entry_of(tb + 2 * kTokens);
     };
