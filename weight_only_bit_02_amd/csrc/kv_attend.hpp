@@ -21,7 +21,7 @@
 //
 // Measured. 24 sequences of 300-4000 tokens, 32 heads, D = 128, groups of 128 (241 MB): 62 us and 5 for
 // the join, 3.9 TB/s; one sequence of 131071 tokens, 8 heads of keys (138 MB): 37 and 7, 3.7 TB/s; 64
-// sequences, 8 heads of keys, groups of 32 (345 MB): 95 and 6, 3.6 TB/s. Bound by loads (alone 52 us
+// sequences, 8 heads of keys, groups of 32 (345 MB): 94 and 6, 3.7 TB/s. Bound by loads (alone 52 us
 // in the first case, 4.6 TB/s) and vector instructions (alone 56) that overlap in part only; matrix
 // cores are busy for 13% of the time. Short calls are chains of loads: the work list's, the
 // page's, the codes', 8 us for one sequence of 77 tokens.
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kAttendWaves* kWave)
   __shared__ __attribute__((aligned(16))) char smem[kRing > (int)sizeof(Sums) ? kRing : (int)sizeof(Sums)];
   Sums& sums = *reinterpret_cast<Sums*>(smem);  // after an item's last step
   // Up to two groups a head, the scale is applied outside the products: operands are code - zero, and a
-  // token's scale multiplies its scores and probabilities in fp32: some 225 vector instructions a step
+  // token's scale multiplies its scores and probabilities in fp32: some 220 vector instructions a step
   // instead of 320 at one group. (The zero outside as well takes 208, but then sums of codes and of
   // zeros, up to 15 scales a token, leave a small difference: 131071 tokens with values around zero
   // came out 1e-3 off, relatively, not 2e-4.)
